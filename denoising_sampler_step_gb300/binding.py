@@ -8,6 +8,7 @@ other path.  Importing this module fails if the library is missing.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -92,6 +93,28 @@ lib.dg_soft_embed_shard_begin_e4m3.restype = ctypes.c_int
 lib.dg_soft_embed_shard_end_e4m3.argtypes = [_p, _i64, _p, _i64, _i64, _p, _p, _i64, _i64, _i64, _f32, _p, _i64, _p,
                                              _sz, _p]
 lib.dg_soft_embed_shard_end_e4m3.restype = ctypes.c_int
+
+_ROWS = [_p, _i32, _i64, _i64, _i64]  # logits, dtype, R, V, ldl
+lib.dg_row_topk_workspace_size.argtypes = [_i64, _i64, _i32, _i32]
+lib.dg_row_topk_workspace_size.restype = _sz
+lib.dg_row_topk.argtypes = _ROWS + [_i32, _f32, _p, _p, _i64, _p, _p, _sz, _p]
+lib.dg_row_topk.restype = ctypes.c_int
+lib.dg_token_logp.argtypes = _ROWS + [_p, _f32, _p, _p, _p, _p]
+lib.dg_token_logp.restype = ctypes.c_int
+lib.dg_token_logp_backward.argtypes = _ROWS + [_p, _f32, _p, _p, _p, _p, _i64, _p]
+lib.dg_token_logp_backward.restype = ctypes.c_int
+lib.dg_distill_loss.argtypes = _ROWS + [_p, _p, _i32, _i64, _p, _f32, _p, _p, _p, _p, _p, _i64, _p]
+lib.dg_distill_loss.restype = ctypes.c_int
+lib.dg_distill_loss_backward.argtypes = _ROWS + [_p, _p, _i32, _i64, _p, _f32, _p, _p, _p, _p, _i64, _p]
+lib.dg_distill_loss_backward.restype = ctypes.c_int
+lib.dg_policy_loss.argtypes = _ROWS + [_p, _p, _p, _p, _f32, _f32, _f32, _f32] + [_p] * 8 + [_i64, _p]
+lib.dg_policy_loss.restype = ctypes.c_int
+lib.dg_preference_loss.argtypes = _ROWS + [_p, _p, _p, _i32, _f32, _f32, _f32] + [_p] * 8 + [_i64, _p]
+lib.dg_preference_loss.restype = ctypes.c_int
+
+# element types of the loss calls' logits and gradients (dg_dtype)
+DG_F32, DG_BF16 = 0, 1
+_DTYPE = {torch.float32: DG_F32, torch.bfloat16: DG_BF16}
 
 STATUS = {0: "DG_OK", 1: "DG_ERR_INVALID_ARG", 2: "DG_ERR_UNSUPPORTED", 3: "DG_ERR_CUDA", 4: "DG_ERR_TIMEOUT"}
 
@@ -529,3 +552,255 @@ def dg_check_wait_timeout(limit_us: int, stream=None) -> None:
     """Queues the diagnostic wait that gives up after limit_us; the next
     dg_get_device_status() raises DgError with DG_ERR_TIMEOUT."""
     _check(lib.dg_check_wait_timeout(int(limit_us), _stream(stream)), "dg_check_wait_timeout")
+
+
+# --------------------------------------------------------------------------- training on the logits
+#
+# Common to the calls below: `logits` [R, V] in fp32 or bf16 with unit column stride, V taken from its
+# shape (slice the padding off: logits[:, :V]); per-row vectors are contiguous, on the logits' device;
+# `out` holds preallocated outputs by name, and an output it lacks is allocated.  `stream` is the
+# stream the kernels run on; its tensors are the caller's to keep alive and ordered, as everywhere.
+
+def _logits(t: torch.Tensor) -> tuple:
+    """(pointer, dtype code, R, V, row stride) of a matrix of logits."""
+    code = _DTYPE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"logits must be float32 or bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError("logits must be on the GPU")
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError("logits must be [R, V] with unit column stride")
+    R, V = t.shape
+    return t.data_ptr(), code, R, V, _row_stride(t)
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Elements between rows.  The stride of a single row says nothing and is rounded up to 16 bytes."""
+    if t.shape[0] > 1:
+        return t.stride(0)
+    per = 16 // t.element_size()
+    return (t.shape[1] + per - 1) // per * per
+
+
+def _vec(t, n: int, dtype, device, name: str):
+    """Pointer of a contiguous vector of n elements (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != (n,) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _grad_like(grad: torch.Tensor, logits: torch.Tensor) -> tuple:
+    """(pointer, row stride) of a gradient of these logits."""
+    if grad.dtype is not logits.dtype or grad.shape != logits.shape or grad.device != logits.device:
+        raise ValueError("grad must have the logits' type, shape and device")
+    if grad.stride(1) != 1 and grad.shape[1] > 1:
+        raise ValueError("grad must have unit column stride")
+    return grad.data_ptr(), _row_stride(grad)
+
+
+def _new_grad(logits: torch.Tensor, stream) -> torch.Tensor:
+    """An uninitialised gradient [R, V] whose rows start on 16-byte boundaries."""
+    R, V = logits.shape
+    per = 16 // logits.element_size()
+    with _on(stream):
+        return _new((R, (V + per - 1) // per * per), logits.dtype, logits.device)[:, :V]
+
+
+def _on(stream):
+    """Allocations inside belong to the stream that writes them."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _fill(out: dict | None, shapes: dict, device, stream) -> dict:
+    """`out` with the missing outputs of {name: (shape, dtype)} allocated."""
+    o = {} if out is None else out
+    missing = [k for k in shapes if k not in o]
+    if missing:
+        with _on(stream):
+            for k in missing:
+                o[k] = _new(shapes[k][0], shapes[k][1], device)
+    return o
+
+
+def _table(t: torch.Tensor, R: int, K: int, dtype, device, name: str) -> int:
+    """Row stride of an [R, K] table with unit column stride."""
+    if t.dtype is not dtype or t.shape != (R, K) or t.device != device or (K > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be {dtype} [{R}, {K}] with unit column stride on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.stride(0) if R > 1 else K
+
+
+def _entries(indices, teacher, R: int, device) -> tuple:
+    """(K, row stride) of a teacher's entries."""
+    if indices.dim() != 2:
+        raise ValueError("indices must be [R, K]")
+    K = indices.shape[1]
+    ld = _table(indices, R, K, torch.int32, device, "indices")
+    if _table(teacher, R, K, torch.float32, device, "teacher") != ld:
+        raise ValueError("indices and teacher must have the same row stride")
+    return K, ld
+
+
+def dg_row_topk_workspace_size(R: int, V: int, K: int, dtype: int = DG_F32) -> int:
+    return int(lib.dg_row_topk_workspace_size(R, V, K, dtype))
+
+
+def topk_workspace(R: int, V: int, K: int, device, dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """A workspace tensor large enough for dg_row_topk."""
+    n = max(16, dg_row_topk_workspace_size(R, V, K, _DTYPE[dtype]))
+    return torch.empty((n + 15) // 16 * 16, dtype=torch.uint8, device=device)
+
+
+def dg_row_topk(logits: torch.Tensor, K: int, temperature: float = 1.0, lse: bool = False,
+                ws: torch.Tensor | None = None, stream=None, out: dict | None = None) -> dict:
+    """The K largest logits per row, in order, ties to the lowest index -> dict values (fp32 [R, K]),
+    indices (int32 [R, K]) and, with lse=True or an `lse` in `out`, the log-sum-exp of logits / T."""
+    x, code, R, V, ld = _logits(logits)
+    dev = logits.device
+    shapes = {"values": ((R, K), torch.float32), "indices": ((R, K), torch.int32)}
+    if lse:
+        shapes["lse"] = (R, torch.float32)
+    o = _fill(out, shapes, dev, stream)
+    ldk = _table(o["values"], R, K, torch.float32, dev, "values")
+    if _table(o["indices"], R, K, torch.int32, dev, "indices") != ldk:
+        raise ValueError("values and indices must have the same row stride")
+    if ws is None:
+        with _on(stream):
+            ws = topk_workspace(R, V, K, dev, logits.dtype)
+    _check(lib.dg_row_topk(x, code, R, V, ld, K, temperature, o["values"].data_ptr(), o["indices"].data_ptr(), ldk,
+                           _vec(o.get("lse"), R, torch.float32, dev, "lse"), ws.data_ptr(), ws.numel(),
+                           _stream(stream)), "dg_row_topk")
+    return o
+
+
+def dg_token_logp(logits: torch.Tensor, token: torch.Tensor, temperature: float = 1.0,
+                  weight: torch.Tensor | None = None, stream=None, out: dict | None = None) -> dict:
+    """ln softmax(logits / T)[token] per row -> dict logp, lse (fp32 [R]).  Rows of weight 0 or with a
+    negative token are left out (0)."""
+    x, code, R, V, ld = _logits(logits)
+    dev, f32 = logits.device, torch.float32
+    o = _fill(out, {"logp": (R, f32), "lse": (R, f32)}, dev, stream)
+    _check(lib.dg_token_logp(x, code, R, V, ld, _vec(token, R, torch.int32, dev, "token"), temperature,
+                             _vec(weight, R, f32, dev, "weight"), _vec(o["logp"], R, f32, dev, "logp"),
+                             _vec(o["lse"], R, f32, dev, "lse"), _stream(stream)), "dg_token_logp")
+    return o
+
+
+def dg_token_logp_backward(logits: torch.Tensor, token: torch.Tensor, lse: torch.Tensor, dlogp: torch.Tensor,
+                           scale: torch.Tensor | None = None, temperature: float = 1.0, stream=None,
+                           out: torch.Tensor | None = None) -> torch.Tensor:
+    """The logits' gradient of sum_r scale_r dlogp_r logp_r from a forward call's lse (scale: the upstream
+    gradient per row).  `out` may be the logits themselves."""
+    x, code, R, V, ld = _logits(logits)
+    dev, f32 = logits.device, torch.float32
+    if out is None:
+        out = _new_grad(logits, stream)
+    g, ldg = _grad_like(out, logits)
+    _check(lib.dg_token_logp_backward(x, code, R, V, ld, _vec(token, R, torch.int32, dev, "token"), temperature,
+                                      _vec(lse, R, f32, dev, "lse"), _vec(dlogp, R, f32, dev, "dlogp"),
+                                      _vec(scale, R, f32, dev, "scale"), g, ldg, _stream(stream)),
+           "dg_token_logp_backward")
+    return out
+
+
+def dg_distill_loss(logits: torch.Tensor, indices: torch.Tensor, teacher: torch.Tensor,
+                    teacher_lse: torch.Tensor | None = None, temperature: float = 1.0,
+                    weight: torch.Tensor | None = None, grad: bool = False, stream=None,
+                    out: dict | None = None) -> dict:
+    """Distillation from a teacher's top logits (dg_row_topk's indices and values, with teacher_lse its lse
+    for the bucket of the other entries) -> dict loss, lse (fp32 [R]), tail_logp (with teacher_lse) and,
+    with grad=True or a `grad` in `out`, the logits' gradient of sum_r weight_r loss_r."""
+    x, code, R, V, ld = _logits(logits)
+    dev, f32 = logits.device, torch.float32
+    K, ldk = _entries(indices, teacher, R, dev)
+    shapes = {"loss": (R, f32), "lse": (R, f32)}
+    if teacher_lse is not None:
+        shapes["tail_logp"] = (R, f32)
+    o = _fill(out, shapes, dev, stream)
+    if grad and "grad" not in o:
+        o["grad"] = _new_grad(logits, stream)
+    g, ldg = _grad_like(o["grad"], logits) if "grad" in o else (None, 0)
+    _check(lib.dg_distill_loss(x, code, R, V, ld, indices.data_ptr(), teacher.data_ptr(), K, ldk,
+                               _vec(teacher_lse, R, f32, dev, "teacher_lse"), temperature,
+                               _vec(weight, R, f32, dev, "weight"), _vec(o["loss"], R, f32, dev, "loss"),
+                               _vec(o["lse"], R, f32, dev, "lse"), _vec(o.get("tail_logp"), R, f32, dev, "tail_logp"),
+                               g, ldg, _stream(stream)), "dg_distill_loss")
+    return o
+
+
+def dg_distill_loss_backward(logits: torch.Tensor, indices: torch.Tensor, teacher: torch.Tensor,
+                             lse: torch.Tensor, dloss: torch.Tensor | None = None,
+                             teacher_lse: torch.Tensor | None = None, tail_logp: torch.Tensor | None = None,
+                             temperature: float = 1.0, stream=None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The logits' gradient of sum_r dloss_r loss_r from a forward call's lse (and tail_logp).  `out` may be
+    the logits themselves."""
+    x, code, R, V, ld = _logits(logits)
+    dev, f32 = logits.device, torch.float32
+    K, ldk = _entries(indices, teacher, R, dev)
+    if out is None:
+        out = _new_grad(logits, stream)
+    g, ldg = _grad_like(out, logits)
+    _check(lib.dg_distill_loss_backward(x, code, R, V, ld, indices.data_ptr(), teacher.data_ptr(), K, ldk,
+                                        _vec(teacher_lse, R, f32, dev, "teacher_lse"), temperature,
+                                        _vec(lse, R, f32, dev, "lse"), _vec(tail_logp, R, f32, dev, "tail_logp"),
+                                        _vec(dloss, R, f32, dev, "dloss"), g, ldg, _stream(stream)),
+           "dg_distill_loss_backward")
+    return out
+
+
+def dg_policy_loss(logits: torch.Tensor, token: torch.Tensor, old_logp: torch.Tensor, advantage: torch.Tensor,
+                   ref_logp: torch.Tensor | None = None, clip_low: float = 0.2, clip_high: float = 0.2,
+                   kl_coef: float = 0.0, temperature: float = 1.0, weight: torch.Tensor | None = None,
+                   grad: bool = False, stream=None, out: dict | None = None) -> dict:
+    """Clipped policy loss with a KL term against a reference -> dict loss, logp, lse, kl, dlogp (fp32 [R]),
+    clipped (uint8 [R]) and, with grad=True or a `grad` in `out`, the logits' gradient of
+    sum_r weight_r loss_r."""
+    x, code, R, V, ld = _logits(logits)
+    dev, f32 = logits.device, torch.float32
+    o = _fill(out, {"loss": (R, f32), "logp": (R, f32), "lse": (R, f32), "kl": (R, f32), "dlogp": (R, f32),
+                    "clipped": (R, torch.uint8)}, dev, stream)
+    if grad and "grad" not in o:
+        o["grad"] = _new_grad(logits, stream)
+    g, ldg = _grad_like(o["grad"], logits) if "grad" in o else (None, 0)
+    _check(lib.dg_policy_loss(x, code, R, V, ld, _vec(token, R, torch.int32, dev, "token"),
+                              _vec(old_logp, R, f32, dev, "old_logp"), _vec(ref_logp, R, f32, dev, "ref_logp"),
+                              _vec(advantage, R, f32, dev, "advantage"), temperature, clip_low, clip_high, kl_coef,
+                              _vec(weight, R, f32, dev, "weight"), _vec(o["loss"], R, f32, dev, "loss"),
+                              _vec(o["logp"], R, f32, dev, "logp"), _vec(o["lse"], R, f32, dev, "lse"),
+                              _vec(o["kl"], R, f32, dev, "kl"), _vec(o["clipped"], R, torch.uint8, dev, "clipped"),
+                              _vec(o["dlogp"], R, f32, dev, "dlogp"), g, ldg, _stream(stream)), "dg_policy_loss")
+    return o
+
+
+def dg_preference_loss(logits: torch.Tensor, token: torch.Tensor, ref_logp: torch.Tensor | None,
+                       seq_start: torch.Tensor, beta: float = 0.1, label_smoothing: float = 0.0,
+                       temperature: float = 1.0, weight: torch.Tensor | None = None,
+                       pair_weight: torch.Tensor | None = None, grad: bool = False, stream=None,
+                       out: dict | None = None) -> dict:
+    """Preference loss on the log ratios of P pairs of packed sequences (rows [seq_start[j], seq_start[j+1]);
+    pair i prefers sequence 2i over 2i + 1) -> dict loss [P], log_ratio [2P], logp, lse, dlogp [R] and, with
+    grad=True or a `grad` in `out`, the logits' gradient of sum_i pair_weight_i loss_i."""
+    x, code, R, V, ld = _logits(logits)
+    dev, f32 = logits.device, torch.float32
+    n = seq_start.numel()
+    if n % 2 != 1:
+        raise ValueError("seq_start must hold 2P + 1 offsets")
+    P = n // 2
+    o = _fill(out, {"loss": (P, f32), "log_ratio": (2 * P, f32), "logp": (R, f32), "lse": (R, f32),
+                    "dlogp": (R, f32)}, dev, stream)
+    if grad and "grad" not in o:
+        o["grad"] = _new_grad(logits, stream)
+    g, ldg = _grad_like(o["grad"], logits) if "grad" in o else (None, 0)
+    _check(lib.dg_preference_loss(x, code, R, V, ld, _vec(token, R, torch.int32, dev, "token"),
+                                  _vec(ref_logp, R, f32, dev, "ref_logp"),
+                                  _vec(seq_start, n, torch.int32, dev, "seq_start"), P, beta, label_smoothing,
+                                  temperature, _vec(weight, R, f32, dev, "weight"),
+                                  _vec(pair_weight, P, f32, dev, "pair_weight"), _vec(o["loss"], P, f32, dev, "loss"),
+                                  _vec(o["log_ratio"], 2 * P, f32, dev, "log_ratio"),
+                                  _vec(o["logp"], R, f32, dev, "logp"), _vec(o["lse"], R, f32, dev, "lse"),
+                                  _vec(o["dlogp"], R, f32, dev, "dlogp"), g, ldg, _stream(stream)),
+           "dg_preference_loss")
+    return o

@@ -605,6 +605,8 @@ dg_status dg_get_device_status(dg_stream_t stream) {
         const unsigned int zero = 0;
         e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero));
         if (e != cudaSuccess) return cuda_fail(e, "device status: clear");
+        if (!(word & 1u))
+            return fail(DG_ERR_INVALID_ARG, "a token or index of a loss call lies past the vocabulary");
         return fail(DG_ERR_TIMEOUT, "a kernel gave up waiting on a device barrier");
     }
     return DG_OK;

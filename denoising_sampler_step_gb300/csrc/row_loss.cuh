@@ -1,0 +1,85 @@
+// Losses on rows of full-vocabulary logits: what the host code and the kernel share.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/dgsamp.h"
+
+namespace dg {
+
+// What a row's loss is taken from.
+enum RowLossHead {
+    kHeadToken = 0,   // the log-probability of one token per row
+    kHeadDistill = 1  // a teacher's top logits
+};
+// Which passes a call makes over a row.
+enum RowLossPass {
+    kPassForward = 1,   // statistics and losses
+    kPassBackward = 2,  // the gradient from the statistics a forward call saved
+    kPassStep = 3       // both in one call
+};
+
+struct RowLossArgs {
+    const void *logits;  // [R, ldl] fp32 or bf16
+    int64_t ldl;
+    int dtype;  // dg_dtype, of logits and grad
+    int64_t R, V;
+    float T;              // temperature
+    const float *weight;  // [R] or NULL (1): a row of weight 0 is not read, its outputs are 0
+    void *grad;           // [R, ldg] or NULL
+    int64_t ldg;
+    float *lse;           // [R]: written forward, read backward
+    float *loss;          // [R] or NULL
+    // kHeadToken
+    const int32_t *token;    // [R]; a negative token leaves the row out like weight 0
+    bool policy;             // the clipped policy loss; else the log-probability alone
+    const float *old_logp, *ref_logp, *advantage;
+    float clip_low, clip_high, kl_coef;
+    float *logp, *kl;
+    uint8_t *clipped;
+    float *dlogp;  // [R] dloss/dlogp: written forward, read backward (then the coefficient is dlogp * weight)
+    // kHeadDistill
+    const int32_t *indices;  // [R, ldk]; a negative index leaves the entry out
+    const float *teacher;    // [R, ldk]
+    int64_t ldk;
+    int K;
+    const float *teacher_lse;  // [R] or NULL (renormalise over the K entries)
+    float *tail_logp;          // [R] ln p_0 with teacher_lse: written forward, read backward
+};
+
+cudaError_t launch_row_loss(const RowLossArgs &a, RowLossHead head, RowLossPass pass, cudaStream_t stream);
+
+// Preference loss of P pairs from the rows' log-probabilities: losses, log ratios, dlogp.
+struct PairLossArgs {
+    const float *logp, *ref_logp;  // ref_logp may be NULL (0)
+    const float *weight;           // [R] or NULL
+    const int32_t *token;
+    const int32_t *seq_start;      // [2P + 1]
+    int64_t R;
+    int32_t P;
+    float beta, label_smoothing;
+    const float *pair_weight;  // [P] or NULL
+    float *loss, *log_ratio, *dlogp;
+};
+cudaError_t launch_pair_loss(const PairLossArgs &a, cudaStream_t stream);
+
+// The K largest logits of each row (row_topk.cu).
+struct RowTopKArgs {
+    const void *logits;
+    int64_t ldl;
+    int dtype;
+    int64_t R, V;
+    int K;
+    float T;
+    float *values;
+    int32_t *indices;
+    int64_t ldk;
+    float *lse;  // [R] or NULL
+};
+size_t row_topk_workspace_bytes(int64_t R, int64_t V, int K, int dtype);
+cudaError_t launch_row_topk(const RowTopKArgs &a, void *workspace, cudaStream_t stream);
+
+constexpr int kMaxTopK = 1024;
+
+}  // namespace dg

@@ -233,7 +233,8 @@ dg_status dg_sampler_step(const float *logits, int32_t n_req, int32_t L_c, int64
 
 /*
  * Synchronises `stream`, then reports (and clears) the device-side error word:
- * DG_ERR_TIMEOUT if a kernel gave up waiting since the last call, DG_ERR_CUDA if
+ * DG_ERR_TIMEOUT if a kernel gave up waiting since the last call, DG_ERR_INVALID_ARG if
+ * one met a token or index past the vocabulary (the loss calls), DG_ERR_CUDA if
  * the stream reports a CUDA error, else DG_OK.  This call blocks the host.
  */
 dg_status dg_get_device_status(dg_stream_t stream);
@@ -531,6 +532,145 @@ dg_status dg_sampler_loop_step_e4m3(const float *logits, int32_t n_req, int32_t 
                                     int32_t *prev_argmax, int32_t *stable, int32_t *steps,
                                     uint8_t *converged, uint32_t flags, void *workspace,
                                     size_t workspace_bytes, dg_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------------------
+ * Training on the sampler's logits: a teacher's top logits, and losses with the gradient of
+ * the logits.  The pages describe sampling only; these calls are what a user needs to train
+ * the model whose logits the calls above sample from.
+ *
+ * Conventions of this part:
+ *   logits, grad   [R, ldl] and [R, ldg] of one element type (dtype), V columns used.  Both bases
+ *                  16-byte aligned and both row strides a multiple of 16 bytes (else
+ *                  DG_ERR_UNSUPPORTED); any V >= 1.  Columns at V and past it are neither read
+ *                  nor written.  grad may be the logits themselves (same base, ldg == ldl: the
+ *                  gradient replaces them); any other overlap is DG_ERR_INVALID_ARG.
+ *   temperature T  positive and finite; z = x / T, lse = ln sum_v exp(z_v), p_v = exp(z_v - lse).
+ *   weight         [R] fp32 or NULL (every row 1).  The gradient is that of sum_r weight_r loss_r:
+ *                  a mean, a mask and the upstream gradient go in here.  Losses come unweighted.
+ *                  A row of weight 0 is left out: its logits are not read (they may hold
+ *                  anything, NaN included), its outputs are 0 and its gradient row is 0.
+ *   token          [R] int32 in [0, V); a negative token leaves the row out like weight 0.
+ *   A token or index at or past V leaves its row or entry out as well, and dg_get_device_status
+ *   reports it (DG_ERR_INVALID_ARG).
+ *   Statistics, losses and sums are fp32 or wider whatever dtype is; a bf16 gradient is rounded
+ *   once.  Results are bitwise reproducible.  -inf and the type's lowest finite value are allowed
+ *   in the logits (masked vocabulary); a row whose logits are all -inf has no distribution and
+ *   gives NaN.  NaN and +inf logits are undefined in rows that are read.
+ */
+
+/* Element type of logits and gradients. */
+typedef enum dg_dtype {
+    DG_F32 = 0,
+    DG_BF16 = 1
+} dg_dtype;
+
+/*
+ * The K largest logits of every row, from the largest down, equal ones by index (-0 and +0 are
+ * equal).  -inf entries count as the smallest.
+ *
+ *   values   [R, ldk] fp32: the logits as they are (no temperature)
+ *   indices  [R, ldk] int32
+ *   lse      [R] fp32 or NULL: ln sum_v exp(x_v / T) of the whole row in the same read, what the
+ *            distillation call takes as teacher_lse (NaN for an all -inf row)
+ *   workspace  device scratch of at least dg_row_topk_workspace_size bytes, 16-byte aligned; its
+ *            contents on entry do not matter
+ * Requires 1 <= K <= min(V, 1024) (above 1024: DG_ERR_UNSUPPORTED), ldk >= K, V < 2^31 - 16.
+ */
+dg_status dg_row_topk(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl, int32_t K,
+                      float temperature, float *values, int32_t *indices, int64_t ldk, float *lse,
+                      void *workspace, size_t workspace_bytes, dg_stream_t stream);
+
+/* Bytes of workspace dg_row_topk needs on the current device (0 for an invalid shape). */
+size_t dg_row_topk_workspace_size(int64_t R, int64_t V, int32_t K, int32_t dtype);
+
+/*
+ * Log-probability of one token per row: logp_r = z_token - lse (logp or lse may be NULL).  A
+ * policy's or a reference's log-probabilities for the losses below; dg_row_sample's log_p is the
+ * same quantity for its candidate at temperature 1.
+ */
+dg_status dg_token_logp(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
+                        const int32_t *token, float temperature, const float *weight, float *logp, float *lse,
+                        dg_stream_t stream);
+
+/*
+ * The gradient of sum_r weight_r dlogp_r logp_r for given dlogp and the lse a forward call saved:
+ *   grad[r, v] = weight_r dlogp_r / T ([v == token_r] - p_v).
+ * With dlogp from dg_policy_loss or dg_preference_loss this is their backward pass (weight: the
+ * upstream gradient per row).  A row whose coefficient is 0 is not read.
+ */
+dg_status dg_token_logp_backward(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
+                                 const int32_t *token, float temperature, const float *lse, const float *dlogp,
+                                 const float *weight, void *grad, int64_t ldg, dg_stream_t stream);
+
+/*
+ * Distillation from a teacher's top logits: per row K indices and the teacher's logits there
+ * (dg_row_topk's outputs, or any K distinct entries; a negative index leaves its entry out).
+ *   q_k = softmax(teacher_k / T) over the row's entries              (teacher_lse NULL)
+ *   q_k = exp(teacher_k / T - teacher_lse), q_0 = max(0, 1 - sum q)  (teacher_lse given)
+ *   loss = T^2 [ sum_k q_k (ln q_k - ln p_k)  +  q_0 (ln q_0 - ln p_0) ]
+ * With teacher_lse the entries outside the teacher's form one bucket, p_0 = the student's
+ * probability of all of them (the second term; left out where ln p_0 is below -87: no fp32
+ * probability, as when all of them are masked).  Terms with q = 0 are 0.
+ *   grad[r, v] = weight_r T (M p_v - q_v)        on the teacher's entries, M = sum_k q_k + q_0
+ *   grad[r, v] = weight_r T p_v (M - q_0 / p_0)  elsewhere
+ *
+ *   indices [R, ldk] int32, teacher [R, ldk] fp32, teacher_lse [R] fp32 or NULL (dg_row_topk's
+ *   lse at the same T); a row's valid indices must differ from one another
+ *   loss, lse [R] fp32 (each may be NULL); tail_logp [R] fp32: ln p_0 (may be NULL; written only with
+ *   teacher_lse); grad: NULL for the losses alone
+ * Requires 1 <= K <= 1024 (above: DG_ERR_UNSUPPORTED), ldk >= K.  A row without a valid entry has
+ * loss 0 and gradient 0.
+ *
+ * dg_distill_loss_backward: the gradient alone, from the lse (and, with teacher_lse, the
+ * tail_logp) a forward call saved; dloss [R] or NULL takes weight's place.
+ */
+dg_status dg_distill_loss(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
+                          const int32_t *indices, const float *teacher, int32_t K, int64_t ldk,
+                          const float *teacher_lse, float temperature, const float *weight, float *loss, float *lse,
+                          float *tail_logp, void *grad, int64_t ldg, dg_stream_t stream);
+dg_status dg_distill_loss_backward(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
+                                   const int32_t *indices, const float *teacher, int32_t K, int64_t ldk,
+                                   const float *teacher_lse, float temperature, const float *lse,
+                                   const float *tail_logp, const float *dloss, void *grad, int64_t ldg,
+                                   dg_stream_t stream);
+
+/*
+ * Clipped policy loss per row with a KL term against a reference policy:
+ *   ratio = exp(logp - old_logp),  d = ref_logp - logp
+ *   loss  = -min(ratio A, clip(ratio, 1 - clip_low, 1 + clip_high) A) + kl_coef (e^d - 1 - d)
+ *   dlogp = [ratio A <= clipped ratio A] (-ratio A) - kl_coef (e^d - 1)
+ *
+ *   token (the sampled actions), old_logp, advantage A [R]; ref_logp [R] or NULL (no KL term)
+ *   loss, logp, lse, kl (e^d - 1 - d), dlogp [R] fp32, clipped [R] uint8 (1 where the clipped branch
+ *   was taken): each may be NULL; grad: NULL for the losses alone
+ * Requires 0 <= clip_low <= 1, clip_high >= 0, kl_coef >= 0, all finite.
+ */
+dg_status dg_policy_loss(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
+                         const int32_t *token, const float *old_logp, const float *ref_logp, const float *advantage,
+                         float temperature, float clip_low, float clip_high, float kl_coef, const float *weight,
+                         float *loss, float *logp, float *lse, float *kl, uint8_t *clipped, float *dlogp,
+                         void *grad, int64_t ldg, dg_stream_t stream);
+
+/*
+ * Preference loss on P pairs of packed sequences.  Sequence j is the rows
+ * [seq_start[j], seq_start[j+1]); pair i prefers sequence 2i over sequence 2i + 1.
+ *   s_j  = sum over the sequence's rows of weight_r (logp_r - ref_logp_r)   (ref_logp NULL: 0)
+ *   z    = beta (s_2i - s_2i+1)
+ *   loss = -(1 - label_smoothing) ln sigmoid(z) - label_smoothing ln sigmoid(-z)
+ * The gradient is that of sum_i pair_weight_i loss_i (pair_weight NULL: 1); weight masks tokens and
+ * may normalise by length.  Rows in no sequence get gradient 0, an empty sequence has s = 0.
+ *
+ *   seq_start [2P + 1] int32, not decreasing, within [0, R]
+ *   loss [P], logp, lse, dlogp [R] fp32: required; log_ratio [2P] fp32 (s_j) or NULL; grad: NULL for
+ *   the losses alone (dlogp then serves dg_token_logp_backward)
+ * Requires P >= 0, beta finite, 0 <= label_smoothing < 1.
+ */
+dg_status dg_preference_loss(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
+                             const int32_t *token, const float *ref_logp, const int32_t *seq_start, int32_t P,
+                             float beta, float label_smoothing, float temperature, const float *weight,
+                             const float *pair_weight, float *loss, float *log_ratio, float *logp, float *lse,
+                             float *dlogp, void *grad, int64_t ldg, dg_stream_t stream);
 
 #ifdef __cplusplus
 }
