@@ -71,17 +71,6 @@ __device__ __forceinline__ void fold(MaxSum &st, const float (&x)[N], float c) {
     st.s += sum;
 }
 
-__device__ __forceinline__ MaxSum warp_merge(MaxSum st, float c) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        MaxSum o;
-        o.m = __shfl_xor_sync(0xffffffffu, st.m, off);
-        o.s = __shfl_xor_sync(0xffffffffu, st.s, off);
-        merge(st, o, c);
-    }
-    return st;
-}
-
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -92,6 +81,51 @@ __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
     return v;
+}
+
+// The 32 lanes' states as one, the same in every lane: the maximum first, so that each sum is
+// rescaled once.
+__device__ __forceinline__ MaxSum warp_merge(MaxSum st, float c) {
+    const float m = warp_max(st.m);
+    return MaxSum{m, warp_sum(st.s * exp_below(st.m, finite_max(m), c))};
+}
+
+// ------------------------------------------------------------------ rings and clusters
+
+// Global -> shared bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned),
+// completing on the barrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar,
+                                          uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], "
+        "%4;" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+// mbar_wait that returns at once where another wait of the CTA has already given up.
+__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    return mbar_wait(bar, parity, abort_flag);
+}
+__device__ __forceinline__ bool ring_wait_cluster(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (*abort_flag) return false;
+    return mbar_wait_cluster(bar, parity, abort_flag);
+}
+
+// Stores to, and an arrival on, shared memory of a CTA of the cluster (shared::cluster addresses);
+// the arrival releases the thread's earlier stores to a wait with cluster-scope acquire.
+__device__ __forceinline__ void st_cluster_v4(uint32_t dst, float a, float b, float c, float d) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "f"(a), "f"(b), "f"(c), "f"(d)
+                 : "memory");
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t dst, float a) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(a) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 }  // namespace vocab
