@@ -49,6 +49,16 @@ dg_status check_grad(const char *what, const void *logits, int32_t dtype, int64_
     return DG_OK;
 }
 
+dg_status check_workspace(const char *what, int64_t R, int64_t V, int32_t dtype, const void *workspace,
+                          size_t workspace_bytes) {
+    const size_t need = row_loss_workspace_bytes(R, V, dtype);
+    if (!workspace || workspace_bytes < need)
+        return fail(DG_ERR_INVALID_ARG, "%s: workspace of %zu bytes is below the %zu needed", what, workspace_bytes,
+                    need);
+    if (!aligned16(workspace)) return fail(DG_ERR_UNSUPPORTED, "%s: workspace must be 16-byte aligned", what);
+    return DG_OK;
+}
+
 dg_status check_teacher(const char *what, int64_t R, const int32_t *indices, const float *teacher, int32_t K,
                         int64_t ldk) {
     if (K < 1 || ldk < K) return fail(DG_ERR_INVALID_ARG, "%s: need K >= 1 and ldk >= K", what);
@@ -73,8 +83,9 @@ RowLossArgs row_args(const void *logits, int32_t dtype, int64_t R, int64_t V, in
     return a;
 }
 
-dg_status run(const char *what, const RowLossArgs &a, RowLossHead head, RowLossPass pass, dg_stream_t stream) {
-    const cudaError_t e = launch_row_loss(a, head, pass, (cudaStream_t)stream);
+dg_status run(const char *what, const RowLossArgs &a, RowLossHead head, RowLossPass pass, void *workspace,
+              dg_stream_t stream) {
+    const cudaError_t e = launch_row_loss(a, head, pass, workspace, (cudaStream_t)stream);
     return e == cudaSuccess ? DG_OK : cuda_fail(e, what);
 }
 
@@ -88,6 +99,11 @@ extern "C" {
 size_t dg_row_topk_workspace_size(int64_t R, int64_t V, int32_t K, int32_t dtype) {
     if (R < 1 || V < 1 || K < 1 || K > kMaxTopK || K > V || (dtype != DG_F32 && dtype != DG_BF16)) return 0;
     return row_topk_workspace_bytes(R, V, K, dtype);
+}
+
+size_t dg_row_loss_workspace_size(int64_t R, int64_t V, int32_t dtype) {
+    if (R < 1 || R > (1LL << 28) || V < 1 || V > 0x7ffffff0LL || (dtype != DG_F32 && dtype != DG_BF16)) return 0;
+    return row_loss_workspace_bytes(R, V, dtype);
 }
 
 dg_status dg_row_topk(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl, int32_t K,
@@ -114,7 +130,7 @@ dg_status dg_row_topk(const void *logits, int32_t dtype, int64_t R, int64_t V, i
 }
 
 dg_status dg_token_logp(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl, const int32_t *token,
-                        float temperature, const float *weight, float *logp, float *lse, dg_stream_t stream) {
+                        float temperature, const float *weight, float *logp, float *lse, void *workspace, size_t workspace_bytes, dg_stream_t stream) {
     t_last_error[0] = 0;
     const char *what = "token logp";
     dg_status st = check_rows(what, logits, dtype, R, V, ldl, temperature);
@@ -124,12 +140,14 @@ dg_status dg_token_logp(const void *logits, int32_t dtype, int64_t R, int64_t V,
     a.token = token;
     a.logp = logp;
     a.lse = lse;
-    return run(what, a, kHeadToken, kPassForward, stream);
+    st = check_workspace(what, R, V, dtype, workspace, workspace_bytes);
+    if (st != DG_OK) return st;
+    return run(what, a, kHeadToken, kPassForward, workspace, stream);
 }
 
 dg_status dg_token_logp_backward(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
                                  const int32_t *token, float temperature, const float *lse, const float *dlogp,
-                                 const float *weight, void *grad, int64_t ldg, dg_stream_t stream) {
+                                 const float *weight, void *grad, int64_t ldg, void *workspace, size_t workspace_bytes, dg_stream_t stream) {
     t_last_error[0] = 0;
     const char *what = "token logp backward";
     dg_status st = check_rows(what, logits, dtype, R, V, ldl, temperature);
@@ -141,13 +159,15 @@ dg_status dg_token_logp_backward(const void *logits, int32_t dtype, int64_t R, i
     a.token = token;
     a.lse = const_cast<float *>(lse);
     a.dlogp = const_cast<float *>(dlogp);
-    return run(what, a, kHeadToken, kPassBackward, stream);
+    st = check_workspace(what, R, V, dtype, workspace, workspace_bytes);
+    if (st != DG_OK) return st;
+    return run(what, a, kHeadToken, kPassBackward, workspace, stream);
 }
 
 dg_status dg_distill_loss(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
                           const int32_t *indices, const float *teacher, int32_t K, int64_t ldk,
                           const float *teacher_lse, float temperature, const float *weight, float *loss, float *lse,
-                          float *tail_logp, void *grad, int64_t ldg, dg_stream_t stream) {
+                          float *tail_logp, void *grad, int64_t ldg, void *workspace, size_t workspace_bytes, dg_stream_t stream) {
     t_last_error[0] = 0;
     const char *what = "distill loss";
     dg_status st = check_rows(what, logits, dtype, R, V, ldl, temperature);
@@ -164,14 +184,16 @@ dg_status dg_distill_loss(const void *logits, int32_t dtype, int64_t R, int64_t 
     a.loss = loss;
     a.lse = lse;
     a.tail_logp = teacher_lse ? tail_logp : nullptr;
-    return run(what, a, kHeadDistill, grad ? kPassStep : kPassForward, stream);
+    st = check_workspace(what, R, V, dtype, workspace, workspace_bytes);
+    if (st != DG_OK) return st;
+    return run(what, a, kHeadDistill, grad ? kPassStep : kPassForward, workspace, stream);
 }
 
 dg_status dg_distill_loss_backward(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
                                    const int32_t *indices, const float *teacher, int32_t K, int64_t ldk,
                                    const float *teacher_lse, float temperature, const float *lse,
                                    const float *tail_logp, const float *dloss, void *grad, int64_t ldg,
-                                   dg_stream_t stream) {
+                                   void *workspace, size_t workspace_bytes, dg_stream_t stream) {
     t_last_error[0] = 0;
     const char *what = "distill loss backward";
     dg_status st = check_rows(what, logits, dtype, R, V, ldl, temperature);
@@ -190,14 +212,16 @@ dg_status dg_distill_loss_backward(const void *logits, int32_t dtype, int64_t R,
     a.teacher_lse = teacher_lse;
     a.lse = const_cast<float *>(lse);
     a.tail_logp = const_cast<float *>(tail_logp);
-    return run(what, a, kHeadDistill, kPassBackward, stream);
+    st = check_workspace(what, R, V, dtype, workspace, workspace_bytes);
+    if (st != DG_OK) return st;
+    return run(what, a, kHeadDistill, kPassBackward, workspace, stream);
 }
 
 dg_status dg_policy_loss(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl, const int32_t *token,
                          const float *old_logp, const float *ref_logp, const float *advantage, float temperature,
                          float clip_low, float clip_high, float kl_coef, const float *weight, float *loss,
                          float *logp, float *lse, float *kl, uint8_t *clipped, float *dlogp, void *grad, int64_t ldg,
-                         dg_stream_t stream) {
+                         void *workspace, size_t workspace_bytes, dg_stream_t stream) {
     t_last_error[0] = 0;
     const char *what = "policy loss";
     dg_status st = check_rows(what, logits, dtype, R, V, ldl, temperature);
@@ -225,14 +249,16 @@ dg_status dg_policy_loss(const void *logits, int32_t dtype, int64_t R, int64_t V
     a.kl = kl;
     a.clipped = clipped;
     a.dlogp = dlogp;
-    return run(what, a, kHeadToken, grad ? kPassStep : kPassForward, stream);
+    st = check_workspace(what, R, V, dtype, workspace, workspace_bytes);
+    if (st != DG_OK) return st;
+    return run(what, a, kHeadToken, grad ? kPassStep : kPassForward, workspace, stream);
 }
 
 dg_status dg_preference_loss(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
                              const int32_t *token, const float *ref_logp, const int32_t *seq_start, int32_t P,
                              float beta, float label_smoothing, float temperature, const float *weight,
                              const float *pair_weight, float *loss, float *log_ratio, float *logp, float *lse,
-                             float *dlogp, void *grad, int64_t ldg, dg_stream_t stream) {
+                             float *dlogp, void *grad, int64_t ldg, void *workspace, size_t workspace_bytes, dg_stream_t stream) {
     t_last_error[0] = 0;
     const char *what = "preference loss";
     dg_status st = check_rows(what, logits, dtype, R, V, ldl, temperature);
@@ -250,10 +276,11 @@ dg_status dg_preference_loss(const void *logits, int32_t dtype, int64_t R, int64
     a.logp = logp;
     a.lse = lse;
     a.dlogp = dlogp;  // 0 in every row, then the pairs' rows
-    if (R > 0) st = run(what, a, kHeadToken, kPassForward, stream);
+    if (R > 0) st = check_workspace(what, R, V, dtype, workspace, workspace_bytes);
+    if (R > 0 && st == DG_OK) st = run(what, a, kHeadToken, kPassForward, workspace, stream);
     if (st != DG_OK) return st;
     if (P > 0) {
-        const PairLossArgs pa{logp, ref_logp, weight,          token,       seq_start, R,         P,
+        const PairLossArgs pa{logp, ref_logp, weight,          token,       seq_start, R, V, P,
                               beta, label_smoothing, pair_weight, loss, log_ratio, dlogp};
         const cudaError_t e = launch_pair_loss(pa, (cudaStream_t)stream);
         if (e != cudaSuccess) return cuda_fail(e, "preference loss: pairs");
@@ -262,7 +289,7 @@ dg_status dg_preference_loss(const void *logits, int32_t dtype, int64_t R, int64
     a.weight = nullptr;  // dlogp holds it
     a.grad = grad;
     a.ldg = ldg;
-    return run(what, a, kHeadToken, kPassBackward, stream);
+    return run(what, a, kHeadToken, kPassBackward, workspace, stream);
 }
 
 }  // extern "C"

@@ -48,7 +48,9 @@ struct RowLossArgs {
     float *tail_logp;          // [R] ln p_0 with teacher_lse: written forward, read backward
 };
 
-cudaError_t launch_row_loss(const RowLossArgs &a, RowLossHead head, RowLossPass pass, cudaStream_t stream);
+size_t row_loss_workspace_bytes(int64_t R, int64_t V, int dtype);
+cudaError_t launch_row_loss(const RowLossArgs &a, RowLossHead head, RowLossPass pass, void *workspace,
+                            cudaStream_t stream);
 
 // Preference loss of P pairs from the rows' log-probabilities: losses, log ratios, dlogp.
 struct PairLossArgs {
@@ -56,7 +58,7 @@ struct PairLossArgs {
     const float *weight;           // [R] or NULL
     const int32_t *token;
     const int32_t *seq_start;      // [2P + 1]
-    int64_t R;
+    int64_t R, V;
     int32_t P;
     float beta, label_smoothing;
     const float *pair_weight;  // [P] or NULL

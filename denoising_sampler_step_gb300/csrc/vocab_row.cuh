@@ -55,20 +55,63 @@ __device__ __forceinline__ void merge(MaxSum &a, const MaxSum &b, float c) {
     a.m = m;
 }
 
+// Two floats in one register pair, for the instructions that work on both (sm_100 family).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(f32x2 v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// exp_below of both: the same two roundings, with minus_m = (-m, -m) and cc = (c, c).
+__device__ __forceinline__ f32x2 exp_below2(f32x2 x, f32x2 minus_m, f32x2 cc) {
+    float lo, hi;
+    unpair(mul2(add2(x, minus_m), cc), lo, hi);
+    return pair(ex2_approx(lo), ex2_approx(hi));
+}
+
+// The largest of N values, and their sum, as trees: chains of N dependent operations would leave a
+// warp waiting for most of its time.
+template <int N>
+__device__ __forceinline__ float tree_max(const float *x) {
+    if constexpr (N == 1) return x[0];
+    if constexpr (N == 2) return fmaxf(x[0], x[1]);
+    if constexpr (N >= 3) {
+        constexpr int A = N / 3, B = (N - A) / 2;
+        return max3f(tree_max<A>(x), tree_max<B>(x + A), tree_max<N - A - B>(x + A + B));
+    }
+}
+template <int N>
+__device__ __forceinline__ float tree_sum(const float *x) {
+    if constexpr (N == 1) return x[0];
+    if constexpr (N >= 2) return tree_sum<N / 2>(x) + tree_sum<N - N / 2>(x + N / 2);
+}
+
+// Folds N values into the state.
 template <int N>
 __device__ __forceinline__ void fold(MaxSum &st, const float (&x)[N], float c) {
-    float bm = x[0];
-#pragma unroll
-    for (int j = 1; j < N; ++j) bm = fmaxf(bm, x[j]);
+    const float bm = tree_max<N>(x);
     if (bm > st.m) {
         st.s *= exp_below(st.m, bm, c);
         st.m = bm;
     }
     const float f = finite_max(st.m);
-    float sum = 0.0f;
+    float e[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) sum += exp_below(x[j], f, c);
-    st.s += sum;
+    for (int j = 0; j < N; ++j) e[j] = exp_below(x[j], f, c);
+    st.s += tree_sum<N>(e);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -90,7 +133,104 @@ __device__ __forceinline__ MaxSum warp_merge(MaxSum st, float c) {
     return MaxSum{m, warp_sum(st.s * exp_below(st.m, finite_max(m), c))};
 }
 
-// ------------------------------------------------------------------ rings and clusters
+// A 16-byte vector of the row: its entries as pairs of floats, their maximum over several vectors,
+// and the way back.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+    static constexpr int N = 4;
+    static constexpr uint32_t kLow = 0xff800000u;  // -inf
+    __device__ static __forceinline__ void pairs(const uint4 &v, f32x2 *p) {
+        p[0] = pair(__uint_as_float(v.x), __uint_as_float(v.y));
+        p[1] = pair(__uint_as_float(v.z), __uint_as_float(v.w));
+    }
+    __device__ static __forceinline__ uint4 pack(const f32x2 *p) {
+        float a, b, c, d;
+        unpair(p[0], a, b);
+        unpair(p[1], c, d);
+        return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+    }
+    template <int K>
+    __device__ static __forceinline__ float largest(const uint4 (&v)[K]) {
+        float f[4 * K];
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            f[4 * i] = __uint_as_float(v[i].x);
+            f[4 * i + 1] = __uint_as_float(v[i].y);
+            f[4 * i + 2] = __uint_as_float(v[i].z);
+            f[4 * i + 3] = __uint_as_float(v[i].w);
+        }
+        return tree_max<4 * K>(f);
+    }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static constexpr uint32_t kLow = 0xff80ff80u;
+    __device__ static __forceinline__ f32x2 widen(uint32_t w) {
+        return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    __device__ static __forceinline__ void pairs(const uint4 &v, f32x2 *p) {
+        p[0] = widen(v.x);
+        p[1] = widen(v.y);
+        p[2] = widen(v.z);
+        p[3] = widen(v.w);
+    }
+    __device__ static __forceinline__ uint32_t narrow(f32x2 v) {
+        float lo, hi;
+        unpair(v, lo, hi);
+        uint32_t r;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    }
+    __device__ static __forceinline__ uint4 pack(const f32x2 *p) {
+        return make_uint4(narrow(p[0]), narrow(p[1]), narrow(p[2]), narrow(p[3]));
+    }
+    __device__ static __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    // in bf16, two at a time: a maximum rounds nothing
+    template <int K>
+    __device__ static __forceinline__ float largest(const uint4 (&v)[K]) {
+        uint32_t m[K];
+#pragma unroll
+        for (int i = 0; i < K; ++i) m[i] = max2(max2(v[i].x, v[i].y), max2(v[i].z, v[i].w));
+#pragma unroll
+        for (int d = 1; d < K; d *= 2)
+#pragma unroll
+            for (int i = 0; i + d < K; i += 2 * d) m[i] = max2(m[i], m[i + d]);
+        return fmaxf(__uint_as_float(m[0] << 16), __uint_as_float(m[0] & 0xffff0000u));
+    }
+};
+
+// Folds K vectors into the state.
+template <typename T, int K>
+__device__ __forceinline__ void fold_vecs(MaxSum &st, const uint4 (&v)[K], float c) {
+    const float bm = Vec<T>::largest(v);
+    if (bm > st.m) {
+        st.s *= exp_below(st.m, bm, c);
+        st.m = bm;
+    }
+    const float f = -finite_max(st.m);
+    const f32x2 minus_m = pair(f, f), cc = pair(c, c);
+    constexpr int P = Vec<T>::N / 2;
+    f32x2 sum[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        f32x2 p[P];
+        Vec<T>::pairs(v[i], p);
+#pragma unroll
+        for (int j = 0; j < P; ++j) sum[j & 1] = add2(sum[j & 1], exp_below2(p[j], minus_m, cc));
+    }
+    float a, b;
+    unpair(add2(sum[0], sum[1]), a, b);
+    st.s += a + b;
+}
+
+// ------------------------------------------------------------------ rings
 
 // Global -> shared bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned),
 // completing on the barrier.
@@ -103,30 +243,37 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
         : "memory");
 }
 
-// mbar_wait that returns at once where another wait of the CTA has already given up.
+// mbar_wait in few instructions (kernels whose warps run different code wait in many places, and are
+// slowed by what does not fit the instruction cache): gives up after kWaitLimitNs, or at once where
+// another wait of the CTA has given up.
 __device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
     if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    return mbar_wait(bar, parity, abort_flag);
+    const unsigned long long t0 = globaltimer_ns();
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            *abort_flag = 1;
+            record_timeout();
+            return false;
+        }
+    }
+    return true;
 }
-__device__ __forceinline__ bool ring_wait_cluster(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if (*abort_flag) return false;
-    return mbar_wait_cluster(bar, parity, abort_flag);
+// Whether the phase is over, without a wait.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
-
-// Stores to, and an arrival on, shared memory of a CTA of the cluster (shared::cluster addresses);
-// the arrival releases the thread's earlier stores to a wait with cluster-scope acquire.
-__device__ __forceinline__ void st_cluster_v4(uint32_t dst, float a, float b, float c, float d) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "f"(a), "f"(b), "f"(c), "f"(d)
-                 : "memory");
-}
-__device__ __forceinline__ void st_cluster_f32(uint32_t dst, float a) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(a) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
+// e^x by the hardware's power of two: relative error (|x| + 4) 2^-23 or so.
+__device__ __forceinline__ float exp_fast(float x) { return ex2_approx(x * kLog2e); }
 
 }  // namespace vocab
 }  // namespace dg

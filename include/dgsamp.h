@@ -559,6 +559,13 @@ dg_status dg_sampler_loop_step_e4m3(const float *logits, int32_t n_req, int32_t 
  *   gives NaN.  NaN and +inf logits are undefined in rows that are read.
  */
 
+/*
+ * Bytes of device workspace each loss call below needs (0 for an invalid shape): 16-byte aligned,
+ * owned by the caller, its contents on entry do not matter; calls that may overlap on the GPU need
+ * one each.
+ */
+size_t dg_row_loss_workspace_size(int64_t R, int64_t V, int32_t dtype);
+
 /* Element type of logits and gradients. */
 typedef enum dg_dtype {
     DG_F32 = 0,
@@ -591,7 +598,7 @@ size_t dg_row_topk_workspace_size(int64_t R, int64_t V, int32_t K, int32_t dtype
  */
 dg_status dg_token_logp(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
                         const int32_t *token, float temperature, const float *weight, float *logp, float *lse,
-                        dg_stream_t stream);
+                        void *workspace, size_t workspace_bytes, dg_stream_t stream);
 
 /*
  * The gradient of sum_r weight_r dlogp_r logp_r for given dlogp and the lse a forward call saved:
@@ -601,7 +608,7 @@ dg_status dg_token_logp(const void *logits, int32_t dtype, int64_t R, int64_t V,
  */
 dg_status dg_token_logp_backward(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
                                  const int32_t *token, float temperature, const float *lse, const float *dlogp,
-                                 const float *weight, void *grad, int64_t ldg, dg_stream_t stream);
+                                 const float *weight, void *grad, int64_t ldg, void *workspace, size_t workspace_bytes, dg_stream_t stream);
 
 /*
  * Distillation from a teacher's top logits: per row K indices and the teacher's logits there
@@ -628,12 +635,12 @@ dg_status dg_token_logp_backward(const void *logits, int32_t dtype, int64_t R, i
 dg_status dg_distill_loss(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
                           const int32_t *indices, const float *teacher, int32_t K, int64_t ldk,
                           const float *teacher_lse, float temperature, const float *weight, float *loss, float *lse,
-                          float *tail_logp, void *grad, int64_t ldg, dg_stream_t stream);
+                          float *tail_logp, void *grad, int64_t ldg, void *workspace, size_t workspace_bytes, dg_stream_t stream);
 dg_status dg_distill_loss_backward(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
                                    const int32_t *indices, const float *teacher, int32_t K, int64_t ldk,
                                    const float *teacher_lse, float temperature, const float *lse,
                                    const float *tail_logp, const float *dloss, void *grad, int64_t ldg,
-                                   dg_stream_t stream);
+                                   void *workspace, size_t workspace_bytes, dg_stream_t stream);
 
 /*
  * Clipped policy loss per row with a KL term against a reference policy:
@@ -650,7 +657,7 @@ dg_status dg_policy_loss(const void *logits, int32_t dtype, int64_t R, int64_t V
                          const int32_t *token, const float *old_logp, const float *ref_logp, const float *advantage,
                          float temperature, float clip_low, float clip_high, float kl_coef, const float *weight,
                          float *loss, float *logp, float *lse, float *kl, uint8_t *clipped, float *dlogp,
-                         void *grad, int64_t ldg, dg_stream_t stream);
+                         void *grad, int64_t ldg, void *workspace, size_t workspace_bytes, dg_stream_t stream);
 
 /*
  * Preference loss on P pairs of packed sequences.  Sequence j is the rows
@@ -670,7 +677,7 @@ dg_status dg_preference_loss(const void *logits, int32_t dtype, int64_t R, int64
                              const int32_t *token, const float *ref_logp, const int32_t *seq_start, int32_t P,
                              float beta, float label_smoothing, float temperature, const float *weight,
                              const float *pair_weight, float *loss, float *log_ratio, float *logp, float *lse,
-                             float *dlogp, void *grad, int64_t ldg, dg_stream_t stream);
+                             float *dlogp, void *grad, int64_t ldg, void *workspace, size_t workspace_bytes, dg_stream_t stream);
 
 #ifdef __cplusplus
 }

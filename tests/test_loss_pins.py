@@ -115,16 +115,19 @@ P, Q, BIG = ctypes.c_void_p(256), ctypes.c_void_p(264), ctypes.c_void_p(1 << 40)
 ROWS = [P, 0, 4, 100, 100]
 
 
-def calls(lib, rows, T=1.0, grad=BIG, ldg=100, K=5, ldk=5):
+WS = [P, 1 << 30, None]    # workspace, its size, stream
+
+
+def calls(lib, rows, T=1.0, grad=BIG, ldg=100, K=5, ldk=5, ws=WS):
     """Every call of this part on the same rows, by name."""
     return {
         "topk": lib.dg_row_topk(*rows, K, T, P, P, ldk, P, P, 1 << 30, None),
-        "logp": lib.dg_token_logp(*rows, P, T, None, P, P, None),
-        "logp_bwd": lib.dg_token_logp_backward(*rows, P, T, P, P, None, grad, ldg, None),
-        "distill": lib.dg_distill_loss(*rows, P, P, K, ldk, None, T, None, P, P, P, grad, ldg, None),
-        "distill_bwd": lib.dg_distill_loss_backward(*rows, P, P, K, ldk, None, T, P, None, None, grad, ldg, None),
-        "policy": lib.dg_policy_loss(*rows, P, P, P, P, T, 0.2, 0.2, 0.0, None, *([P] * 6), grad, ldg, None),
-        "pref": lib.dg_preference_loss(*rows, P, P, P, 1, 0.1, 0.0, T, None, None, *([P] * 5), grad, ldg, None),
+        "logp": lib.dg_token_logp(*rows, P, T, None, P, P, *ws),
+        "logp_bwd": lib.dg_token_logp_backward(*rows, P, T, P, P, None, grad, ldg, *ws),
+        "distill": lib.dg_distill_loss(*rows, P, P, K, ldk, None, T, None, P, P, P, grad, ldg, *ws),
+        "distill_bwd": lib.dg_distill_loss_backward(*rows, P, P, K, ldk, None, T, P, None, None, grad, ldg, *ws),
+        "policy": lib.dg_policy_loss(*rows, P, P, P, P, T, 0.2, 0.2, 0.0, None, *([P] * 6), grad, ldg, *ws),
+        "pref": lib.dg_preference_loss(*rows, P, P, P, 1, 0.1, 0.0, T, None, None, *([P] * 5), grad, ldg, *ws),
     }
 
 
@@ -166,12 +169,12 @@ def test_calls_refuse_bad_gradients(lib, grad, ldg, status):
 
 def test_backward_calls_need_a_gradient_and_saved_values(lib):
     rows = ROWS
-    assert lib.dg_token_logp_backward(*rows, P, 1.0, P, P, None, None, 100, None) == 1
-    assert lib.dg_token_logp_backward(*rows, P, 1.0, None, P, None, BIG, 100, None) == 1
-    assert lib.dg_token_logp_backward(*rows, P, 1.0, P, None, None, BIG, 100, None) == 1
-    assert lib.dg_distill_loss_backward(*rows, P, P, 5, 5, None, 1.0, P, None, None, None, 100, None) == 1
-    assert lib.dg_distill_loss_backward(*rows, P, P, 5, 5, None, 1.0, None, None, None, BIG, 100, None) == 1
-    assert lib.dg_distill_loss_backward(*rows, P, P, 5, 5, P, 1.0, P, None, None, BIG, 100, None) == 1
+    assert lib.dg_token_logp_backward(*rows, P, 1.0, P, P, None, None, 100, *WS) == 1
+    assert lib.dg_token_logp_backward(*rows, P, 1.0, None, P, None, BIG, 100, *WS) == 1
+    assert lib.dg_token_logp_backward(*rows, P, 1.0, P, None, None, BIG, 100, *WS) == 1
+    assert lib.dg_distill_loss_backward(*rows, P, P, 5, 5, None, 1.0, P, None, None, None, 100, *WS) == 1
+    assert lib.dg_distill_loss_backward(*rows, P, P, 5, 5, None, 1.0, None, None, None, BIG, 100, *WS) == 1
+    assert lib.dg_distill_loss_backward(*rows, P, P, 5, 5, P, 1.0, P, None, None, BIG, 100, *WS) == 1
     assert b"tail_logp" in lib.dg_last_error()
 
 
@@ -191,9 +194,17 @@ def test_topk_refuses_more_entries_than_columns_and_a_small_workspace(lib):
     assert lib.dg_row_topk_workspace_size(0, 100, 5, 0) == 0
 
 
+def test_losses_refuse_a_small_or_unaligned_workspace(lib):
+    need = lib.dg_row_loss_workspace_size(4, 100, 0)
+    assert need > 0 and lib.dg_row_loss_workspace_size(4, 100, 2) == 0 and lib.dg_row_loss_workspace_size(0, 9, 0) == 0
+    for ws, n, status in ((None, 1 << 30, 1), (P, need - 1, 1), (Q, 1 << 30, 2)):
+        for name, st in calls(lib, ROWS, ws=[ws, n, None]).items():
+            assert name == "topk" or st == status, (name, st)
+
+
 def test_policy_refuses_bad_coefficients(lib):
     def call(lo=0.2, hi=0.2, kl=0.0, tok=P, old=P, adv=P):
-        return lib.dg_policy_loss(*ROWS, tok, old, None, adv, 1.0, lo, hi, kl, None, *([P] * 6), None, 0, None)
+        return lib.dg_policy_loss(*ROWS, tok, old, None, adv, 1.0, lo, hi, kl, None, *([P] * 6), None, 0, *WS)
     nan, inf = float("nan"), float("inf")
     for bad in (dict(lo=-0.1), dict(lo=1.1), dict(lo=nan), dict(hi=-0.1), dict(hi=inf), dict(hi=nan), dict(kl=-1.0),
                 dict(kl=inf), dict(kl=nan), dict(tok=None), dict(old=None), dict(adv=None)):
@@ -203,7 +214,7 @@ def test_policy_refuses_bad_coefficients(lib):
 def test_preference_refuses_bad_pairs(lib):
     def call(pairs=1, beta=0.1, eps=0.0, start=P, loss=P, dlogp=P):
         return lib.dg_preference_loss(*ROWS, P, P, start, pairs, beta, eps, 1.0, None, None, loss, P, P, P, dlogp,
-                                      None, 0, None)
+                                      None, 0, *WS)
     nan, inf = float("nan"), float("inf")
     for bad in (dict(pairs=-1), dict(beta=inf), dict(beta=nan), dict(eps=-0.1), dict(eps=1.0), dict(eps=nan),
                 dict(start=None), dict(loss=None), dict(dlogp=None)):
@@ -213,10 +224,10 @@ def test_preference_refuses_bad_pairs(lib):
 def test_no_rows_queue_nothing(lib):
     rows = [None, 0, 0, 100, 100]
     assert lib.dg_row_topk(*rows, 5, 1.0, None, None, 5, None, None, 0, None) == 0
-    assert lib.dg_token_logp(*rows, None, 1.0, None, None, None, None) == 0
-    assert lib.dg_token_logp_backward(*rows, None, 1.0, None, None, None, None, 100, None) == 0
-    assert lib.dg_distill_loss(*rows, None, None, 5, 5, None, 1.0, None, None, None, None, None, 100, None) == 0
-    assert lib.dg_distill_loss_backward(*rows, None, None, 5, 5, None, 1.0, None, None, None, None, 100, None) == 0
-    assert lib.dg_policy_loss(*rows, None, None, None, None, 1.0, 0.2, 0.2, 0.0, None, *([None] * 7), 100, None) == 0
+    assert lib.dg_token_logp(*rows, None, 1.0, None, None, None, None, 0, None) == 0
+    assert lib.dg_token_logp_backward(*rows, None, 1.0, None, None, None, None, 100, None, 0, None) == 0
+    assert lib.dg_distill_loss(*rows, None, None, 5, 5, None, 1.0, None, None, None, None, None, 100, None, 0, None) == 0
+    assert lib.dg_distill_loss_backward(*rows, None, None, 5, 5, None, 1.0, None, None, None, None, 100, None, 0, None) == 0
+    assert lib.dg_policy_loss(*rows, None, None, None, None, 1.0, 0.2, 0.2, 0.0, None, *([None] * 7), 100, None, 0, None) == 0
     assert lib.dg_preference_loss(*rows, None, None, None, 0, 0.1, 0.0, 1.0, None, None, *([None] * 6), 100,
-                                  None) == 0
+                                  None, 0, None) == 0
