@@ -4,14 +4,19 @@
 // HBM-bound: every logit is read once.  An entry is a 64-bit key (its value in an
 // order-preserving integer form above its complemented index), so that all keys differ and "the K
 // largest" means one set whatever the order in which they are met.  A CTA streams a contiguous
-// piece of the rows through a ring of shared-memory stages and keeps a buffer of candidates:
-//   - the entries above the threshold, the K-th largest key met so far, are pushed (entries equal
-//     to its value come later in the row, so they lose to those already held);
-//   - when the next step might not fit, a radix selection cuts the buffer to its K largest, whose
-//     smallest is the new threshold.  After the first few thousand entries of a row hardly any
-//     entry passes: a step costs a maximum and a comparison per entry.
-// The rows are cut into steps of 2,048 entries and the steps dealt out evenly, so that every CTA
-// reads as much as every other; a row that several CTAs share leaves each one's K candidates in the
+// piece of the rows through a ring of shared-memory stages and keeps a buffer of candidates: the
+// entries above a threshold that the K-th largest of the piece cannot be below.
+//   - The first step's threshold is a value that K of its 256 threads' maxima reach (of its 1,024 vectors'
+//     where K is large): at least K entries reach it, and not many more do.  Without it the first steps
+//     passed whole into the buffer, and every row began with two cuts of 4,096 entries.
+//   - When the buffer fills up it is cut to its K largest and a few more, whose smallest is the new
+//     threshold (entries equal to it come later in the row, so they lose to those already held).
+//   - A cut finds the K-th largest by histograms of 256 bins over the range of the keys, of the bin
+//     that holds it, and so on; it stops as soon as what lies in and above that bin is few enough.
+// So a step costs a maximum per vector, and a second look at the vectors of lanes whose maximum is
+// above the threshold.
+// The rows are cut into steps of 16 KB and the steps dealt out evenly, so that every CTA reads as
+// much as every other; a row that several CTAs share leaves each one's K candidates in the
 // workspace, and a second kernel takes the K largest of those.
 #include <atomic>
 
@@ -27,13 +32,16 @@ using namespace vocab;
 
 constexpr int kThreads = 256;                 // selecting threads
 constexpr int kWarps = kThreads / 32;
-constexpr int kStep = 2048;                   // entries between two looks at the buffer
-constexpr int kPerThread = kStep / kThreads;
-constexpr int kBuffer = 4096;                 // candidates
-constexpr int kStageBytes = 8192;
-constexpr int kStages = 5;
-constexpr int kPerSm = 3;
-constexpr int kMinSteps = 4;                  // a CTA's least share, where a row is split
+constexpr int kVecs = 4;                      // 16-byte vectors per thread and step
+constexpr int kStageBytes = kVecs * kThreads * 16;  // a step
+constexpr int kStages = 2;
+constexpr int kBuffer = 4096;               // candidates
+constexpr int kPerSm = 2;
+constexpr int kMinSteps = 1;                  // a CTA's least share, where a row is split
+constexpr int kRanked = 256;                  // most candidates ordered by counting
+
+// Candidates beyond K that a cut may leave (each less costs it another look at them).
+__host__ __device__ constexpr int cut_slack(int K) { return K / 8 + 16; }
 
 struct Shared {
     uint64_t buf[kBuffer];
@@ -41,8 +49,8 @@ struct Shared {
     uint64_t full[kStages], empty[kStages];
     MaxSum warp_state[kWarps];
     uint32_t warp_lo[kWarps], warp_hi[kWarps];
-    uint32_t count, digit, need, done;
-    int abort_flag;
+    uint32_t count, least, digit, before, inside;
+    int overflow, abort_flag;
 };
 
 // Larger floats have larger keys; -0 and +0 the same one; every number's key is above 0.
@@ -71,54 +79,63 @@ __device__ __forceinline__ bool sync_or(bool p) {
     return r != 0;
 }
 
-// Cuts the buffer's first n <= kBuffer entries (0 where there is none) to its K largest, in any
-// order at the front (0 after them where there are fewer); returns the smallest one's value, its
-// index left out.  All selecting threads; n >= K.
-__device__ __forceinline__ uint64_t select_top(Shared &sh, int n, int K) {
-    constexpr int R = kBuffer / kThreads;
+// The number of selecting threads with p.
+__device__ __forceinline__ int sync_count(bool p) {
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.popc.aligned.u32 %0, 1, %2, p;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)p), "n"(kThreads)
+        : "memory");
+    return r;
+}
+
+// A lower edge of the K largest of the buffer's first n entries: at least K of them reach it, and at
+// most K + slack.
+// All selecting threads; n >= K.
+__device__ __noinline__ uint64_t edge_of(Shared &sh, int n, int K, int slack) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint64_t r[R];
-    uint32_t lo = 0xffffffffu, hi = 0;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        r[i] = tid + i * kThreads < n ? sh.buf[tid + i * kThreads] : 0;
-        if (tid + i * kThreads < n) {
-            lo = min(lo, (uint32_t)(r[i] >> 32));
-            hi = max(hi, (uint32_t)(r[i] >> 32));
-        }
+    if (n <= K + slack) return 0;
+    // The bins start at a value that at least K entries reach: the threads' least one, or where there
+    // are K threads with entries, the least of their largest.
+    uint32_t least = 0xffffffffu, hi32 = 0;
+#pragma unroll 2
+    for (int i = tid; i < n; i += kThreads) {
+        const uint32_t v = (uint32_t)(sh.buf[i] >> 32);
+        least = min(least, v);
+        hi32 = max(hi32, v);
     }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
+    uint32_t lo32 = K <= kThreads && tid < n ? hi32 : least;
+    lo32 = __reduce_min_sync(0xffffffffu, lo32);
+    hi32 = __reduce_max_sync(0xffffffffu, hi32);
     if (lane == 0) {
-        sh.warp_lo[warp] = lo;
-        sh.warp_hi[warp] = hi;
+        sh.warp_lo[warp] = lo32;
+        sh.warp_hi[warp] = hi32;
     }
-    if (tid == 0) sh.count = 0;
+    for (int i = tid; i < 256; i += kThreads) sh.hist[i] = 0;
     sync();
-    lo = __reduce_min_sync(0xffffffffu, sh.warp_lo[lane & (kWarps - 1)]);
-    hi = __reduce_max_sync(0xffffffffu, sh.warp_hi[lane & (kWarps - 1)]);
-    // the digits start at the first bit in which the values differ: most keys share the top ones
-    int top = 64 - (lo == hi ? 32 : __clz(lo ^ hi));  // bits below this one are undecided
-    uint64_t prefix = top == 64 ? 0 : ((uint64_t)hi << 32) >> top;  // of the K-th largest, so far
+    lo32 = __reduce_min_sync(0xffffffffu, sh.warp_lo[lane & (kWarps - 1)]);
+    hi32 = __reduce_max_sync(0xffffffffu, sh.warp_hi[lane & (kWarps - 1)]);
+    uint64_t lo = (uint64_t)lo32 << 32;
+    int shift = max(0, 56 - __clzll((int64_t)(((uint64_t)(hi32 - lo32) << 32) | 0xffffffffu)));
+    int bits = 8;  // the bins: entries with (key - lo) >> shift below 2^bits
     uint32_t need = (uint32_t)K;
+#pragma unroll 1
     while (true) {
-        const int shift = max(0, top - 8);
-        const int bits = top - shift;
-        for (int i = tid; i < 256; i += kThreads) sh.hist[i] = 0;
-        sync();
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-            if (tid + i * kThreads < n && (top == 64 || (r[i] >> top) == prefix))
-                atomicAdd(&sh.hist[(uint32_t)(r[i] >> shift) & ((1u << bits) - 1)], 1u);
+#pragma unroll 2
+        for (int i = tid; i < n; i += kThreads) {
+            const uint64_t e = sh.buf[i], d = (e - lo) >> shift;
+            if (e >= lo && (d >> bits) == 0) atomicAdd(&sh.hist[(uint32_t)d], 1u);
+        }
         sync();
         if (warp == 0) {
-            // lane l holds the digits 255 - 8 l down to 248 - 8 l; counts from the largest digit on
-            uint32_t h[8], sum = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                h[i] = sh.hist[255 - 8 * lane - i];
-                sum += h[i];
-            }
+            // lane l holds the bins 255 - 8 l down to 248 - 8 l; counts from the largest one on
+            const uint4 *bins = reinterpret_cast<const uint4 *>(sh.hist) + 62 - 2 * lane;
+            const uint4 b1 = bins[0], b0 = bins[1];
+            const uint32_t h[8] = {b0.w, b0.z, b0.y, b0.x, b1.w, b1.z, b1.y, b1.x};
+            const uint32_t sum = b0.x + b0.y + b0.z + b0.w + b1.x + b1.y + b1.z + b1.w;
             uint32_t upto = sum;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -131,77 +148,120 @@ __device__ __forceinline__ uint64_t select_top(Shared &sh, int n, int K) {
                 for (int i = 0; i < 8; ++i) {
                     if (before < need && need <= before + h[i]) {
                         sh.digit = 255 - 8 * lane - i;
-                        sh.need = need - before;
-                        sh.done = h[i] == need - before;
+                        sh.before = before;
+                        sh.inside = h[i];
                     }
                     before += h[i];
                 }
             }
         }
         sync();
-        prefix = (prefix << bits) | sh.digit;
-        need = sh.need;
-        top = shift;
-        // every entry of the last digit is wanted, or the keys are decided to the last bit
-        if (sh.done || top == 0) break;
+        lo += (uint64_t)sh.digit << shift;
+        need -= sh.before;
+        if (shift == 0 || sh.inside - need <= (uint32_t)slack) return lo;
+        bits = min(8, shift);
+        shift -= bits;
+        for (int i = tid; i < 256; i += kThreads) sh.hist[i] = 0;
+        sync();
     }
-    const uint64_t least = top == 64 ? 0 : prefix << top;
-    uint64_t smallest = ~0ull;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const bool take = tid + i * kThreads < n && r[i] >= least && r[i] != 0;
-        if (take) smallest = min(smallest, r[i]);
-        const uint32_t votes = __ballot_sync(0xffffffffu, take);
-        if (votes) {
-            uint32_t base = 0;
-            if (lane == 0) base = atomicAdd(&sh.count, (uint32_t)__popc(votes));
-            base = __shfl_sync(0xffffffffu, base, 0);
-            if (take) sh.buf[base + __popc(votes & ((1u << lane) - 1))] = r[i];
-        }
-    }
-    const uint32_t h32 = __reduce_min_sync(0xffffffffu, (uint32_t)(smallest >> 32));
-    if (lane == 0) sh.warp_lo[warp] = h32;
-    sync();
-    for (int i = (int)sh.count + tid; i < K; i += kThreads) sh.buf[i] = 0;
-    sync();
-    return (uint64_t)__reduce_min_sync(0xffffffffu, sh.warp_lo[lane & (kWarps - 1)]) << 32;
 }
 
-// Orders the buffer's first K entries from the largest down.
-__device__ __forceinline__ void sort_top(Shared &sh, int K) {
-    const int tid = threadIdx.x;
-    int n2 = 1;
-    while (n2 < K) n2 *= 2;
-    for (int i = K + tid; i < n2; i += kThreads) sh.buf[i] = 0;
+// Keeps those of the buffer's first n entries that reach `least` and lie before the row's entry
+// `end`; sets the count and the smallest one's value.  All selecting threads.
+__device__ __noinline__ void keep(Shared &sh, int n, uint64_t least, uint32_t end) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    constexpr int kAtOnce = 2;
+    if (tid == 0) {
+        sh.count = 0;
+        sh.least = 0xffffffffu;
+    }
+    uint32_t smallest = 0xffffffffu;
+#pragma unroll 1
+    for (int b = 0; b < n; b += kAtOnce * kThreads) {
+        uint64_t r[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int at = b + tid + i * kThreads;
+            r[i] = at < n ? sh.buf[at] : 0;
+        }
+        sync();  // what follows writes over places read so far
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            if (r[i] != 0 && r[i] >= least && 0xffffffffu - (uint32_t)r[i] < end) {
+                sh.buf[atomicAdd(&sh.count, 1u)] = r[i];
+                smallest = min(smallest, (uint32_t)(r[i] >> 32));
+            }
+        }
+    }
+    smallest = __reduce_min_sync(0xffffffffu, smallest);
+    if (lane == 0) atomicMin(&sh.least, smallest);
     sync();
+}
+
+// The K largest of the buffer's first n entries, from the largest down, to the row's outputs.
+__device__ __noinline__ void write_top(Shared &sh, const RowTopKArgs &a, int64_t row, int n) {
+    const int tid = threadIdx.x, K = a.K;
+    int n2 = K <= kRanked / 2 - kRanked / 16 ? kRanked / 2 : kRanked;  // to be put in order
+    while (n2 < K) n2 *= 2;
+    if (n > n2) {
+        keep(sh, n, edge_of(sh, n, K, n2 - K), 0xffffffffu);
+        n = (int)sh.count;
+    }
+    auto write = [&](int k, uint64_t e) {
+        a.values[row * a.ldk + k] = key_value((uint32_t)(e >> 32));
+        a.indices[row * a.ldk + k] = (int32_t)(0xffffffffu - (uint32_t)e);
+    };
+    for (int i = n + tid; i < n2; i += kThreads) sh.buf[i] = 0;
+    sync();
+    if (n2 <= kRanked) {
+        // an entry's place is the number of larger ones, counted by neighbouring threads
+        constexpr int kParts = kThreads > kRanked ? kThreads / kRanked : 1;
+        const ulonglong2 *all = reinterpret_cast<const ulonglong2 *>(sh.buf);
+#pragma unroll 1
+        for (int k = tid / kParts; k < (n + 31) / 32 * 32; k += kThreads / kParts) {
+            const uint64_t e = sh.buf[k];
+            int place = 0;
+#pragma unroll 4
+            for (int i = tid % kParts; i < (n + 1) / 2; i += kParts) {
+                const ulonglong2 o = all[i];
+                place += (o.x > e) + (o.y > e);
+            }
+#pragma unroll
+            for (int off = 1; off < kParts; off *= 2) place += __shfl_xor_sync(0xffffffffu, place, off);
+            if (tid % kParts == 0 && k < n && place < K) write(place, e);
+        }
+        return;
+    }
     for (int size = 2; size <= n2; size *= 2)
         for (int stride = size / 2; stride > 0; stride /= 2) {
             for (int i = tid; i < n2 / 2; i += kThreads) {
-                const int a = 2 * i - (i & (stride - 1)), b = a + stride;
-                const uint64_t p = sh.buf[a], q = sh.buf[b];
-                if ((p < q) == ((a & size) == 0)) {
-                    sh.buf[a] = q;
-                    sh.buf[b] = p;
+                const int p = 2 * i - (i & (stride - 1)), q = p + stride;
+                const uint64_t u = sh.buf[p], v = sh.buf[q];
+                if ((u < v) == ((p & size) == 0)) {
+                    sh.buf[p] = v;
+                    sh.buf[q] = u;
                 }
             }
             sync();
         }
+    for (int k = tid; k < K; k += kThreads) write(k, sh.buf[k]);
 }
 
+// Steps are counted in 32 bits: 2^31 of them are 32 TiB of logits.
 struct Layout {
-    int64_t steps_per_row;  // ceil(V / kStep)
-    int64_t steps;          // of all rows
+    int steps_per_row;  // ceil(V / entries of a step)
+    int steps;          // of all rows
     int ctas;
     int pieces;             // most CTAs that share a row
 };
 
 // The steps of CTA b: [b * steps / ctas, (b + 1) * steps / ctas).
-__host__ __device__ __forceinline__ int64_t share_begin(const Layout &l, int64_t b) {
-    return b * l.steps / l.ctas;
+__host__ __device__ __forceinline__ int share_begin(const Layout &l, int b) {
+    return (int)((int64_t)b * l.steps / l.ctas);
 }
 // The CTA that holds step s.
-__device__ __forceinline__ int64_t share_of(const Layout &l, int64_t s) {
-    int64_t b = s * l.ctas / l.steps;
+__device__ __forceinline__ int share_of(const Layout &l, int s) {
+    int b = (int)((int64_t)s * l.ctas / l.steps);
     while (share_begin(l, b + 1) <= s) ++b;
     return b;
 }
@@ -209,7 +269,7 @@ __device__ __forceinline__ int64_t share_of(const Layout &l, int64_t s) {
 // The workspace: per row and piece the maximum and sum, then its K candidates.
 __device__ __forceinline__ uint64_t *piece_entries(void *ws, const Layout &l, int64_t R, int K, int64_t row,
                                                    int64_t piece) {
-    return static_cast<uint64_t *>(ws) + R * l.pieces + (row * l.pieces + piece) * K;
+    return static_cast<uint64_t *>(ws) + R * l.pieces + (row * l.pieces + piece) * (K + cut_slack(K));
 }
 __device__ __forceinline__ MaxSum *piece_state(void *ws, const Layout &l, int64_t row, int64_t piece) {
     return static_cast<MaxSum *>(ws) + row * l.pieces + piece;
@@ -219,28 +279,20 @@ __device__ __forceinline__ float row_lse(const MaxSum &st, float T) {
     return st.m == -INFINITY ? __int_as_float(0x7fc00000) : st.m / T + logf(st.s);
 }
 
-__device__ __forceinline__ void write_row(const RowTopKArgs &a, int64_t row, const uint64_t *best) {
-    for (int k = threadIdx.x; k < a.K; k += kThreads) {
-        const uint64_t e = best[k];
-        const uint32_t v = 0xffffffffu - (uint32_t)e;
-        a.values[row * a.ldk + k] = key_value((uint32_t)(e >> 32));
-        a.indices[row * a.ldk + k] = (int32_t)v;
-    }
-}
-
 template <typename T, bool LSE>
 __global__ void __launch_bounds__(kThreads + 32, kPerSm)
     topk_pieces_kernel(const RowTopKArgs a, const Layout lay, void *ws) {
-    constexpr int kSize = sizeof(T), N = 16 / kSize;
-    constexpr int kStepBytes = kStep * kSize;
-    constexpr int kStepsPerStage = kStageBytes / kStepBytes;  // 1 (fp32) or 2 (bf16)
-    constexpr int kVecs = kPerThread / N;                     // 16-byte vectors per thread and step
+    constexpr int N = Vec<T>::N;
+    constexpr int kStep = kStageBytes / sizeof(T);
+    // after a cut, and as long as a vector of every thread still fits
+    constexpr int kFits = kBuffer - kThreads * N;
+    static_assert(kFits >= kMaxTopK + cut_slack(kMaxTopK) && kBuffer >= kVecs * kThreads, "");
     extern __shared__ __align__(128) unsigned char ring[];
     Shared &sh = *reinterpret_cast<Shared *>(ring + kStages * kStageBytes);
 
     const int tid = threadIdx.x, lane = tid & 31;
-    const int64_t V = a.V, nv = V / N * N;  // entries that bulk copies bring
-    const int64_t begin = share_begin(lay, blockIdx.x), end = share_begin(lay, (int64_t)blockIdx.x + 1);
+    const int V = (int)a.V, nv = V / N;  // entries, and vectors that bulk copies bring
+    const int begin = share_begin(lay, blockIdx.x), end = share_begin(lay, blockIdx.x + 1);
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_u32(&sh.full[i]), 1);
@@ -252,154 +304,195 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm)
     __syncthreads();
     grid_launch_dependents();
 
+    int slot = 0;
+    uint32_t use = 0;
+    auto next_stage = [&]() {
+        if (++slot == kStages) {
+            slot = 0;
+            ++use;
+        }
+    };
+    // vectors of the row's step i
+    auto vecs_of = [&](int i) { return max(0, min(kVecs * kThreads, nv - i * (kVecs * kThreads))); };
     if (tid >= kThreads) {
         // ------------------------------------------------------------ loader
-        if (lane == 0) {
-            const uint64_t policy = l2_policy_evict_first();
-            int slot = 0;
-            uint32_t use = 0;
-            bool ok = true;
-            for (int64_t s = begin; s < end && ok;) {
-                const int64_t row = s / lay.steps_per_row, s0 = s % lay.steps_per_row;
-                const int64_t n = min(end - s, lay.steps_per_row - s0);
-                const T *x = static_cast<const T *>(a.logits) + row * a.ldl;
-                for (int64_t i = 0; i < n && ok; i += kStepsPerStage) {
-                    const int64_t v0 = (s0 + i) * kStep;
-                    const int64_t v1 = min(nv, (s0 + min(i + kStepsPerStage, n)) * kStep);
-                    if (use > 0) ok = ring_wait(smem_u32(&sh.empty[slot]), (use - 1) & 1, &sh.abort_flag);
-                    if (!ok) break;
-                    const uint32_t bytes = v1 > v0 ? (uint32_t)(v1 - v0) * kSize : 0u, bar = smem_u32(&sh.full[slot]);
-                    mbar_arrive_expect_tx(bar, bytes);
-                    if (bytes) bulk_load(smem_u32(ring + slot * kStageBytes), x + v0, bytes, bar, policy);
-                    if (++slot == kStages) {
-                        slot = 0;
-                        ++use;
-                    }
-                }
-                s += n;
+        if (lane != 0) return;
+        const uint64_t policy = l2_policy_evict_first();
+        bool ok = true;
+        int row = begin / lay.steps_per_row, i = begin % lay.steps_per_row;
+#pragma unroll 1
+        for (int s = begin; s < end; ++s) {
+            if (use > 0) ok = ring_wait(smem_u32(&sh.empty[slot]), (use - 1) & 1, &sh.abort_flag);
+            if (!ok) break;
+            const uint32_t bytes = (uint32_t)vecs_of(i) * 16u, bar = smem_u32(&sh.full[slot]);
+            mbar_arrive_expect_tx(bar, bytes);
+            if (bytes)
+                bulk_load(smem_u32(ring + slot * kStageBytes), static_cast<const T *>(a.logits) + row * a.ldl + (int64_t)i * kStep,
+                          bytes, bar, policy);
+            next_stage();
+            if (++i == lay.steps_per_row) {
+                i = 0;
+                ++row;
             }
-            // a CTA that gave up leaves only after its copies in flight have landed
-            if (!ok)
-                for (int i = 0; i < kStages; ++i) {
-                    const uint32_t issued = use + (i < slot ? 1 : 0);
-                    if (issued > 0) drain_wait(smem_u32(&sh.full[i]), (issued - 1) & 1);
-                }
         }
+        // a CTA that gave up leaves only after its copies in flight have landed
+        if (!ok)
+            for (int k = 0; k < kStages; ++k) {
+                const uint32_t issued = use + (k < slot ? 1 : 0);
+                if (issued > 0) drain_wait(smem_u32(&sh.full[k]), (issued - 1) & 1);
+            }
         return;
     }
 
     // ---------------------------------------------------------------- selecting threads
     const float c = kLog2e / a.T;
-    int slot = 0;
-    uint32_t phase = 0;
-    for (int64_t s = begin; s < end;) {
-        const int64_t row = s / lay.steps_per_row, s0 = s % lay.steps_per_row;
-        const int64_t n = min(end - s, lay.steps_per_row - s0);
+    const uint4 low = make_uint4(Vec<T>::kLow, Vec<T>::kLow, Vec<T>::kLow, Vec<T>::kLow);
+    const int slack = cut_slack(a.K), limit = min(kFits, max(1024, 4 * a.K));
+#pragma unroll 1
+    for (int s = begin; s < end;) {
+        const int row = s / lay.steps_per_row, s0 = s - row * lay.steps_per_row;
+        const int n = min(end - s, lay.steps_per_row - s0);
+        const bool whole = n == lay.steps_per_row;
         const T *x = static_cast<const T *>(a.logits) + row * a.ldl;
         MaxSum st{-INFINITY, 0.0f};
         float threshold = 0.0f;
-        bool open = true;  // fewer than K entries seen: everything is a candidate
-        int held = 0;      // entries placed while open
-        if (tid == 0) sh.count = 0;
+        if (tid == 0) {
+            sh.count = 0;
+            sh.overflow = 0;
+        }
         sync();
-        for (int64_t i = 0; i < n; ++i) {
-            const int part = (int)(i % kStepsPerStage);
-            if (part == 0) ring_wait(smem_u32(&sh.full[slot]), phase, &sh.abort_flag);
-            const int64_t v0 = (s0 + i) * kStep;
-            const uint4 *stage = reinterpret_cast<const uint4 *>(ring + slot * kStageBytes + part * kStepBytes);
-            float f[kPerThread];
-            const bool whole = v0 + kStep <= nv;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            // (where the ring gave up: stale bytes, but all in bounds, and the error word is set)
+            ring_wait(smem_u32(&sh.full[slot]), use & 1, &sh.abort_flag);
+            const int v0 = (s0 + i) * kStep, here = vecs_of(s0 + i);
+            const uint4 *stage = reinterpret_cast<const uint4 *>(ring + slot * kStageBytes);
+            const bool last = i + 1 == n, ends_row = s0 + i + 1 == lay.steps_per_row;
+            uint4 in[kVecs];
 #pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                const int e0 = (tid + j * kThreads) * N;
-                const uint4 v = stage[tid + j * kThreads];
-                if constexpr (N == 4) {
-                    f[4 * j] = __uint_as_float(v.x);
-                    f[4 * j + 1] = __uint_as_float(v.y);
-                    f[4 * j + 2] = __uint_as_float(v.z);
-                    f[4 * j + 3] = __uint_as_float(v.w);
-                } else {
-                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+            for (int j = 0; j < kVecs; ++j) in[j] = tid + j * kThreads < here ? stage[tid + j * kThreads] : low;
+            // the row's last V % N entries, which no copy brings
+            const bool tail = ends_row && tid < V - nv * N;
+            const float one[1] = {tail ? to_f32(x[nv * N + tid]) : -INFINITY};
+            const float bm = Vec<T>::largest(in);
+            if (i == 0) {
+                // A value that K of the threads' maxima reach, or of their vectors' where K is too many:
+                // bit by bit, until not many more than K reach it.
+                constexpr int kMost = kThreads * 7 / 8;
+                uint32_t key[kVecs], edge = 0;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        f[2 * q] = __uint_as_float(u[q] << 16);
-                        f[2 * q + 1] = __uint_as_float(u[q] & 0xffff0000u);
+                for (int j = 0; j < kVecs; ++j) {
+                    const uint4 v[1] = {in[j]};
+                    key[j] = order_key(Vec<T>::largest(v));
+                }
+                if (a.K <= kMost) key[0] = order_key(bm);
+#pragma unroll 1
+                for (uint32_t bit = 1u << 31; bit; bit >>= 1) {
+                    int reach = sync_count(key[0] >= (edge | bit));
+                    if (a.K > kMost) {
+#pragma unroll
+                        for (int j = 1; j < kVecs; ++j) reach += sync_count(key[j] >= (edge | bit));
                     }
+                    if (reach >= a.K) edge |= bit;
+                    if (reach >= a.K && reach <= a.K + a.K / 8) break;
                 }
-                if (!whole) {
-                    // the row's end: what the copy did not bring, from memory or not there
-#pragma unroll
-                    for (int e = 0; e < N; ++e)
-                        if (v0 + e0 + e >= nv) f[j * N + e] = v0 + e0 + e < V ? to_f32(x[v0 + e0 + e]) : -INFINITY;
-                }
+                // Candidates are above the threshold: it is the next number below the edge (below 0 is not
+                // -0), and below -inf, as where there is no edge, a NaN: every entry is a candidate.
+                threshold = edge > 0 ? key_value(edge - (edge == order_key(0.0f) ? 2 : 1)) : __int_as_float(0x7fc00000);
             }
-            if (part == kStepsPerStage - 1 || i + 1 == n) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.empty[slot]));
-                if (++slot == kStages) {
-                    slot = 0;
-                    phase ^= 1;
-                }
+            if (LSE) {
+                fold_vecs<T>(st, in, c);
+                if (ends_row) fold(st, one, c);
             }
-            if (LSE) fold(st, f, c);
-            bool crowded = false;
-            if (open) {
-                // every entry has its place; those past the row's end are 0, below all others
+            // all vectors at once; where that is more than the buffer takes, once more one at a time
+            int width = kVecs;
+#pragma unroll 1
+            for (int j0 = 0; j0 < kVecs;) {
+                const bool ends = last && j0 + width == kVecs;
+                bool crowded = false;
+                if (__any_sync(0xffffffffu, !(bm <= threshold))) {
+                    // a bit per entry of the lane's that is a candidate
+                    uint32_t mask = 0;
 #pragma unroll
-                for (int j = 0; j < kPerThread; ++j) {
-                    const int e = (tid + j / N * kThreads) * N + j % N;
-                    sh.buf[held + e] = v0 + e < V ? entry(f[j], (uint32_t)(v0 + e)) : 0;
-                }
-                held += kStep;
-                if (held >= a.K) crowded = true;
-            } else {
-                float bm = f[0];
+                    for (int j = 0; j < kVecs; ++j) {
+                        const uint4 v[1] = {in[j]};
+                        if (__any_sync(0xffffffffu, !(Vec<T>::largest(v) <= threshold)) && j >= j0 && j < j0 + width &&
+                            tid + j * kThreads < here) {
+                            f32x2 p[N / 2];
+                            Vec<T>::pairs(in[j], p);
 #pragma unroll
-                for (int j = 1; j < kPerThread; ++j) bm = fmaxf(bm, f[j]);
-                if (bm > threshold) {
-#pragma unroll
-                    for (int j = 0; j < kPerThread; ++j)
-                        if (f[j] > threshold) {
-                            const int e = (tid + j / N * kThreads) * N + j % N;
-                            const uint32_t p = atomicAdd(&sh.count, 1u);
-                            sh.buf[p] = entry(f[j], (uint32_t)(v0 + e));
-                            crowded = crowded || p >= (uint32_t)(kBuffer - kStep);
+                            for (int e = 0; e < N / 2; ++e) {
+                                float f, g;
+                                unpair(p[e], f, g);
+                                mask |= (f <= threshold ? 0u : 1u << (j * N + 2 * e)) |
+                                        (g <= threshold ? 0u : 2u << (j * N + 2 * e));
+                            }
                         }
-                }
-            }
-            // the buffer is cut when the next step might not fit, and at the end of the piece
-            if (sync_or(crowded) || i + 1 == n) {
-                const int got = open ? held : (int)sh.count;
-                if (got > a.K || open) {
-                    if (got >= a.K) {
-                        sync();  // every thread has read the count
-                        const uint64_t least = select_top(sh, got, a.K);
-                        threshold = key_value((uint32_t)(least >> 32));
-                        open = false;
-                        held = a.K;
+                    }
+                    // their places: one addition per warp
+                    const int mine = __popc(mask);
+                    int upto = mine;
+#pragma unroll
+                    for (int off = 1; off < 32; off <<= 1) {
+                        const int o = __shfl_up_sync(0xffffffffu, upto, off);
+                        if (lane >= off) upto += o;
+                    }
+                    int at = 0;
+                    if (lane == 31 && upto > 0) at = (int)atomicAdd(&sh.count, (uint32_t)upto);
+                    at = __shfl_sync(0xffffffffu, at, 31) + upto - mine;
+#pragma unroll 1
+                    for (; mask; mask &= mask - 1, ++at) {
+                        const int bit = __ffs(mask) - 1, e = (tid + bit / N * kThreads) * N + bit % N;
+                        if (at < kBuffer)
+                            sh.buf[at] = entry(to_f32(reinterpret_cast<const T *>(stage)[e]), (uint32_t)(v0 + e));
+                        else
+                            sh.overflow = 1;
+                        crowded = at >= limit;
                     }
                 }
+                if (tail && j0 + width == kVecs && !(one[0] <= threshold)) {
+                    const int at = (int)atomicAdd(&sh.count, 1u);
+                    if (at < kBuffer)
+                        sh.buf[at] = entry(one[0], (uint32_t)(nv * N + tid));
+                    else
+                        sh.overflow = 1;
+                    crowded |= at >= limit;
+                }
+                if (sync_or(crowded) || (ends && !whole)) {
+                    if (width == kVecs && sh.overflow) {
+                        keep(sh, kBuffer, 0, (uint32_t)v0);
+                        if (tid == 0) sh.overflow = 0;
+                        width = 1;
+                        continue;
+                    }
+                    const int got = (int)sh.count;
+                    sync();  // every thread has read the count
+                    if (got > limit || (ends && !whole && got > a.K + slack)) {
+                        keep(sh, got, edge_of(sh, got, a.K, slack), 0xffffffffu);
+                        threshold = key_value(sh.least);
+                    }
+                }
+                j0 += width;
             }
+            if (lane == 0) mbar_arrive(smem_u32(&sh.empty[slot]));
+            next_stage();
         }
         // ------------------------------------------------------------ the piece's result
-        const int got = open ? held : a.K;  // open: a short piece, padded with 0 to a step
-        const int64_t cta0 = share_of(lay, row * lay.steps_per_row);
         if (LSE) {
             st = warp_merge(st, c);
             if (lane == 0) sh.warp_state[tid >> 5] = st;
             sync();
             st = warp_merge(lane < kWarps ? sh.warp_state[lane] : MaxSum{-INFINITY, 0.0f}, c);
         }
-        if (n == lay.steps_per_row) {
-            sync();
-            sort_top(sh, a.K);
-            write_row(a, row, sh.buf);
+        const int got = (int)sh.count;
+        if (whole) {
+            write_top(sh, a, row, got);
             if (LSE && tid == 0) a.lse[row] = row_lse(st, a.T);
         } else {
-            sync();
-            uint64_t *out = piece_entries(ws, lay, a.R, a.K, row, blockIdx.x - cta0);
-            for (int k = tid; k < a.K; k += kThreads) out[k] = k < got ? sh.buf[k] : 0;
-            if (LSE && tid == 0) *piece_state(ws, lay, row, blockIdx.x - cta0) = st;
+            const int piece = (int)blockIdx.x - share_of(lay, row * lay.steps_per_row);
+            uint64_t *out = piece_entries(ws, lay, a.R, a.K, row, piece);
+            for (int k = tid; k < a.K + slack; k += kThreads) out[k] = k < got ? sh.buf[k] : 0;
+            if (LSE && tid == 0) *piece_state(ws, lay, row, piece) = st;
         }
         sync();  // the buffer is free for the next row
         s += n;
@@ -409,47 +502,41 @@ __global__ void __launch_bounds__(kThreads + 32, kPerSm)
 // Takes the K largest of a split row's candidates.
 template <bool LSE>
 __global__ void __launch_bounds__(kThreads) topk_merge_kernel(const RowTopKArgs a, const Layout lay, void *ws) {
-    __shared__ Shared sh;
+    extern __shared__ __align__(128) unsigned char ring[];
+    Shared &sh = *reinterpret_cast<Shared *>(ring);
     grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31;
-    const int64_t row = blockIdx.x;
-    const int64_t first = share_of(lay, row * lay.steps_per_row);
-    const int64_t last = share_of(lay, (row + 1) * lay.steps_per_row - 1);
+    const int row = blockIdx.x;
+    const int first = share_of(lay, row * lay.steps_per_row);
+    const int last = share_of(lay, (row + 1) * lay.steps_per_row - 1);
     if (first == last) return;  // the pieces kernel has written the row
-    const int64_t total = (last - first + 1) * a.K;
+    const int total = (last - first + 1) * (a.K + cut_slack(a.K));
     const uint64_t *in = piece_entries(ws, lay, a.R, a.K, row, 0);
     uint64_t least = 0;
-    int held = 0;
     if (tid == 0) sh.count = 0;
     sync();
-    for (int64_t e0 = 0; e0 < total;) {
-        // as many as the buffer takes; what lies below the K-th largest so far is passed over
-        const int room = kBuffer - held;
-        const int n = (int)min((int64_t)room, total - e0);
+    // as many at once as the buffer takes; what lies below the K-th largest so far is passed over
+    for (int e0 = 0; e0 < total;) {
+        const int n = min(kBuffer - (int)sh.count, total - e0);
+        sync();
         for (int i = tid; i < n; i += kThreads) {
             const uint64_t e = in[e0 + i];
-            if (e >= least && e != 0) sh.buf[held + atomicAdd(&sh.count, 1u)] = e;
+            if (e >= least && e != 0) sh.buf[atomicAdd(&sh.count, 1u)] = e;
         }
-        sync();
-        const int got = held + (int)sh.count;
         sync();
         e0 += n;
-        if (got > a.K) {
-            least = select_top(sh, got, a.K);
-            held = a.K;
-        } else {
-            held = got;
+        const int got = (int)sh.count;
+        sync();
+        if (e0 < total && got > a.K) {
+            least = edge_of(sh, got, a.K, 0);
+            keep(sh, got, least, 0xffffffffu);
         }
-        sync();
-        if (tid == 0) sh.count = 0;
-        sync();
     }
-    sort_top(sh, a.K);
-    write_row(a, row, sh.buf);
+    write_top(sh, a, row, (int)sh.count);
     if (LSE && tid < 32) {
         const float c = kLog2e / a.T;
         MaxSum st{-INFINITY, 0.0f};
-        for (int64_t p = lane; p <= last - first; p += 32) merge(st, *piece_state(ws, lay, row, p), c);
+        for (int p = lane; p <= last - first; p += 32) merge(st, *piece_state(ws, lay, row, p), c);
         st = warp_merge(st, c);
         if (lane == 0) a.lse[row] = row_lse(st, a.T);
     }
@@ -458,18 +545,21 @@ __global__ void __launch_bounds__(kThreads) topk_merge_kernel(const RowTopKArgs 
 constexpr size_t kDynamic = kStages * kStageBytes + sizeof(Shared);
 
 // The deal of the rows' steps over the device's CTAs.
-bool layout(int64_t R, int64_t V, int K, Layout *l) {
+bool layout(int64_t R, int64_t V, int K, int dtype, Layout *l) {
     const int sms = device_sm_count();
     if (sms <= 0) return false;
-    l->steps_per_row = (V + kStep - 1) / kStep;
-    l->steps = R * l->steps_per_row;
+    const int64_t step = kStageBytes / (dtype == DG_BF16 ? 2 : 4);
+    const int64_t per_row = (V + step - 1) / step, steps = R * per_row;
+    if (steps > INT32_MAX) return false;
+    l->steps_per_row = (int)per_row;
+    l->steps = (int)steps;
     // a piece of a row costs a selection and K candidates to merge: no fewer than kMinSteps steps,
     // nor than 8 K entries
-    const int64_t least = max((int64_t)kMinSteps, ((int64_t)8 * K + kStep - 1) / kStep);
+    const int64_t least = max((int64_t)kMinSteps, (8 * (int64_t)K + step - 1) / step);
     const int64_t want = (l->steps + least - 1) / least;
     l->ctas = (int)max((int64_t)1, min((int64_t)sms * kPerSm, want));
-    const int64_t share = l->steps / l->ctas;  // every CTA has at least this
-    l->pieces = (int)min((l->steps_per_row + share - 1) / share + 1, l->steps_per_row);
+    const int share = l->steps / l->ctas;  // every CTA has at least this
+    l->pieces = min((l->steps_per_row + share - 1) / share + 1, l->steps_per_row);
     return true;
 }
 
@@ -483,6 +573,8 @@ cudaError_t launch(const RowTopKArgs &a, const Layout &lay, void *ws, cudaStream
     if (e != cudaSuccess) return e;
     if (dev >= kMaxDevices || !attr_set[dev].load(std::memory_order_acquire)) {
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDynamic);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(topk_merge_kernel<LSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
         if (e != cudaSuccess) return e;
         if (dev < kMaxDevices) attr_set[dev].store(1, std::memory_order_release);
     }
@@ -493,6 +585,7 @@ cudaError_t launch(const RowTopKArgs &a, const Layout &lay, void *ws, cudaStream
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.R);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Shared);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -504,15 +597,15 @@ cudaError_t launch(const RowTopKArgs &a, const Layout &lay, void *ws, cudaStream
 
 }  // namespace
 
-size_t row_topk_workspace_bytes(int64_t R, int64_t V, int K, int) {
+size_t row_topk_workspace_bytes(int64_t R, int64_t V, int K, int dtype) {
     Layout l;
-    if (!layout(R, V, K, &l)) return 0;
-    return (size_t)R * l.pieces * (sizeof(MaxSum) + (size_t)K * sizeof(uint64_t));
+    if (!layout(R, V, K, dtype, &l)) return 0;
+    return (size_t)R * l.pieces * (sizeof(MaxSum) + (size_t)(K + cut_slack(K)) * sizeof(uint64_t));
 }
 
 cudaError_t launch_row_topk(const RowTopKArgs &a, void *workspace, cudaStream_t stream) {
     Layout l;
-    if (!layout(a.R, a.V, a.K, &l)) return cudaErrorNoDevice;
+    if (!layout(a.R, a.V, a.K, a.dtype, &l)) return cudaErrorNoDevice;
     if (a.dtype == DG_BF16)
         return a.lse ? launch<__nv_bfloat16, true>(a, l, workspace, stream)
                      : launch<__nv_bfloat16, false>(a, l, workspace, stream);
