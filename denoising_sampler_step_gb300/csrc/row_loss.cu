@@ -15,9 +15,10 @@
 // leaves the memory idle.  Rows of up to kMaxTile bytes are one tile and need no exchange.
 //
 // Measured, 1,024 rows of 262,144 entries, against a plain copy's 6,780 GB/s: policy loss fp32 forward
-// 99%, step 89%, backward 93%; bf16 74%, 85%, 95%; distillation, K = 64, fp32 88%, 89%, 94%, bf16 66%,
-// 83%, 89%; a step with K = 512 67%, with K = 1,024 44% (every tile's share of the teacher's entries is
-// found by looking at all of them).
+// 101%, step 89%, backward 97%; bf16 82%, 85%, 89%; distillation, K = 64, fp32 94%, 88%, 94%, bf16 74%,
+// 82%, 91%; a step with K = 512 75%, with K = 1,024 60% (each tile's share of the teacher's entries is
+// found by looking at all of them).  What is left in a step: reads and writes that alternate, and in bf16
+// the folding warps, which have twice the entries per byte.
 //
 // In a CTA, each warp or group of warps walks the CTA's tiles at its own pace, held together by an
 // mbarrier per stage and step:
@@ -81,9 +82,10 @@ __device__ __forceinline__ float never_zero(float v) { return v == 0.0f ? -0.0f 
 template <int HEAD, int PASS, bool SPLIT>
 struct Roles {
     static constexpr bool kForward = (PASS & kPassForward) != 0, kBackward = (PASS & kPassBackward) != 0;
+    // (16 folding warps where no others do arithmetic: policy loss forward, bf16, 97 us; 8 warps 109)
     static constexpr int kClear = HEAD == kHeadDistill ? 3 : 0, kPost = kForward && SPLIT ? 1 : 0,
                          kOwn = kForward ? (SPLIT ? 2 : 4) : 0, kWatch = kForward && kBackward && SPLIT ? 1 : 0,
-                         kSettle = kBackward ? 2 : 0, kFold = kForward ? 8 : 0, kGrad = kBackward ? 8 : 0;
+                         kSettle = kBackward ? 2 : 0, kFold = !kForward ? 0 : kBackward ? 8 : 16, kGrad = kBackward ? 8 : 0;
     // first warps (the loader is 0, the zero warp 1)
     static constexpr int clear = 2, post = clear + kClear, own = post + kPost, watch = own + kOwn,
                          settle = watch + kWatch, fold = settle + kSettle, grad = fold + kFold, end = grad + kGrad;
@@ -105,7 +107,7 @@ struct Shared {
         done[kMaxStages], empty[kMaxStages];
     Tile tile[kMaxStages];
     RowClose close[kMaxStages];
-    MaxSum warp_sum[kMaxStages][8];
+    MaxSum warp_sum[kMaxStages][16];
     int entries[kMaxStages];          // of the teacher's in the tile
     uint32_t tail_taken[kMaxStages];  // which of the row's last entries are among them
     int abort_flag;
@@ -181,6 +183,22 @@ __device__ __forceinline__ bool look_up(const RowClose *in, RowClose *cl) {
     auto hi = [](unsigned long long v) { return __uint_as_float((uint32_t)(v >> 32)); };
     *cl = RowClose{lo(w[0]), hi(w[0]), lo(w[1]), hi(w[1]), lo(w[2]), hi(w[2]), lo(w[3]), 1u};
     return w[0] && w[1] && w[2] && w[3];
+}
+
+// From a saved log-sum-exp, p = exp((x - T lse) / T): T lse as m, what its rounding lost as a factor.
+__device__ __forceinline__ RowClose close_saved(const RowLossArgs &a, float lse) {
+    RowClose cl{};
+    cl.m = never_zero(finite_max(lse * a.T));
+    cl.inv_s = expf(-fmaf(lse, a.T, -lse * a.T) / a.T);
+    cl.flag = 1;
+    return cl;
+}
+__device__ __forceinline__ RowClose close_token(const RowLossArgs &a, float w, float lse) {
+    RowClose cl = close_saved(a, lse);
+    cl.coef = -w / a.T;
+    cl.mass = 1.0f;
+    cl.scale = cl.coef * cl.inv_s;
+    return cl;
 }
 
 // A posted sum, polled for at most kWaitLimitNs (0: gave up).
@@ -279,7 +297,9 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
         float next_close = 0.0f;
         auto fetch = [&](int64_t r) {
             next.load(a, r);
-            if (!kForward && warp == 0 && lane < 8) next_close = reinterpret_cast<const float *>(plan.rows + r)[lane];
+            if (!kForward && warp == 0 && !kDistill) next_close = next.live(V) ? a.lse[r] : 0.0f;
+            if (!kForward && warp == 0 && kDistill && lane < 8)
+                next_close = reinterpret_cast<const float *>(plan.rows + r)[lane];
         };
         auto take_stage = [&]() {
             // (also its last copy has landed: an aborted CTA's roles leave stages as they are)
@@ -317,7 +337,8 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
             if (warp == 0 && live) {
                 take_stage();
                 if (ok) {
-                    if (!kForward && lane < 8) reinterpret_cast<float *>(&sh.close[slot])[lane] = my_close;
+                    if (!kForward && kDistill && lane < 8) reinterpret_cast<float *>(&sh.close[slot])[lane] = my_close;
+                    if (!kForward && !kDistill && lane == 0) sh.close[slot] = close_token(a, key.w, my_close);
                     if (lane == 0) sh.tile[slot] = t;
                     __syncwarp();
                     if (lane == 0) {
@@ -336,8 +357,9 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
                     for (int v = lane; v < vecs; v += 32) gv[v] = make_uint4(0, 0, 0, 0);
                     if (lane < t.end - t.len) g[t.len + lane] = from_f32<T>(0.0f);
                 }
+                if (HEAD == kHeadToken && starts_row && lane == 0 && key.w != 0.0f && key.tok >= V)
+                    atomicOr(&g_device_error, kErrorIndexRange);
                 if (kForward && starts_row && lane == 0) {
-                    if (HEAD == kHeadToken && key.w != 0.0f && key.tok >= V) atomicOr(&g_device_error, kErrorIndexRange);
                     if (a.lse) a.lse[t.row] = 0.0f;
                     if (a.loss) a.loss[t.row] = 0.0f;
                     if (a.logp) a.logp[t.row] = 0.0f;
@@ -379,32 +401,35 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
                 float *const lt = reinterpret_cast<float *>(at + kp), *const lx = lt + kp;
                 int count = 0;
                 uint32_t tail = 0;
-                constexpr int kAhead = 4;
+                bool beyond = false;
+                constexpr int kAhead = 16;  // loads at once (K = 1,024: 533 us a step; with 4, 657)
 #pragma unroll 1
                 for (int k0 = lane; k0 - lane < kp; k0 += 32 * kAhead) {
                     int v[kAhead];
-                    float tv[kAhead];
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i) v[i] = k0 + 32 * i < kp ? idx[k0 + 32 * i] : -1;
 #pragma unroll
                     for (int i = 0; i < kAhead; ++i) {
-                        const bool some = k0 + 32 * i < kp;
-                        v[i] = some ? idx[k0 + 32 * i] : -1;
-                        tv[i] = kBackward && some ? tl[k0 + 32 * i] : 0.0f;
-                    }
-#pragma unroll
-                    for (int i = 0; i < kAhead; ++i) {
-                        if (v[i] >= V) atomicOr(&g_device_error, kErrorIndexRange);
+                        if (k0 - lane + 32 * i >= kp) break;
                         const int off = v[i] - t.first;
                         const bool here = v[i] >= t.first && off < t.end;
+                        beyond |= v[i] >= V;
                         const uint32_t votes = __ballot_sync(0xffffffffu, here);
                         if (here) {
                             const int n = count + __popc(votes & ((1u << lane) - 1));
                             at[n] = off;
-                            lt[n] = tv[i];
+                            if (kBackward) lt[n] = __int_as_float(k0 + 32 * i);
                             if (off >= t.len) tail |= 1u << (off - t.len);
                         }
                         count += __popc(votes);
                     }
                 }
+                __syncwarp();
+                if (kBackward) {
+#pragma unroll 1
+                    for (int k = lane; k < count; k += 32) lt[k] = tl[__float_as_int(lt[k])];
+                }
+                if (beyond) atomicOr(&g_device_error, kErrorIndexRange);
                 tail = __reduce_or_sync(0xffffffffu, tail);
                 if (lane == 0) {
                     sh.entries[slot] = count;
@@ -476,11 +501,19 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
                 // for the loss (here, because the gradient may replace the logits once the row is
                 // published): sum of e_k [(t_k - t_max) - (x_k - x_max)] / T
 #pragma unroll 1
-                for (int k = lane; k < kp && a.loss; k += 32) {
-                    const int v = idx[k];
-                    if (v >= 0 && v < V) {
-                        const float dt = tl[k] - finite_max(teacher.m), e = ex2_approx(dt * c);
-                        if (e > 0.0f) spread += e * (dt - (to_f32(x[v]) - finite_max(top.m))) * inv_T;
+                for (int k0 = lane; k0 - lane < kp && a.loss; k0 += 32 * kAhead) {
+                    float xv[kAhead], tv[kAhead];
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i) {
+                        const int v = k0 + 32 * i < kp ? idx[k0 + 32 * i] : -1;
+                        const bool valid = v >= 0 && v < V;
+                        xv[i] = valid ? to_f32(x[v]) : 0.0f;
+                        tv[i] = valid ? tl[k0 + 32 * i] : -INFINITY;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i) {
+                        const float dt = tv[i] - finite_max(teacher.m), e = ex2_approx(dt * c);
+                        if (e > 0.0f) spread += e * (dt - (xv[i] - finite_max(top.m))) * inv_T;
                     }
                 }
                 spread = warp_sum(spread);
@@ -736,42 +769,26 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
     }
 }
 
-// Backward alone: what the gradient of each row needs, from the saved log-sum-exp.  A warp per row.
+// Distillation, backward alone: what the gradient of each row needs, from the saved log-sum-exp.  A warp
+// per row.
 constexpr int kCloseWarps = 8;
-template <typename T, int HEAD>
 __global__ void __launch_bounds__(32 * kCloseWarps) row_close_kernel(const RowLossArgs a, RowClose *rows) {
     const int64_t row = (int64_t)blockIdx.x * kCloseWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (row >= a.R) return;
-    RowKey<HEAD, kPassBackward> key;
-    key.load(a, row);
-    if (!key.live(a.V)) {
-        if (HEAD == kHeadToken && lane == 0 && key.w != 0.0f && key.tok >= a.V)
-            atomicOr(&g_device_error, kErrorIndexRange);
-        return;
-    }
-    const float c = kLog2e / a.T, lse = a.lse[row];
-    // p = exp((x - T lse) / T): T lse as m, what its rounding lost as a factor
-    RowClose cl{};
-    cl.m = never_zero(finite_max(lse * a.T));
-    cl.inv_s = expf(-fmaf(lse, a.T, -lse * a.T) / a.T);
-    cl.flag = 1;
-    if (HEAD == kHeadToken) {
-        cl.coef = -key.w / a.T;
-        cl.mass = 1.0f;
-        cl.scale = cl.coef * cl.inv_s;
-    } else {
-        MaxSum teacher{-INFINITY, 0.0f};
+    const float w = a.weight ? a.weight[row] : 1.0f, c = kLog2e / a.T;
+    if (w == 0.0f) return;
+    RowClose cl = close_saved(a, a.lse[row]);
+    MaxSum teacher{-INFINITY, 0.0f};
 #pragma unroll 1
-        for (int k = lane; k < a.K; k += 32) {
-            const int v = a.indices[row * a.ldk + k];
-            const float one[1] = {v >= 0 && v < a.V ? a.teacher[row * a.ldk + k] : -INFINITY};
-            fold(teacher, one, c);
-        }
-        teacher = warp_merge(teacher, c);
-        const float q_rest = teacher_terms(a, teacher, a.teacher_lse ? a.teacher_lse[row] : 0.0f, key.w, &cl);
-        cl.scale = bucket_scale(a, a.teacher_lse ? a.tail_logp[row] : 0.0f, q_rest, &cl) * cl.inv_s;
+    for (int k = lane; k < a.K; k += 32) {
+        const int v = a.indices[row * a.ldk + k];
+        const float one[1] = {v >= 0 && v < a.V ? a.teacher[row * a.ldk + k] : -INFINITY};
+        fold(teacher, one, c);
     }
+    teacher = warp_merge(teacher, c);
+    const float q_rest = teacher_terms(a, teacher, a.teacher_lse ? a.teacher_lse[row] : 0.0f, w, &cl);
+    cl.scale = bucket_scale(a, a.teacher_lse ? a.tail_logp[row] : 0.0f, q_rest, &cl) * cl.inv_s;
     if (lane == 0) rows[row] = cl;
 }
 
@@ -903,14 +920,11 @@ cudaError_t launch_pass(const RowLossArgs &a, RowLossHead head, RowLossPass pass
     plan.sums = reinterpret_cast<unsigned long long *>(plan.rows + a.R);
     cudaError_t e;
     const bool bf16 = a.dtype == DG_BF16;
-    if (pass == kPassBackward) {
+    if (pass == kPassBackward && head == kHeadDistill) {
         const unsigned blocks = (unsigned)((a.R + kCloseWarps - 1) / kCloseWarps);
-        if (head == kHeadToken)
-            row_close_kernel<float, kHeadToken><<<blocks, 32 * kCloseWarps, 0, stream>>>(a, plan.rows);
-        else
-            row_close_kernel<float, kHeadDistill><<<blocks, 32 * kCloseWarps, 0, stream>>>(a, plan.rows);
+        row_close_kernel<<<blocks, 32 * kCloseWarps, 0, stream>>>(a, plan.rows);
         e = cudaGetLastError();
-    } else if (tl.tiles > 1) {
+    } else if (pass != kPassBackward && tl.tiles > 1) {
         e = cudaMemsetAsync(workspace, 0, (size_t)a.R * (sizeof(RowClose) + 8 * (size_t)tl.tiles), stream);
     } else {
         e = cudaSuccess;
