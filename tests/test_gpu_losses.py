@@ -440,6 +440,23 @@ def test_a_row_without_a_distribution_gives_nan(B, dtype, V):
     assert torch.isnan(k["lse"][0]) and k["indices"].tolist() == [[0, 1, 2], [0, 1, 2]]
 
 
+def test_rows_longer_than_the_chip(B):
+    """More tiles than all SMs' shared memory holds: the row is read a second time for its gradient."""
+    R, V, K = 2, 7000001, 40
+    rng, x, xf, tok = token_case(R, V, "f32", pad=1)
+    logp = L.token_logp(xf, tok, 1.0)["logp"]
+    old, A = (logp - 0.1).astype(np.float32), np.float32([0.5, -1.5])
+    o = B.dg_policy_loss(x, i32(tok), f32(old), f32(A), grad=True)
+    want = L.policy_loss(xf, tok, old, A, None, T=1.0, weight=None, clip_low=0.2, clip_high=0.2, kl_coef=0.0)
+    tl = tol_logp(xf, tok, 1.0)
+    near(o["loss"], want["loss"], 2 * np.abs(A) * (tl + 16 * U), "loss")
+    mine = o["dlogp"].double().cpu().numpy()
+    want_g = L.token_grad(xf, tok, mine, 1.0, None)
+    near(o["grad"], want_g, grad_tol(want_g, softmax(xf, 1.0), mine, xf, 1.0, "f32", 4 * U), "gradient")
+    rng, x, xf, idx, t, lse = distill_case(R, V, K, "f32", 1.4, True)
+    check_distill(B, x, xf, idx, t, lse, 1.4, np.float32([1.0, 0.5]), "f32")
+
+
 @pytest.mark.parametrize("gap", [50.0, 1e4, 1e30])
 def test_one_hot_rows(B, gap):
     xf = np.zeros((2, 5000))
@@ -618,6 +635,24 @@ def test_topk_orders(B, dtype, V, K, shape):
     want = L.row_topk(xf, K)
     assert np.array_equal(o["indices"].cpu().numpy(), want["indices"])
     assert np.array_equal(o["values"].double().cpu().numpy(), want["values"])
+
+
+@pytest.mark.parametrize("R,V,K", [(700, 20000, 64), (310, 100003, 600), (1500, 3001, 300), (2048, 4096, 8), (400, 65536, 1)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_topk_of_many_rows(B, R, V, K, dtype):
+    """Several rows per CTA and rows that two CTAs share, in ascending order (the buffers of candidates fill
+    up again and again) and at random, against a stable sort."""
+    g = torch.Generator(device="cuda").manual_seed(R)
+    x = torch.randn(R, (V + 7) // 8 * 8, device="cuda", generator=g)[:, :V]
+    x[::3, :] = torch.arange(V, device="cuda") / V * 8 - 4
+    x[1::6, V // 2:] = -float("inf")
+    x = x.to(dtype)
+    x = torch.nn.functional.pad(x, (0, -V % 8))[:, :V]
+    o = B.dg_row_topk(x, K, lse=True)
+    values, order = x.float().sort(dim=1, descending=True, stable=True)
+    assert torch.equal(o["indices"].long(), order[:, :K]) and torch.equal(o["values"], values[:, :K])
+    want = x.double().logsumexp(1)
+    near(o["lse"], want.cpu().numpy(), tol_lse(x.double().cpu().numpy(), 1.0), "lse")
 
 
 def test_topk_feeds_the_distillation(B):
