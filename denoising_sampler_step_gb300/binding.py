@@ -102,6 +102,8 @@ lib.dg_row_topk.argtypes = _ROWS + [_i32, _f32, _p, _p, _i64, _p, _p, _sz, _p]
 lib.dg_row_topk.restype = ctypes.c_int
 lib.dg_row_loss_workspace_size.argtypes = [_i64, _i64, _i32]
 lib.dg_row_loss_workspace_size.restype = _sz
+lib.dg_row_loss_needs_workspace.argtypes = [_i64, _i32]
+lib.dg_row_loss_needs_workspace.restype = _i32
 lib.dg_token_logp.argtypes = _ROWS + [_p, _f32, _p, _p, _p, _p, _sz, _p]
 lib.dg_token_logp.restype = ctypes.c_int
 lib.dg_token_logp_backward.argtypes = _ROWS + [_p, _f32, _p, _p, _p, _p, _i64, _p, _sz, _p]
@@ -650,9 +652,14 @@ def _entries(indices, teacher, R: int, device) -> tuple:
     return K, ld
 
 
-@functools.lru_cache(maxsize=256)
 def dg_row_loss_workspace_size(R: int, V: int, dtype: int = DG_F32) -> int:
     return int(lib.dg_row_loss_workspace_size(R, V, dtype))
+
+
+@functools.lru_cache(maxsize=256)
+def dg_row_loss_needs_workspace(V: int, dtype: int = DG_F32) -> bool:
+    """Whether the loss calls but dg_distill_loss_backward, which always does, need a workspace."""
+    return bool(lib.dg_row_loss_needs_workspace(V, dtype))
 
 
 def loss_workspace(R: int, V: int, device, dtype: torch.dtype = torch.float32) -> torch.Tensor:
@@ -661,15 +668,16 @@ def loss_workspace(R: int, V: int, device, dtype: torch.dtype = torch.float32) -
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _loss_ws(ws, R: int, V: int, code: int, device, stream) -> torch.Tensor:
-    """The caller's workspace, or a new one (its memory stays with the stream that uses it)."""
-    if ws is not None:
-        return ws
-    n = max(16, dg_row_loss_workspace_size(R, V, code))
-    if stream is None:
-        return torch.empty(n, dtype=torch.uint8, device=device)
-    with _on(stream):
-        return torch.empty(n, dtype=torch.uint8, device=device)
+def _loss_ws(ws, R: int, V: int, code: int, device, stream, always: bool = False) -> tuple:
+    """(tensor, pointer, bytes) of the caller's workspace, of a new one (its memory stays with the stream
+    that uses it), or of none where the call needs none."""
+    if ws is None:
+        if not always and not dg_row_loss_needs_workspace(V, code):
+            return None, None, 0
+        n = max(16, dg_row_loss_workspace_size(R, V, code))
+        with _on(stream):
+            ws = torch.empty(n, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr(), ws.numel()
 
 
 def dg_row_topk_workspace_size(R: int, V: int, K: int, dtype: int = DG_F32) -> int:
@@ -705,22 +713,24 @@ def dg_row_topk(logits: torch.Tensor, K: int, temperature: float = 1.0, lse: boo
 
 
 def dg_token_logp(logits: torch.Tensor, token: torch.Tensor, temperature: float = 1.0,
-                  weight: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None, out: dict | None = None) -> dict:
+                  weight: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None,
+                  out: dict | None = None) -> dict:
     """ln softmax(logits / T)[token] per row -> dict logp, lse (fp32 [R]).  Rows of weight 0 or with a
     negative token are left out (0)."""
     x, code, R, V, ld = _logits(logits)
     dev, f32 = logits.device, torch.float32
     o = _fill(out, {"logp": (R, f32), "lse": (R, f32)}, dev, stream)
-    ws = _loss_ws(ws, R, V, code, dev, stream)
+    ws, ws_ptr, ws_bytes = _loss_ws(ws, R, V, code, dev, stream)
     _check(lib.dg_token_logp(x, code, R, V, ld, _vec(token, R, torch.int32, dev, "token"), temperature,
                              _vec(weight, R, f32, dev, "weight"), _vec(o["logp"], R, f32, dev, "logp"),
-                             _vec(o["lse"], R, f32, dev, "lse"), ws.data_ptr(), ws.numel(), _stream(stream)), "dg_token_logp")
+                             _vec(o["lse"], R, f32, dev, "lse"), ws_ptr, ws_bytes, _stream(stream)),
+           "dg_token_logp")
     return o
 
 
 def dg_token_logp_backward(logits: torch.Tensor, token: torch.Tensor, lse: torch.Tensor, dlogp: torch.Tensor,
-                           scale: torch.Tensor | None = None, temperature: float = 1.0, ws: torch.Tensor | None = None, stream=None,
-                           out: torch.Tensor | None = None) -> torch.Tensor:
+                           scale: torch.Tensor | None = None, temperature: float = 1.0,
+                           ws: torch.Tensor | None = None, stream=None, out: torch.Tensor | None = None) -> torch.Tensor:
     """The logits' gradient of sum_r scale_r dlogp_r logp_r from a forward call's lse (scale: the upstream
     gradient per row).  `out` may be the logits themselves."""
     x, code, R, V, ld = _logits(logits)
@@ -728,18 +738,19 @@ def dg_token_logp_backward(logits: torch.Tensor, token: torch.Tensor, lse: torch
     if out is None:
         out = _new_grad(logits, stream)
     g, ldg = _grad_like(out, logits)
-    ws = _loss_ws(ws, R, V, code, dev, stream)
+    ws, ws_ptr, ws_bytes = _loss_ws(ws, R, V, code, dev, stream)
     _check(lib.dg_token_logp_backward(x, code, R, V, ld, _vec(token, R, torch.int32, dev, "token"), temperature,
                                       _vec(lse, R, f32, dev, "lse"), _vec(dlogp, R, f32, dev, "dlogp"),
-                                      _vec(scale, R, f32, dev, "scale"), g, ldg, ws.data_ptr(), ws.numel(), _stream(stream)),
+                                      _vec(scale, R, f32, dev, "scale"), g, ldg, ws_ptr, ws_bytes,
+                                      _stream(stream)),
            "dg_token_logp_backward")
     return out
 
 
 def dg_distill_loss(logits: torch.Tensor, indices: torch.Tensor, teacher: torch.Tensor,
                     teacher_lse: torch.Tensor | None = None, temperature: float = 1.0,
-                    weight: torch.Tensor | None = None, grad: bool = False, ws: torch.Tensor | None = None, stream=None,
-                    out: dict | None = None) -> dict:
+                    weight: torch.Tensor | None = None, grad: bool = False,
+                    ws: torch.Tensor | None = None, stream=None, out: dict | None = None) -> dict:
     """Distillation from a teacher's top logits (dg_row_topk's indices and values, with teacher_lse its lse
     for the bucket of the other entries) -> dict loss, lse (fp32 [R]), tail_logp (with teacher_lse) and,
     with grad=True or a `grad` in `out`, the logits' gradient of sum_r weight_r loss_r."""
@@ -753,19 +764,20 @@ def dg_distill_loss(logits: torch.Tensor, indices: torch.Tensor, teacher: torch.
     if grad and "grad" not in o:
         o["grad"] = _new_grad(logits, stream)
     g, ldg = _grad_like(o["grad"], logits) if "grad" in o else (None, 0)
-    ws = _loss_ws(ws, R, V, code, dev, stream)
+    ws, ws_ptr, ws_bytes = _loss_ws(ws, R, V, code, dev, stream)
     _check(lib.dg_distill_loss(x, code, R, V, ld, indices.data_ptr(), teacher.data_ptr(), K, ldk,
                                _vec(teacher_lse, R, f32, dev, "teacher_lse"), temperature,
                                _vec(weight, R, f32, dev, "weight"), _vec(o["loss"], R, f32, dev, "loss"),
                                _vec(o["lse"], R, f32, dev, "lse"), _vec(o.get("tail_logp"), R, f32, dev, "tail_logp"),
-                               g, ldg, ws.data_ptr(), ws.numel(), _stream(stream)), "dg_distill_loss")
+                               g, ldg, ws_ptr, ws_bytes, _stream(stream)), "dg_distill_loss")
     return o
 
 
 def dg_distill_loss_backward(logits: torch.Tensor, indices: torch.Tensor, teacher: torch.Tensor,
                              lse: torch.Tensor, dloss: torch.Tensor | None = None,
                              teacher_lse: torch.Tensor | None = None, tail_logp: torch.Tensor | None = None,
-                             temperature: float = 1.0, ws: torch.Tensor | None = None, stream=None, out: torch.Tensor | None = None) -> torch.Tensor:
+                             temperature: float = 1.0, ws: torch.Tensor | None = None, stream=None,
+                             out: torch.Tensor | None = None) -> torch.Tensor:
     """The logits' gradient of sum_r dloss_r loss_r from a forward call's lse (and tail_logp).  `out` may be
     the logits themselves."""
     x, code, R, V, ld = _logits(logits)
@@ -774,11 +786,12 @@ def dg_distill_loss_backward(logits: torch.Tensor, indices: torch.Tensor, teache
     if out is None:
         out = _new_grad(logits, stream)
     g, ldg = _grad_like(out, logits)
-    ws = _loss_ws(ws, R, V, code, dev, stream)
+    ws, ws_ptr, ws_bytes = _loss_ws(ws, R, V, code, dev, stream, always=True)
     _check(lib.dg_distill_loss_backward(x, code, R, V, ld, indices.data_ptr(), teacher.data_ptr(), K, ldk,
                                         _vec(teacher_lse, R, f32, dev, "teacher_lse"), temperature,
                                         _vec(lse, R, f32, dev, "lse"), _vec(tail_logp, R, f32, dev, "tail_logp"),
-                                        _vec(dloss, R, f32, dev, "dloss"), g, ldg, ws.data_ptr(), ws.numel(), _stream(stream)),
+                                        _vec(dloss, R, f32, dev, "dloss"), g, ldg, ws_ptr, ws_bytes,
+                                        _stream(stream)),
            "dg_distill_loss_backward")
     return out
 
@@ -797,22 +810,23 @@ def dg_policy_loss(logits: torch.Tensor, token: torch.Tensor, old_logp: torch.Te
     if grad and "grad" not in o:
         o["grad"] = _new_grad(logits, stream)
     g, ldg = _grad_like(o["grad"], logits) if "grad" in o else (None, 0)
-    ws = _loss_ws(ws, R, V, code, dev, stream)
+    ws, ws_ptr, ws_bytes = _loss_ws(ws, R, V, code, dev, stream)
     _check(lib.dg_policy_loss(x, code, R, V, ld, _vec(token, R, torch.int32, dev, "token"),
                               _vec(old_logp, R, f32, dev, "old_logp"), _vec(ref_logp, R, f32, dev, "ref_logp"),
                               _vec(advantage, R, f32, dev, "advantage"), temperature, clip_low, clip_high, kl_coef,
                               _vec(weight, R, f32, dev, "weight"), _vec(o["loss"], R, f32, dev, "loss"),
                               _vec(o["logp"], R, f32, dev, "logp"), _vec(o["lse"], R, f32, dev, "lse"),
                               _vec(o["kl"], R, f32, dev, "kl"), _vec(o["clipped"], R, torch.uint8, dev, "clipped"),
-                              _vec(o["dlogp"], R, f32, dev, "dlogp"), g, ldg, ws.data_ptr(), ws.numel(), _stream(stream)), "dg_policy_loss")
+                              _vec(o["dlogp"], R, f32, dev, "dlogp"), g, ldg, ws_ptr, ws_bytes, _stream(stream)),
+           "dg_policy_loss")
     return o
 
 
 def dg_preference_loss(logits: torch.Tensor, token: torch.Tensor, ref_logp: torch.Tensor | None,
                        seq_start: torch.Tensor, beta: float = 0.1, label_smoothing: float = 0.0,
                        temperature: float = 1.0, weight: torch.Tensor | None = None,
-                       pair_weight: torch.Tensor | None = None, grad: bool = False, ws: torch.Tensor | None = None, stream=None,
-                       out: dict | None = None) -> dict:
+                       pair_weight: torch.Tensor | None = None, grad: bool = False,
+                       ws: torch.Tensor | None = None, stream=None, out: dict | None = None) -> dict:
     """Preference loss on the log ratios of P pairs of packed sequences (rows [seq_start[j], seq_start[j+1]);
     pair i prefers sequence 2i over 2i + 1) -> dict loss [P], log_ratio [2P], logp, lse, dlogp [R] and, with
     grad=True or a `grad` in `out`, the logits' gradient of sum_i pair_weight_i loss_i."""
@@ -827,7 +841,7 @@ def dg_preference_loss(logits: torch.Tensor, token: torch.Tensor, ref_logp: torc
     if grad and "grad" not in o:
         o["grad"] = _new_grad(logits, stream)
     g, ldg = _grad_like(o["grad"], logits) if "grad" in o else (None, 0)
-    ws = _loss_ws(ws, R, V, code, dev, stream)
+    ws, ws_ptr, ws_bytes = _loss_ws(ws, R, V, code, dev, stream)
     _check(lib.dg_preference_loss(x, code, R, V, ld, _vec(token, R, torch.int32, dev, "token"),
                                   _vec(ref_logp, R, f32, dev, "ref_logp"),
                                   _vec(seq_start, n, torch.int32, dev, "seq_start"), P, beta, label_smoothing,
@@ -835,6 +849,6 @@ def dg_preference_loss(logits: torch.Tensor, token: torch.Tensor, ref_logp: torc
                                   _vec(pair_weight, P, f32, dev, "pair_weight"), _vec(o["loss"], P, f32, dev, "loss"),
                                   _vec(o["log_ratio"], 2 * P, f32, dev, "log_ratio"),
                                   _vec(o["logp"], R, f32, dev, "logp"), _vec(o["lse"], R, f32, dev, "lse"),
-                                  _vec(o["dlogp"], R, f32, dev, "dlogp"), g, ldg, ws.data_ptr(), ws.numel(), _stream(stream)),
+                                  _vec(o["dlogp"], R, f32, dev, "dlogp"), g, ldg, ws_ptr, ws_bytes, _stream(stream)),
            "dg_preference_loss")
     return o

@@ -49,8 +49,9 @@ dg_status check_grad(const char *what, const void *logits, int32_t dtype, int64_
     return DG_OK;
 }
 
-dg_status check_workspace(const char *what, int64_t R, int64_t V, int32_t dtype, const void *workspace,
+dg_status check_workspace(const char *what, int64_t R, int64_t V, int32_t dtype, bool always, const void *workspace,
                           size_t workspace_bytes) {
+    if (!always && row_is_one_tile(V, dtype)) return DG_OK;
     const size_t need = row_loss_workspace_bytes(R, V, dtype);
     if (!workspace || workspace_bytes < need)
         return fail(DG_ERR_INVALID_ARG, "%s: workspace of %zu bytes is below the %zu needed", what, workspace_bytes,
@@ -106,6 +107,10 @@ size_t dg_row_loss_workspace_size(int64_t R, int64_t V, int32_t dtype) {
     return row_loss_workspace_bytes(R, V, dtype);
 }
 
+int32_t dg_row_loss_needs_workspace(int64_t V, int32_t dtype) {
+    return V >= 1 && V <= 0x7ffffff0LL && (dtype == DG_F32 || dtype == DG_BF16) && !row_is_one_tile(V, dtype);
+}
+
 dg_status dg_row_topk(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl, int32_t K,
                       float temperature, float *values, int32_t *indices, int64_t ldk, float *lse, void *workspace,
                       size_t workspace_bytes, dg_stream_t stream) {
@@ -130,7 +135,8 @@ dg_status dg_row_topk(const void *logits, int32_t dtype, int64_t R, int64_t V, i
 }
 
 dg_status dg_token_logp(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl, const int32_t *token,
-                        float temperature, const float *weight, float *logp, float *lse, void *workspace, size_t workspace_bytes, dg_stream_t stream) {
+                        float temperature, const float *weight, float *logp, float *lse, void *workspace,
+                        size_t workspace_bytes, dg_stream_t stream) {
     t_last_error[0] = 0;
     const char *what = "token logp";
     dg_status st = check_rows(what, logits, dtype, R, V, ldl, temperature);
@@ -140,14 +146,15 @@ dg_status dg_token_logp(const void *logits, int32_t dtype, int64_t R, int64_t V,
     a.token = token;
     a.logp = logp;
     a.lse = lse;
-    st = check_workspace(what, R, V, dtype, workspace, workspace_bytes);
+    st = check_workspace(what, R, V, dtype, false, workspace, workspace_bytes);
     if (st != DG_OK) return st;
     return run(what, a, kHeadToken, kPassForward, workspace, stream);
 }
 
 dg_status dg_token_logp_backward(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
                                  const int32_t *token, float temperature, const float *lse, const float *dlogp,
-                                 const float *weight, void *grad, int64_t ldg, void *workspace, size_t workspace_bytes, dg_stream_t stream) {
+                                 const float *weight, void *grad, int64_t ldg, void *workspace,
+                                 size_t workspace_bytes, dg_stream_t stream) {
     t_last_error[0] = 0;
     const char *what = "token logp backward";
     dg_status st = check_rows(what, logits, dtype, R, V, ldl, temperature);
@@ -159,7 +166,7 @@ dg_status dg_token_logp_backward(const void *logits, int32_t dtype, int64_t R, i
     a.token = token;
     a.lse = const_cast<float *>(lse);
     a.dlogp = const_cast<float *>(dlogp);
-    st = check_workspace(what, R, V, dtype, workspace, workspace_bytes);
+    st = check_workspace(what, R, V, dtype, false, workspace, workspace_bytes);
     if (st != DG_OK) return st;
     return run(what, a, kHeadToken, kPassBackward, workspace, stream);
 }
@@ -167,7 +174,8 @@ dg_status dg_token_logp_backward(const void *logits, int32_t dtype, int64_t R, i
 dg_status dg_distill_loss(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
                           const int32_t *indices, const float *teacher, int32_t K, int64_t ldk,
                           const float *teacher_lse, float temperature, const float *weight, float *loss, float *lse,
-                          float *tail_logp, void *grad, int64_t ldg, void *workspace, size_t workspace_bytes, dg_stream_t stream) {
+                          float *tail_logp, void *grad, int64_t ldg, void *workspace, size_t workspace_bytes,
+                          dg_stream_t stream) {
     t_last_error[0] = 0;
     const char *what = "distill loss";
     dg_status st = check_rows(what, logits, dtype, R, V, ldl, temperature);
@@ -184,7 +192,7 @@ dg_status dg_distill_loss(const void *logits, int32_t dtype, int64_t R, int64_t 
     a.loss = loss;
     a.lse = lse;
     a.tail_logp = teacher_lse ? tail_logp : nullptr;
-    st = check_workspace(what, R, V, dtype, workspace, workspace_bytes);
+    st = check_workspace(what, R, V, dtype, false, workspace, workspace_bytes);
     if (st != DG_OK) return st;
     return run(what, a, kHeadDistill, grad ? kPassStep : kPassForward, workspace, stream);
 }
@@ -212,7 +220,7 @@ dg_status dg_distill_loss_backward(const void *logits, int32_t dtype, int64_t R,
     a.teacher_lse = teacher_lse;
     a.lse = const_cast<float *>(lse);
     a.tail_logp = const_cast<float *>(tail_logp);
-    st = check_workspace(what, R, V, dtype, workspace, workspace_bytes);
+    st = check_workspace(what, R, V, dtype, true, workspace, workspace_bytes);
     if (st != DG_OK) return st;
     return run(what, a, kHeadDistill, kPassBackward, workspace, stream);
 }
@@ -249,7 +257,7 @@ dg_status dg_policy_loss(const void *logits, int32_t dtype, int64_t R, int64_t V
     a.kl = kl;
     a.clipped = clipped;
     a.dlogp = dlogp;
-    st = check_workspace(what, R, V, dtype, workspace, workspace_bytes);
+    st = check_workspace(what, R, V, dtype, false, workspace, workspace_bytes);
     if (st != DG_OK) return st;
     return run(what, a, kHeadToken, grad ? kPassStep : kPassForward, workspace, stream);
 }
@@ -258,7 +266,8 @@ dg_status dg_preference_loss(const void *logits, int32_t dtype, int64_t R, int64
                              const int32_t *token, const float *ref_logp, const int32_t *seq_start, int32_t P,
                              float beta, float label_smoothing, float temperature, const float *weight,
                              const float *pair_weight, float *loss, float *log_ratio, float *logp, float *lse,
-                             float *dlogp, void *grad, int64_t ldg, void *workspace, size_t workspace_bytes, dg_stream_t stream) {
+                             float *dlogp, void *grad, int64_t ldg, void *workspace, size_t workspace_bytes,
+                             dg_stream_t stream) {
     t_last_error[0] = 0;
     const char *what = "preference loss";
     dg_status st = check_rows(what, logits, dtype, R, V, ldl, temperature);
@@ -276,7 +285,7 @@ dg_status dg_preference_loss(const void *logits, int32_t dtype, int64_t R, int64
     a.logp = logp;
     a.lse = lse;
     a.dlogp = dlogp;  // 0 in every row, then the pairs' rows
-    if (R > 0) st = check_workspace(what, R, V, dtype, workspace, workspace_bytes);
+    if (R > 0) st = check_workspace(what, R, V, dtype, false, workspace, workspace_bytes);
     if (R > 0 && st == DG_OK) st = run(what, a, kHeadToken, kPassForward, workspace, stream);
     if (st != DG_OK) return st;
     if (P > 0) {

@@ -958,6 +958,8 @@ size_t exchange_bytes(int64_t R, int64_t V, int dtype) {
 
 }  // namespace
 
+bool row_is_one_tile(int64_t V, int dtype) { return tile_row(V, dtype, 0).tiles == 1; }
+
 size_t row_loss_workspace_bytes(int64_t R, int64_t V, int dtype) {
     return exchange_bytes(R, V, dtype) + (size_t)R * 3 * sizeof(float);
 }

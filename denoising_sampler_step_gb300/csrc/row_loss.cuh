@@ -49,6 +49,9 @@ struct RowLossArgs {
 };
 
 size_t row_loss_workspace_bytes(int64_t R, int64_t V, int dtype);
+// Whether a row of V entries stays whole in one SM's shared memory: only the distillation's backward
+// pass needs the workspace then.
+bool row_is_one_tile(int64_t V, int dtype);
 cudaError_t launch_row_loss(const RowLossArgs &a, RowLossHead head, RowLossPass pass, void *workspace,
                             cudaStream_t stream);
 

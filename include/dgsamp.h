@@ -566,6 +566,12 @@ dg_status dg_sampler_loop_step_e4m3(const float *logits, int32_t n_req, int32_t 
  */
 size_t dg_row_loss_workspace_size(int64_t R, int64_t V, int32_t dtype);
 
+/*
+ * 1 where every loss call takes a workspace; 0 where a row stays whole in one SM's shared memory
+ * (up to 64 KiB) and only dg_distill_loss_backward does: the others ignore it then, NULL included.
+ */
+int32_t dg_row_loss_needs_workspace(int64_t V, int32_t dtype);
+
 /* Element type of logits and gradients. */
 typedef enum dg_dtype {
     DG_F32 = 0,
@@ -608,7 +614,8 @@ dg_status dg_token_logp(const void *logits, int32_t dtype, int64_t R, int64_t V,
  */
 dg_status dg_token_logp_backward(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
                                  const int32_t *token, float temperature, const float *lse, const float *dlogp,
-                                 const float *weight, void *grad, int64_t ldg, void *workspace, size_t workspace_bytes, dg_stream_t stream);
+                                 const float *weight, void *grad, int64_t ldg, void *workspace,
+                                 size_t workspace_bytes, dg_stream_t stream);
 
 /*
  * Distillation from a teacher's top logits: per row K indices and the teacher's logits there
@@ -634,8 +641,9 @@ dg_status dg_token_logp_backward(const void *logits, int32_t dtype, int64_t R, i
  */
 dg_status dg_distill_loss(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
                           const int32_t *indices, const float *teacher, int32_t K, int64_t ldk,
-                          const float *teacher_lse, float temperature, const float *weight, float *loss, float *lse,
-                          float *tail_logp, void *grad, int64_t ldg, void *workspace, size_t workspace_bytes, dg_stream_t stream);
+                          const float *teacher_lse, float temperature, const float *weight, float *loss,
+                          float *lse, float *tail_logp, void *grad, int64_t ldg, void *workspace,
+                          size_t workspace_bytes, dg_stream_t stream);
 dg_status dg_distill_loss_backward(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
                                    const int32_t *indices, const float *teacher, int32_t K, int64_t ldk,
                                    const float *teacher_lse, float temperature, const float *lse,
@@ -654,8 +662,8 @@ dg_status dg_distill_loss_backward(const void *logits, int32_t dtype, int64_t R,
  * Requires 0 <= clip_low <= 1, clip_high >= 0, kl_coef >= 0, all finite.
  */
 dg_status dg_policy_loss(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
-                         const int32_t *token, const float *old_logp, const float *ref_logp, const float *advantage,
-                         float temperature, float clip_low, float clip_high, float kl_coef, const float *weight,
+                         const int32_t *token, const float *old_logp, const float *ref_logp,
+                         const float *advantage, float temperature, float clip_low, float clip_high, float kl_coef, const float *weight,
                          float *loss, float *logp, float *lse, float *kl, uint8_t *clipped, float *dlogp,
                          void *grad, int64_t ldg, void *workspace, size_t workspace_bytes, dg_stream_t stream);
 
@@ -677,7 +685,8 @@ dg_status dg_preference_loss(const void *logits, int32_t dtype, int64_t R, int64
                              const int32_t *token, const float *ref_logp, const int32_t *seq_start, int32_t P,
                              float beta, float label_smoothing, float temperature, const float *weight,
                              const float *pair_weight, float *loss, float *log_ratio, float *logp, float *lse,
-                             float *dlogp, void *grad, int64_t ldg, void *workspace, size_t workspace_bytes, dg_stream_t stream);
+                             float *dlogp, void *grad, int64_t ldg, void *workspace, size_t workspace_bytes,
+                             dg_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -118,17 +118,22 @@ ROWS = [P, 0, 4, 100, 100]
 WS = [P, 1 << 30, None]    # workspace, its size, stream
 
 
-def calls(lib, rows, T=1.0, grad=BIG, ldg=100, K=5, ldk=5, ws=WS):
-    """Every call of this part on the same rows, by name."""
-    return {
-        "topk": lib.dg_row_topk(*rows, K, T, P, P, ldk, P, P, 1 << 30, None),
-        "logp": lib.dg_token_logp(*rows, P, T, None, P, P, *ws),
-        "logp_bwd": lib.dg_token_logp_backward(*rows, P, T, P, P, None, grad, ldg, *ws),
-        "distill": lib.dg_distill_loss(*rows, P, P, K, ldk, None, T, None, P, P, P, grad, ldg, *ws),
-        "distill_bwd": lib.dg_distill_loss_backward(*rows, P, P, K, ldk, None, T, P, None, None, grad, ldg, *ws),
-        "policy": lib.dg_policy_loss(*rows, P, P, P, P, T, 0.2, 0.2, 0.0, None, *([P] * 6), grad, ldg, *ws),
-        "pref": lib.dg_preference_loss(*rows, P, P, P, 1, 0.1, 0.0, T, None, None, *([P] * 5), grad, ldg, *ws),
+NAMES = ("topk", "logp", "logp_bwd", "distill", "distill_bwd", "policy", "pref")
+
+
+def calls(lib, rows, T=1.0, grad=BIG, ldg=100, K=5, ldk=5, ws=WS, names=NAMES):
+    """The named calls of this part on the same rows: status by name.  Only calls that must be refused are
+    made: the pointers are made up."""
+    f = {
+        "topk": lambda: lib.dg_row_topk(*rows, K, T, P, P, ldk, P, *ws),
+        "logp": lambda: lib.dg_token_logp(*rows, P, T, None, P, P, *ws),
+        "logp_bwd": lambda: lib.dg_token_logp_backward(*rows, P, T, P, P, None, grad, ldg, *ws),
+        "distill": lambda: lib.dg_distill_loss(*rows, P, P, K, ldk, None, T, None, P, P, P, grad, ldg, *ws),
+        "distill_bwd": lambda: lib.dg_distill_loss_backward(*rows, P, P, K, ldk, None, T, P, None, None, grad, ldg, *ws),
+        "policy": lambda: lib.dg_policy_loss(*rows, P, P, P, P, T, 0.2, 0.2, 0.0, None, *([P] * 6), grad, ldg, *ws),
+        "pref": lambda: lib.dg_preference_loss(*rows, P, P, P, 1, 0.1, 0.0, T, None, None, *([P] * 5), grad, ldg, *ws),
     }
+    return {n: f[n]() for n in names}
 
 
 @pytest.mark.parametrize("rows,status", [
@@ -162,9 +167,8 @@ def test_calls_refuse_bad_temperatures(lib, T):
     (ctypes.c_void_p(256 + 16), 100, 1),   # overlapping them
     (ctypes.c_void_p(256 + 1584), 100, 1), (BIG, 1 << 55, 2)])
 def test_calls_refuse_bad_gradients(lib, grad, ldg, status):
-    for name, st in calls(lib, ROWS, grad=grad, ldg=ldg).items():
-        if name not in ("topk", "logp"):
-            assert st == status, name
+    for name, st in calls(lib, ROWS, grad=grad, ldg=ldg, names=NAMES[2:]).items():
+        assert st == status, name
 
 
 def test_backward_calls_need_a_gradient_and_saved_values(lib):
@@ -181,9 +185,8 @@ def test_backward_calls_need_a_gradient_and_saved_values(lib):
 @pytest.mark.parametrize("K,ldk,status", [(0, 5, 1), (5, 4, 1), (1025, 1025, 2), (5, 1 << 33, 2)])
 def test_calls_refuse_bad_entry_tables(lib, K, ldk, status):
     rows = [P, 0, 4, 2000, 2000]
-    got = calls(lib, rows, ldg=2000, K=K, ldk=ldk)
-    for name in ("topk", "distill", "distill_bwd"):
-        assert got[name] == status, name
+    for name, st in calls(lib, rows, ldg=2000, K=K, ldk=ldk, names=("topk", "distill", "distill_bwd")).items():
+        assert st == status, name
 
 
 def test_topk_refuses_more_entries_than_columns_and_a_small_workspace(lib):
@@ -195,11 +198,21 @@ def test_topk_refuses_more_entries_than_columns_and_a_small_workspace(lib):
 
 
 def test_losses_refuse_a_small_or_unaligned_workspace(lib):
+    assert lib.dg_row_loss_workspace_size(4, 100, 2) == 0 and lib.dg_row_loss_workspace_size(0, 9, 0) == 0
+    bad = lambda need: ((None, 1 << 30, 1), (P, need - 1, 1), (Q, 1 << 30, 2))
+    need = lib.dg_row_loss_workspace_size(4, 20000, 0)
+    assert need > 0 and lib.dg_row_loss_needs_workspace(20000, 0) == 1
+    for ws, n, status in bad(need):
+        for name, st in calls(lib, [P, 0, 4, 20000, 20000], ldg=20000, ws=[ws, n, None], names=NAMES[1:]).items():
+            assert st == status, (name, st)
+    # rows of one tile take a workspace in one call only
     need = lib.dg_row_loss_workspace_size(4, 100, 0)
-    assert need > 0 and lib.dg_row_loss_workspace_size(4, 100, 2) == 0 and lib.dg_row_loss_workspace_size(0, 9, 0) == 0
-    for ws, n, status in ((None, 1 << 30, 1), (P, need - 1, 1), (Q, 1 << 30, 2)):
-        for name, st in calls(lib, ROWS, ws=[ws, n, None]).items():
-            assert name == "topk" or st == status, (name, st)
+    assert need > 0 and lib.dg_row_loss_needs_workspace(100, 0) == 0
+    for ws, n, status in bad(need):
+        assert lib.dg_distill_loss_backward(*ROWS, P, P, 5, 5, None, 1.0, P, None, None, BIG, 100, ws, n, None) == status
+    assert [lib.dg_row_loss_needs_workspace(16384 + 4 * i, 0) for i in (0, 1)] == [0, 1]
+    assert [lib.dg_row_loss_needs_workspace(32768 + 8 * i, 1) for i in (0, 1)] == [0, 1]
+    assert lib.dg_row_loss_needs_workspace(1 << 20, 2) == 0
 
 
 def test_policy_refuses_bad_coefficients(lib):
