@@ -6,6 +6,7 @@
 #include <float.h>
 
 #include "dg_common.cuh"
+#include "row_loss.cuh"
 
 namespace dg {
 namespace vocab {
@@ -48,7 +49,14 @@ __device__ __forceinline__ float finite_max(float m) { return fmaxf(m, -FLT_MAX)
 // the entries next to the maximum to rounding, and overflow where both are the type's lowest.
 __device__ __forceinline__ float exp_below(float x, float m, float c) { return ex2_approx((x - m) * c); }
 
-__device__ __forceinline__ void merge(MaxSum &a, const MaxSum &b, float c) {
+// With log2(e) / T as two floats (row_loss.cuh); what follows takes either.
+__device__ __forceinline__ float exp_below(float x, float m, const Scale &c) {
+    const float d = x - m;
+    return ex2_approx(fmaf(d, c.hi, d * c.lo));
+}
+
+template <typename C>
+__device__ __forceinline__ void merge(MaxSum &a, const MaxSum &b, const C &c) {
     const float m = fmaxf(a.m, b.m);
     const float f = finite_max(m);
     a.s = a.s * exp_below(a.m, f, c) + b.s * exp_below(b.m, f, c);
@@ -75,11 +83,29 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-// exp_below of both: the same two roundings, with minus_m = (-m, -m) and cc = (c, c).
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// exp_below of both: the same roundings, with minus_m = (-m, -m), and cc = (c, c) or hi and lo pairs.
+__device__ __forceinline__ f32x2 exp_below2(f32x2 x, f32x2 minus_m, f32x2 hi, f32x2 lo) {
+    const f32x2 d = add2(x, minus_m);
+    float a, b;
+    unpair(fma2(d, hi, mul2(d, lo)), a, b);
+    return pair(ex2_approx(a), ex2_approx(b));
+}
 __device__ __forceinline__ f32x2 exp_below2(f32x2 x, f32x2 minus_m, f32x2 cc) {
     float lo, hi;
     unpair(mul2(add2(x, minus_m), cc), lo, hi);
     return pair(ex2_approx(lo), ex2_approx(hi));
+}
+
+__device__ __forceinline__ f32x2 exp_below2(f32x2 x, f32x2 minus_m, float c) {
+    return exp_below2(x, minus_m, pair(c, c));
+}
+__device__ __forceinline__ f32x2 exp_below2(f32x2 x, f32x2 minus_m, const Scale &c) {
+    return exp_below2(x, minus_m, pair(c.hi, c.hi), pair(c.lo, c.lo));
 }
 
 // The largest of N values, and their sum, as trees: chains of N dependent operations would leave a
@@ -100,8 +126,8 @@ __device__ __forceinline__ float tree_sum(const float *x) {
 }
 
 // Folds N values into the state.
-template <int N>
-__device__ __forceinline__ void fold(MaxSum &st, const float (&x)[N], float c) {
+template <int N, typename C>
+__device__ __forceinline__ void fold(MaxSum &st, const float (&x)[N], const C &c) {
     const float bm = tree_max<N>(x);
     if (bm > st.m) {
         st.s *= exp_below(st.m, bm, c);
@@ -128,7 +154,8 @@ __device__ __forceinline__ float warp_max(float v) {
 
 // The 32 lanes' states as one, the same in every lane: the maximum first, so that each sum is
 // rescaled once.
-__device__ __forceinline__ MaxSum warp_merge(MaxSum st, float c) {
+template <typename C>
+__device__ __forceinline__ MaxSum warp_merge(MaxSum st, const C &c) {
     const float m = warp_max(st.m);
     return MaxSum{m, warp_sum(st.s * exp_below(st.m, finite_max(m), c))};
 }
@@ -207,15 +234,15 @@ struct Vec<__nv_bfloat16> {
 };
 
 // Folds K vectors into the state.
-template <typename T, int K>
-__device__ __forceinline__ void fold_vecs(MaxSum &st, const uint4 (&v)[K], float c) {
+template <typename T, int K, typename C>
+__device__ __forceinline__ void fold_vecs(MaxSum &st, const uint4 (&v)[K], const C &c) {
     const float bm = Vec<T>::largest(v);
     if (bm > st.m) {
         st.s *= exp_below(st.m, bm, c);
         st.m = bm;
     }
     const float f = -finite_max(st.m);
-    const f32x2 minus_m = pair(f, f), cc = pair(c, c);
+    const f32x2 minus_m = pair(f, f);
     constexpr int P = Vec<T>::N / 2;
     f32x2 sum[2] = {0, 0};
 #pragma unroll
@@ -223,7 +250,7 @@ __device__ __forceinline__ void fold_vecs(MaxSum &st, const uint4 (&v)[K], float
         f32x2 p[P];
         Vec<T>::pairs(v[i], p);
 #pragma unroll
-        for (int j = 0; j < P; ++j) sum[j & 1] = add2(sum[j & 1], exp_below2(p[j], minus_m, cc));
+        for (int j = 0; j < P; ++j) sum[j & 1] = add2(sum[j & 1], exp_below2(p[j], minus_m, c));
     }
     float a, b;
     unpair(add2(sum[0], sum[1]), a, b);
