@@ -814,8 +814,12 @@ bool layout(int64_t R, int64_t V, int K, int dtype, Layout *l) {
     // nor than 8 K entries
     const int64_t least = max((int64_t)kMinUnits, (8 * (int64_t)K + unit - 1) / unit);
     l->ctas = (int)max((int64_t)1, min((int64_t)sms * kPerSm, (units + least - 1) / least));
-    // Whole rows where that leaves no CTA more than a tenth above its part: the second kernel takes 5 us.
-    l->whole = (R + l->ctas - 1) / l->ctas * l->ctas * 10 <= R * 11;
+    // Whole rows, or shares as even as can be: what the longest share of whole rows has beyond an even one
+    // (and 64 KB more a row, what a row costs whatever its length), against the second kernel and the pieces
+    // that even shares add: as much as reading 120 KB.  1,000 x 50,001 bf16, K = 200: 57.0 us whole, 60.5 in
+    // even shares; 400 x 50,001 fp32, K = 64: 39.6 and 36.7.
+    const int64_t most = (R + l->ctas - 1) / l->ctas, row_bytes = per_row * kUnitBytes;
+    l->whole = (most * l->ctas - R) * (row_bytes + 64 * 1024) <= (int64_t)l->ctas * 120 * 1024;
     const int share = l->units / l->ctas;  // every CTA has at least this
     l->pieces = min((l->units_per_row + share - 1) / share + 1, l->units_per_row);
     return true;
