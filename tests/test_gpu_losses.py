@@ -570,6 +570,39 @@ def test_calls_run_on_the_given_stream_and_in_a_graph(B):
             assert torch.equal(a[name], b[name]), name
 
 
+def test_calls_on_two_streams_do_not_disturb_each_other(B):
+    """Kernels whose CTAs wait for one another, on streams that overlap, with a workspace each."""
+    torch.manual_seed(3)
+    V, K = 100003, 40
+    x = torch.randn(300, 100004, device="cuda")[:, :V]
+    top = B.dg_row_topk(x, K, lse=True)
+    tok = torch.randint(0, V, (300,), device="cuda", dtype=torch.int32)
+    adv = torch.randn(300, device="cuda")
+    old = B.dg_token_logp(x, tok)["logp"] - 0.1
+
+    def all_calls(ws, wk):
+        d = B.dg_distill_loss(x, top["indices"], top["values"], top["lse"], temperature=1.5, grad=True, ws=ws)
+        p = B.dg_policy_loss(x, tok, old, adv, grad=True, ws=ws)
+        f = B.dg_token_logp(x, tok, temperature=0.8, ws=ws)
+        t = B.dg_row_topk(x, K, lse=True, ws=wk)
+        return [*d.values(), *p.values(), *f.values(), *t.values()]
+
+    spaces = [(B.loss_workspace(300, V, x.device), B.topk_workspace(300, V, K, x.device)) for _ in range(2)]
+    want = all_calls(*spaces[0])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    torch.cuda.synchronize()
+    for rep in range(6):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(all_calls(*spaces[i]))
+    torch.cuda.synchronize()
+    B.dg_get_device_status()
+    for runs in got:
+        for r in runs:
+            assert all(torch.equal(a, b) for a, b in zip(r, want))
+
+
 def test_directional_differences(B):
     """The forward call's losses along a direction against the gradient call: (f(x + hu) - f(x - hu)) / 2h
     with h = 2^-6: truncation h^2 / 6 of third derivatives below 1 per unit of sum |u|^3 p, rounding
