@@ -85,8 +85,8 @@ RowLossArgs row_args(const void *logits, int32_t dtype, int64_t R, int64_t V, in
 }
 
 dg_status run(const char *what, const RowLossArgs &a, RowLossHead head, RowLossPass pass, void *workspace,
-              dg_stream_t stream) {
-    const cudaError_t e = launch_row_loss(a, head, pass, workspace, (cudaStream_t)stream);
+              dg_stream_t stream, bool chained = false) {
+    const cudaError_t e = launch_row_loss(a, head, pass, workspace, (cudaStream_t)stream, chained);
     return e == cudaSuccess ? DG_OK : cuda_fail(e, what);
 }
 
@@ -298,7 +298,7 @@ dg_status dg_preference_loss(const void *logits, int32_t dtype, int64_t R, int64
     a.weight = nullptr;  // dlogp holds it
     a.grad = grad;
     a.ldg = ldg;
-    return run(what, a, kHeadToken, kPassBackward, workspace, stream);
+    return run(what, a, kHeadToken, kPassBackward, workspace, stream, P > 0);
 }
 
 }  // extern "C"

@@ -276,6 +276,8 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
     }
     __syncthreads();
 
+    if (kForward) grid_launch_dependents();
+
     // A wait that gives up (a second without what it waits for) raises the abort flag and the device
     // error word; every role then leaves at its next wait.
     auto wait = [&](uint64_t &bar, uint32_t parity) { return ring_wait(smem_u32(&bar), parity & 1, &sh.abort_flag); };
@@ -332,6 +334,7 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
                 ++lap;
             }
         };
+        if (!kForward) grid_dependency_wait();  // on what the kernel before it computes
         if (row < a.R) fetch(row);
 #pragma unroll 1
         while (row < a.R && ok) {
@@ -797,6 +800,7 @@ constexpr int kCloseWarps = 8;
 __global__ void __launch_bounds__(32 * kCloseWarps) row_close_kernel(const RowLossArgs a, RowClose *rows) {
     const int64_t row = (int64_t)blockIdx.x * kCloseWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
+    grid_launch_dependents();
     if (row >= a.R) return;
     const float w = a.weight ? a.weight[row] : 1.0f, c = kLog2e / a.T;
     if (w == 0.0f) return;
@@ -823,6 +827,8 @@ __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(PairLossArgs a)
     __shared__ double slots[kPairWarps];
     __shared__ double seq_sum[2];
     const int pair = blockIdx.x, tid = threadIdx.x;
+    grid_launch_dependents();
+    grid_dependency_wait();
     int64_t begin[2], end[2];
 #pragma unroll 1
     for (int j = 0; j < 2; ++j) {
@@ -931,7 +937,8 @@ cudaError_t allow_shared(const void *fn, int index) {
     return e;
 }
 
-cudaError_t launch_pass(RowLossArgs a, RowLossHead head, RowLossPass pass, void *workspace,
+// chained: the kernel before it on the stream is one of this file's, which lets this one start early.
+cudaError_t launch_pass(RowLossArgs a, bool chained, RowLossHead head, RowLossPass pass, void *workspace,
                         cudaStream_t stream) {
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorNoDevice;
@@ -966,12 +973,16 @@ cudaError_t launch_pass(RowLossArgs a, RowLossHead head, RowLossPass pass, void 
     cfg.blockDim = dim3((unsigned)k.threads);
     cfg.dynamicSmemBytes = (size_t)stages * stage;
     cfg.stream = stream;
-    // CTAs that exchange sums must all be running
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeCooperative;
-    attr[0].val.cooperative = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pass != kPassBackward && split ? 1 : 0;
+    if (pass != kPassBackward && split) {
+        // CTAs that exchange sums must all be running
+        attr[cfg.numAttrs].id = cudaLaunchAttributeCooperative;
+        attr[cfg.numAttrs++].val.cooperative = 1;
+    } else if (pass == kPassBackward && (chained || head == kHeadDistill)) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
     void *args[2] = {&a, &plan};
     return cudaLaunchKernelExC(&cfg, k.fn, args);
 }
@@ -992,7 +1003,7 @@ size_t row_loss_workspace_bytes(int64_t R, int64_t V, int dtype) {
 }
 
 cudaError_t launch_row_loss(const RowLossArgs &a, RowLossHead head, RowLossPass pass, void *workspace,
-                            cudaStream_t stream) {
+                            cudaStream_t stream, bool chained) {
     const Tiling tl = tile_row(a.V, a.dtype, head == kHeadDistill ? a.K : 0);
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorNoDevice;
@@ -1001,22 +1012,31 @@ cudaError_t launch_row_loss(const RowLossArgs &a, RowLossHead head, RowLossPass 
     // A step keeps a row's tiles in the rings until the row is complete: a CTA must have room for its
     // share of one row and the next.  Longer rows are read twice.
     const int64_t grid = a.R * tl.tiles < sms ? a.R * tl.tiles : sms;
-    if (pass != kPassStep || (tl.tiles + grid - 1) / grid + 2 <= stages) return launch_pass(a, head, pass, workspace, stream);
+    if (pass != kPassStep || (tl.tiles + grid - 1) / grid + 2 <= stages) 
+        return launch_pass(a, chained, head, pass, workspace, stream);
     RowLossArgs f = a;
     float *saved = reinterpret_cast<float *>(static_cast<char *>(workspace) + exchange_bytes(a.R, a.V, a.dtype));
     if (!f.lse) f.lse = saved;
     if (!f.dlogp) f.dlogp = saved + a.R;
     if (a.teacher_lse && !f.tail_logp) f.tail_logp = saved + 2 * a.R;
     f.grad = nullptr;
-    const cudaError_t e = launch_pass(f, head, kPassForward, workspace, stream);
+    const cudaError_t e = launch_pass(f, false, head, kPassForward, workspace, stream);
     if (e != cudaSuccess) return e;
     f.grad = a.grad;
-    return launch_pass(f, head, kPassBackward, workspace, stream);
+    return launch_pass(f, true, head, kPassBackward, workspace, stream);
 }
 
 cudaError_t launch_pair_loss(const PairLossArgs &a, cudaStream_t stream) {
-    pair_loss_kernel<<<(unsigned)a.P, kPairThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.P);
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, pair_loss_kernel, a);
 }
 
 }  // namespace dg

@@ -75,8 +75,9 @@ size_t row_loss_workspace_bytes(int64_t R, int64_t V, int dtype);
 // Whether a row of V entries stays whole in one SM's shared memory: only the distillation's backward
 // pass needs the workspace then.
 bool row_is_one_tile(int64_t V, int dtype);
+// chained: the kernel before it on the stream is one of row_loss.cu's.
 cudaError_t launch_row_loss(const RowLossArgs &a, RowLossHead head, RowLossPass pass, void *workspace,
-                            cudaStream_t stream);
+                            cudaStream_t stream, bool chained = false);
 
 // Preference loss of P pairs from the rows' log-probabilities: losses, log ratios, dlogp.
 struct PairLossArgs {
