@@ -56,6 +56,10 @@ constexpr int kBuffer = 2560;                 // candidates
 constexpr int kMinUnits = 4;
 constexpr int kMergeThreads = 256, kMergeBuffer = 4096;
 constexpr int kRanked = 256;                  // most candidates ordered by counting
+// Most that the finishing warp puts in order beside the next row; more would keep the others waiting for
+// it.  By the finishing and by the filtering warps: 1,000 x 50,001 fp32, K = 300, 126 and 138 us; 2,048 x
+// 8,000 fp32, K = 400, 161 and 116; 256 x 262,144 bf16, K = 1,024, 133 and 98.
+constexpr int kFew = 384;
 
 // Candidates beyond K that a cut may leave (each less costs it another look at them).
 __host__ __device__ constexpr int cut_slack(int K) { return K / 8 + 16; }
@@ -362,6 +366,22 @@ __device__ __forceinline__ float row_lse(const MaxSum &st, float T) {
     return st.m == -INFINITY ? __int_as_float(0x7fc00000) : st.m / T + logf(st.s);
 }
 
+// The K > kFew largest of the n entries of a whole row, from the largest down, to the row's outputs.
+// THREADS threads.
+template <int THREADS>
+__device__ __noinline__ void write_many(Select &se, uint64_t *buf, uint32_t *count, int n, const RowTopKArgs &a,
+                                        int row) {
+    const int tid = threadIdx.x % THREADS, n2 = places(a.K);
+    if (n > n2) {
+        keep<THREADS>(se, buf, count, n, edge_of<THREADS>(se, buf, n, a.K, n2 - a.K));
+        n = (int)*(volatile uint32_t *)count;
+    }
+    for (int i = n + tid; i < n2; i += THREADS) buf[i] = 0;
+    sync<THREADS>();
+    sort_entries(buf, n2, tid, THREADS, []() { sync<THREADS>(); });
+    for (int k = tid; k < a.K; k += THREADS) write_entry(a, row, k, buf[k]);
+}
+
 struct Shared {
     uint64_t buf[kBuffers][kBuffer];
     uint32_t hist[kFinish][256];  // the finishing warps'
@@ -382,7 +402,8 @@ struct Roles {
                          loader = finish + kFinish, kAll = 32 * (loader + 1);
 };
 
-template <typename T, bool LSE>
+// MANY: K > kFew, and the filtering warps put a whole row's candidates in order.
+template <typename T, bool LSE, bool MANY>
 __global__ void __launch_bounds__(Roles<LSE>::kAll, kPerSm)
     topk_pieces_kernel(const RowTopKArgs a, const Layout lay, void *ws) {
     using W = Roles<LSE>;
@@ -645,6 +666,11 @@ __global__ void __launch_bounds__(Roles<LSE>::kAll, kPerSm)
                 if (__any_sync(0xffffffffu, crowded())) meet(true);
             }
             while (meet(false)) {}
+            if (MANY && n == lay.units_per_row) {
+                const int got = min((int)*(volatile uint32_t *)count, kBuffer);
+                sync<kThreads>();  // every thread has read the count
+                write_many<kThreads>(sh.sel, sh.buf[b], count, got, a, row);
+            }
             arrive(sh.given[b]);
         }
     } else if (LSE && warp < W::finish) {
@@ -692,7 +718,7 @@ __global__ void __launch_bounds__(Roles<LSE>::kAll, kPerSm)
             uint64_t *buf = sh.buf[b];
             int n = min((int)sh.count[b], kBuffer);
             const bool whole = units == lay.units_per_row;
-            const int n2 = places(a.K), most = whole ? n2 : a.K + slack;
+            const int n2 = places(a.K), most = !whole ? a.K + slack : MANY ? kBuffer : n2;
             if (n > most) n = cut_warp(sh.hist[me], buf, n, a.K, most - a.K, sh.reached[b]);
             if (!whole) {
                 const int piece = (int)blockIdx.x - share_of(lay, row * lay.units_per_row);
@@ -703,7 +729,7 @@ __global__ void __launch_bounds__(Roles<LSE>::kAll, kPerSm)
                     if (lane == 0) *piece_state(ws, lay, row, piece) = st;
                 }
             } else {
-                if (n2 <= 256) {
+                if (!MANY && n2 <= kRanked) {
                     uint64_t r[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) r[i] = 8 * lane + i < n ? buf[8 * lane + i] : 0;
@@ -711,7 +737,7 @@ __global__ void __launch_bounds__(Roles<LSE>::kAll, kPerSm)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         if (8 * lane + i < a.K) write_entry(a, row, 8 * lane + i, r[i]);
-                } else {
+                } else if (!MANY) {
                     for (int i = n + lane; i < n2; i += 32) buf[i] = 0;
                     __syncwarp();
                     sort_entries(buf, n2, lane, 32, []() { __syncwarp(); });
@@ -825,9 +851,9 @@ bool layout(int64_t R, int64_t V, int K, int dtype, Layout *l) {
     return true;
 }
 
-template <typename T, bool LSE>
+template <typename T, bool LSE, bool MANY>
 cudaError_t launch(const RowTopKArgs &a, const Layout &lay, void *ws, cudaStream_t stream) {
-    const void *fn = (const void *)topk_pieces_kernel<T, LSE>;
+    const void *fn = (const void *)topk_pieces_kernel<T, LSE, MANY>;
     constexpr int kMaxDevices = 64;
     static std::atomic<int> attr_set[kMaxDevices];
     int dev = 0;
@@ -838,7 +864,7 @@ cudaError_t launch(const RowTopKArgs &a, const Layout &lay, void *ws, cudaStream
         if (e != cudaSuccess) return e;
         if (dev < kMaxDevices) attr_set[dev].store(1, std::memory_order_release);
     }
-    topk_pieces_kernel<T, LSE><<<(unsigned)lay.ctas, Roles<LSE>::kAll, kDynamic, stream>>>(a, lay, ws);
+    topk_pieces_kernel<T, LSE, MANY><<<(unsigned)lay.ctas, Roles<LSE>::kAll, kDynamic, stream>>>(a, lay, ws);
     e = cudaGetLastError();
     // no row is shared where every CTA's share is whole rows
     if (e != cudaSuccess || lay.whole || lay.ctas == 1) return e;
@@ -852,6 +878,11 @@ cudaError_t launch(const RowTopKArgs &a, const Layout &lay, void *ws, cudaStream
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, topk_merge_kernel<LSE>, a, lay, ws);
+}
+
+template <typename T, bool LSE>
+cudaError_t launch(const RowTopKArgs &a, const Layout &lay, void *ws, cudaStream_t stream) {
+    return a.K > kFew ? launch<T, LSE, true>(a, lay, ws, stream) : launch<T, LSE, false>(a, lay, ws, stream);
 }
 
 }  // namespace
