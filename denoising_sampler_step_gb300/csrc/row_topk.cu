@@ -837,9 +837,10 @@ bool layout(int64_t R, int64_t V, int K, int dtype, Layout *l) {
     l->units_per_row = (int)per_row;
     l->units = (int)units;
     // a piece of a row costs a selection and K candidates to merge: no fewer than kMinUnits units,
-    // nor than 8 K entries
+    // nor than 8 K entries (but a row is never too little for a CTA)
     const int64_t least = max((int64_t)kMinUnits, (8 * (int64_t)K + unit - 1) / unit);
-    l->ctas = (int)max((int64_t)1, min((int64_t)sms * kPerSm, (units + least - 1) / least));
+    const int64_t want = max((units + least - 1) / least, R);
+    l->ctas = (int)max((int64_t)1, min((int64_t)sms * kPerSm, want));
     // Whole rows, or shares as even as can be: what the longest share of whole rows has beyond an even one
     // (and 64 KB more a row, what a row costs whatever its length), against the second kernel and the pieces
     // that even shares add: as much as reading 120 KB.  1,000 x 50,001 bf16, K = 200: 57.0 us whole, 60.5 in
