@@ -284,7 +284,8 @@ dg_status dg_preference_loss(const void *logits, int32_t dtype, int64_t R, int64
     a.token = token;
     a.logp = logp;
     a.lse = lse;
-    a.dlogp = dlogp;  // 0 in every row, then the pairs' rows
+    a.dlogp = dlogp;
+    a.keep_low = P > 0;  // until the pairs' kernel has added it up; without pairs 0
     if (R > 0) st = check_workspace(what, R, V, dtype, false, workspace, workspace_bytes);
     if (R > 0 && st == DG_OK) st = run(what, a, kHeadToken, kPassForward, workspace, stream);
     if (st != DG_OK) return st;

@@ -218,16 +218,26 @@ __device__ __forceinline__ unsigned long long poll_sum(const unsigned long long 
     }
 }
 
-// d - ln s.  The hardware's power of two is 5e-8 too small on average, and so is s but for its largest
-// term, 1, which is exact: little in a row, but the same in every row of a sequence.  The share is added
-// to what the difference rounds off.  (With log2(e) / T as one float nothing is added: its rounding is the
-// other way.  The mean error of ln p over 4,000 rows is 3e-8 at T = 1, below 5e-8 at others; without this
-// and the two floats up to 5e-7.)
+// (x - m) / T - ln s to the nearest float, and in *low what that leaves: a pair's sums, differences from a
+// reference's log-probabilities, are small beside them.  What each operation rounds off is exact in fp32.
+// The hardware's power of two is 5e-8 too small on average, and so is s but for its largest term, 1,
+// which is exact: little in a row, but the same in every row of a sequence, so the share is put back.  (With
+// log2(e) / T as one float it is not: its rounding is the other way.  The mean error of ln p over 4,000
+// rows is 3e-8 at T = 1, below 5e-8 at others; without this and the two floats up to 5e-7.)
 template <bool TWO>
-__device__ __forceinline__ float less_log_sum(float d, float lns, float inv_s) {
-    const float r = d - lns;
-    if (!TWO || !(fabsf(r) < INFINITY)) return r;
-    return r + (((d - r) - lns) - 5e-8f * (1.0f - inv_s));
+__device__ __forceinline__ float log_prob(float x, float m, float T, float lns, float inv_s, float *low) {
+    auto lost = [](float a, float b, float sum) {  // of sum = a + b
+        const float bb = sum - a;
+        return (a - (sum - bb)) + (b - bb);
+    };
+    const float d = x - m, q = d / T, r = q - lns;
+    *low = 0.0f;
+    if (!(fabsf(r) < INFINITY)) return r;
+    const float e = lost(q, -lns, r) + (fmaf(-q, T, d) + lost(x, -m, d)) / T -
+                    (TWO ? 5e-8f * (1.0f - inv_s) : 0.0f);
+    const float p = r + e;
+    *low = e - (p - r);
+    return p;
 }
 
 template <bool TWO>
@@ -569,9 +579,10 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
             bool clipped = false;
             // (little before the row is published: the other CTAs wait)
             if (HEAD == kHeadToken) {
-                // (a product with 1 / T would be off by the same share in every row, and a sequence's sum by
-                // as much)
-                logp = less_log_sum<TWO>((x_tok - m) / a.T, lns, cl.inv_s);
+                // (divided by T: a product with 1 / T would be off by the same share in every row)
+                float low;
+                logp = log_prob<TWO>(x_tok, m, a.T, lns, cl.inv_s, &low);
+                if (a.keep_low) dlogp = low;
                 if (a.policy) {
                     const float ratio = exp_fast(logp - old);
                     const float raw = ratio * A;
@@ -821,8 +832,8 @@ __global__ void __launch_bounds__(32 * kCloseWarps) row_close_kernel(const RowLo
 constexpr int kPairThreads = 256, kPairWarps = kPairThreads / 32;
 
 // One CTA per pair: each sequence's sum of weighted log ratios (fp64, so that a long sequence's
-// sum does not lose what the pair's difference is made of), the pair's loss, and the derivative of
-// every row's log-probability.
+// sum does not lose what the pair's difference is made of; dlogp holds the log-probabilities' low parts
+// until then), the pair's loss, and the derivative of every row's log-probability.
 __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(PairLossArgs a) {
     __shared__ double slots[kPairWarps];
     __shared__ double seq_sum[2];
@@ -839,7 +850,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(PairLossArgs a)
         for (int64_t r = begin[j] + tid; r < end[j]; r += kPairThreads) {
             const float w = a.weight ? a.weight[r] : 1.0f;
             if (w != 0.0f && a.token[r] >= 0 && a.token[r] < a.V)
-                v += (double)w * ((double)a.logp[r] - (a.ref_logp ? (double)a.ref_logp[r] : 0.0));
+                v += (double)w * ((double)a.logp[r] + (double)a.dlogp[r] - (a.ref_logp ? (double)a.ref_logp[r] : 0.0));
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -867,6 +878,11 @@ __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(PairLossArgs a)
             a.log_ratio[2 * pair + 1] = (float)seq_sum[1];
         }
     }
+    // the rows before the first sequence and behind the last
+#pragma unroll 1
+    for (int64_t r = tid; pair == 0 && r < begin[0]; r += kPairThreads) a.dlogp[r] = 0.0f;
+#pragma unroll 1
+    for (int64_t r = end[1] + tid; pair == a.P - 1 && r < a.R; r += kPairThreads) a.dlogp[r] = 0.0f;
 #pragma unroll 1
     for (int j = 0; j < 2; ++j) {
         const float d = pw == 0.0f ? 0.0f : (j == 0 ? a.beta : -a.beta) * dz * pw;

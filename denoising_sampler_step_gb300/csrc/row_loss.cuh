@@ -57,6 +57,7 @@ struct RowLossArgs {
     // kHeadToken
     const int32_t *token;    // [R]; a negative token leaves the row out like weight 0
     bool policy;             // the clipped policy loss; else the log-probability alone
+    bool keep_low;           // and then dlogp is what the log-probability's rounding left
     const float *old_logp, *ref_logp, *advantage;
     float clip_low, clip_high, kl_coef;
     float *logp, *kl;
