@@ -16,7 +16,7 @@
 //
 // Measured, 1,024 rows of 262,144 entries, against a plain copy's 6,780 GB/s: policy loss fp32 forward
 // 101%, step 89%, backward 97%; bf16 82%, 85%, 89%; distillation, K = 64, fp32 94%, 88%, 94%, bf16 74%,
-// 82%, 91%; a step with K = 512 75%, with K = 1,024 60% (each tile's share of the teacher's entries is
+// 82%, 91%; a step with K = 512 77%, with K = 1,024 64% (each tile's share of the teacher's entries is
 // found by looking at all of them).  What is left in a step: reads and writes that alternate, and in bf16
 // the folding warps, which have twice the entries per byte.
 //
@@ -53,8 +53,15 @@ namespace {
 using namespace vocab;
 
 constexpr int kMaxStages = 16;
-constexpr int kMaxTile = 64 * 1024;  // bytes of a row that is one tile
-constexpr int kGoodStages = 7;       // that the tiles of longer rows leave room for
+// Bytes of a row that is one tile: with 32 KB, so two tiles and an exchange, a policy step of 2,048 x 12,000
+// fp32 entries takes 43.7 us instead of 35.1.
+constexpr int kMaxTile = 64 * 1024;
+// Stages that the tiles of longer rows leave room for.  1,024 x 262,144, policy step fp32 and distillation
+// step (K = 64) bf16, us: 5 stages 360 and 194, 7 stages 353 and 197, 9 (tiles of 24 KB) 356 and 217, 14 356
+// and 239.  A long list of a teacher's entries is looked through once per tile: K = 512, fp32, 5 stages 412,
+// 7 stages 423; K = 1,024 493 and 534.
+constexpr int kFewEntries = 256;
+constexpr int good_stages(int K) { return K > kFewEntries ? 5 : 7; }
 constexpr int kMinTile = 24 * 1024;
 // Below this ln p_0 the bucket's probability is no normal fp32 number and its term is left out.
 constexpr float kTailFloor = -87.0f;
@@ -911,8 +918,9 @@ struct Tiling {
 Tiling tile_row(int64_t V, int dtype, int K) {
     const int64_t nv = V / (dtype == DG_BF16 ? 8 : 4);
     if (nv * 16 <= kMaxTile) return Tiling{(int)((nv + 7) / 8 * 8 > 0 ? (nv + 7) / 8 * 8 : 8), 1};
-    int most = kDynamicBytes / kGoodStages - K * kListBytes;
-    if (most < kMinTile) most = kDynamicBytes / (kGoodStages - 1) - K * kListBytes;
+    const int stages = good_stages(K);
+    int most = kDynamicBytes / stages - K * kListBytes;
+    if (most < kMinTile) most = kDynamicBytes / (stages - 1) - K * kListBytes;
     const int64_t limit = most / 128 * 8;  // vectors
     const int64_t n = (nv + limit - 1) / limit;
     const int64_t per = ((nv + n - 1) / n + 7) / 8 * 8;
@@ -1006,10 +1014,11 @@ cudaError_t launch_pass(RowLossArgs a, bool chained, RowLossHead head, RowLossPa
     return cudaLaunchKernelExC(&cfg, k.fn, args);
 }
 
-// The workspace: the rows' numbers, their sums (the shortest tiles are those of the longest lists),
-// then three floats per row for a step in two passes.
+// The workspace: the rows' numbers, their sums (the shortest tiles are those of the longest lists, with
+// either number of stages), then three floats per row for a step in two passes.
 size_t exchange_bytes(int64_t R, int64_t V, int dtype) {
-    const int tiles = tile_row(V, dtype, kMaxTopK).tiles;
+    const int few = tile_row(V, dtype, kFewEntries).tiles, many = tile_row(V, dtype, kMaxTopK).tiles;
+    const int tiles = few > many ? few : many;
     return (size_t)R * (sizeof(RowClose) + 8 * (size_t)tiles);
 }
 
