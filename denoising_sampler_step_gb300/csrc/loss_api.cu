@@ -14,8 +14,6 @@ namespace {
 // R * ld stays below this, so that offsets in bytes fit 64 bits.
 constexpr int64_t kMaxElements = 1LL << 56;
 
-int64_t element_size(int32_t dtype) { return dtype == DG_BF16 ? 2 : 4; }
-
 // The rules every call of this part has in common.
 dg_status check_rows(const char *what, const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
                      float temperature) {
@@ -49,10 +47,10 @@ dg_status check_grad(const char *what, const void *logits, int32_t dtype, int64_
     return DG_OK;
 }
 
-dg_status check_workspace(const char *what, int64_t R, int64_t V, int32_t dtype, bool always, const void *workspace,
-                          size_t workspace_bytes) {
-    if (!always && row_is_one_tile(V, dtype)) return DG_OK;
-    const size_t need = row_loss_workspace_bytes(R, V, dtype);
+dg_status check_workspace(const char *what, const RowLossArgs &a, RowLossHead head, RowLossPass pass,
+                          const void *workspace, size_t workspace_bytes) {
+    if (!takes_workspace(a.V, element_size(a.dtype), head, pass)) return DG_OK;
+    const size_t need = row_loss_workspace_bytes(a.R, a.V, a.dtype);
     if (!workspace || workspace_bytes < need)
         return fail(DG_ERR_INVALID_ARG, "%s: workspace of %zu bytes is below the %zu needed", what, workspace_bytes,
                     need);
@@ -85,7 +83,9 @@ RowLossArgs row_args(const void *logits, int32_t dtype, int64_t R, int64_t V, in
 }
 
 dg_status run(const char *what, const RowLossArgs &a, RowLossHead head, RowLossPass pass, void *workspace,
-              dg_stream_t stream, bool chained = false) {
+              size_t workspace_bytes, dg_stream_t stream, bool chained = false) {
+    const dg_status st = check_workspace(what, a, head, pass, workspace, workspace_bytes);
+    if (st != DG_OK) return st;
     const cudaError_t e = launch_row_loss(a, head, pass, workspace, (cudaStream_t)stream, chained);
     return e == cudaSuccess ? DG_OK : cuda_fail(e, what);
 }
@@ -108,7 +108,8 @@ size_t dg_row_loss_workspace_size(int64_t R, int64_t V, int32_t dtype) {
 }
 
 int32_t dg_row_loss_needs_workspace(int64_t V, int32_t dtype) {
-    return V >= 1 && V <= 0x7ffffff0LL && (dtype == DG_F32 || dtype == DG_BF16) && !row_is_one_tile(V, dtype);
+    return V >= 1 && V <= 0x7ffffff0LL && (dtype == DG_F32 || dtype == DG_BF16) &&
+           takes_workspace(V, element_size(dtype), kHeadToken, kPassForward);
 }
 
 dg_status dg_row_topk(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl, int32_t K,
@@ -146,9 +147,7 @@ dg_status dg_token_logp(const void *logits, int32_t dtype, int64_t R, int64_t V,
     a.token = token;
     a.logp = logp;
     a.lse = lse;
-    st = check_workspace(what, R, V, dtype, false, workspace, workspace_bytes);
-    if (st != DG_OK) return st;
-    return run(what, a, kHeadToken, kPassForward, workspace, stream);
+    return run(what, a, kHeadToken, kPassForward, workspace, workspace_bytes, stream);
 }
 
 dg_status dg_token_logp_backward(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
@@ -166,9 +165,7 @@ dg_status dg_token_logp_backward(const void *logits, int32_t dtype, int64_t R, i
     a.token = token;
     a.lse = const_cast<float *>(lse);
     a.dlogp = const_cast<float *>(dlogp);
-    st = check_workspace(what, R, V, dtype, false, workspace, workspace_bytes);
-    if (st != DG_OK) return st;
-    return run(what, a, kHeadToken, kPassBackward, workspace, stream);
+    return run(what, a, kHeadToken, kPassBackward, workspace, workspace_bytes, stream);
 }
 
 dg_status dg_distill_loss(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
@@ -192,9 +189,7 @@ dg_status dg_distill_loss(const void *logits, int32_t dtype, int64_t R, int64_t 
     a.loss = loss;
     a.lse = lse;
     a.tail_logp = teacher_lse ? tail_logp : nullptr;
-    st = check_workspace(what, R, V, dtype, false, workspace, workspace_bytes);
-    if (st != DG_OK) return st;
-    return run(what, a, kHeadDistill, grad ? kPassStep : kPassForward, workspace, stream);
+    return run(what, a, kHeadDistill, grad ? kPassStep : kPassForward, workspace, workspace_bytes, stream);
 }
 
 dg_status dg_distill_loss_backward(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
@@ -220,9 +215,7 @@ dg_status dg_distill_loss_backward(const void *logits, int32_t dtype, int64_t R,
     a.teacher_lse = teacher_lse;
     a.lse = const_cast<float *>(lse);
     a.tail_logp = const_cast<float *>(tail_logp);
-    st = check_workspace(what, R, V, dtype, true, workspace, workspace_bytes);
-    if (st != DG_OK) return st;
-    return run(what, a, kHeadDistill, kPassBackward, workspace, stream);
+    return run(what, a, kHeadDistill, kPassBackward, workspace, workspace_bytes, stream);
 }
 
 dg_status dg_policy_loss(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl, const int32_t *token,
@@ -257,9 +250,7 @@ dg_status dg_policy_loss(const void *logits, int32_t dtype, int64_t R, int64_t V
     a.kl = kl;
     a.clipped = clipped;
     a.dlogp = dlogp;
-    st = check_workspace(what, R, V, dtype, false, workspace, workspace_bytes);
-    if (st != DG_OK) return st;
-    return run(what, a, kHeadToken, grad ? kPassStep : kPassForward, workspace, stream);
+    return run(what, a, kHeadToken, grad ? kPassStep : kPassForward, workspace, workspace_bytes, stream);
 }
 
 dg_status dg_preference_loss(const void *logits, int32_t dtype, int64_t R, int64_t V, int64_t ldl,
@@ -286,8 +277,7 @@ dg_status dg_preference_loss(const void *logits, int32_t dtype, int64_t R, int64
     a.lse = lse;
     a.dlogp = dlogp;
     a.keep_low = P > 0;  // until the pairs' kernel has added it up; without pairs 0
-    if (R > 0) st = check_workspace(what, R, V, dtype, false, workspace, workspace_bytes);
-    if (R > 0 && st == DG_OK) st = run(what, a, kHeadToken, kPassForward, workspace, stream);
+    if (R > 0) st = run(what, a, kHeadToken, kPassForward, workspace, workspace_bytes, stream);
     if (st != DG_OK) return st;
     if (P > 0) {
         const PairLossArgs pa{logp, ref_logp, weight,          token,       seq_start, R, V, P,
@@ -299,7 +289,7 @@ dg_status dg_preference_loss(const void *logits, int32_t dtype, int64_t R, int64
     a.weight = nullptr;  // dlogp holds it
     a.grad = grad;
     a.ldg = ldg;
-    return run(what, a, kHeadToken, kPassBackward, workspace, stream, P > 0);
+    return run(what, a, kHeadToken, kPassBackward, workspace, workspace_bytes, stream, P > 0);
 }
 
 }  // extern "C"

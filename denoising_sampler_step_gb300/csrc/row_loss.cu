@@ -52,17 +52,6 @@ namespace {
 
 using namespace vocab;
 
-constexpr int kMaxStages = 16;
-// Bytes of a row that is one tile: with 32 KB, so two tiles and an exchange, a policy step of 2,048 x 12,000
-// fp32 entries takes 43.7 us instead of 35.1.
-constexpr int kMaxTile = 64 * 1024;
-// Stages that the tiles of longer rows leave room for.  1,024 x 262,144, policy step fp32 and distillation
-// step (K = 64) bf16, us: 5 stages 360 and 194, 7 stages 353 and 197, 9 (tiles of 24 KB) 356 and 217, 14 356
-// and 239.  A long list of a teacher's entries is looked through once per tile: K = 512, fp32, 5 stages 412,
-// 7 stages 423; K = 1,024 493 and 534.
-constexpr int kFewEntries = 256;
-constexpr int good_stages(int K) { return K > kFewEntries ? 5 : 7; }
-constexpr int kMinTile = 24 * 1024;
 // Below this ln p_0 the bucket's probability is no normal fp32 number and its term is left out.
 constexpr float kTailFloor = -87.0f;
 
@@ -906,26 +895,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(PairLossArgs a)
 
 // ------------------------------------------------------------------ launch
 
-constexpr int kDynamicBytes = 227 * 1024 - (int)sizeof(Shared);
-constexpr int kListBytes = 12;  // per entry of a teacher's table and stage
-
-// Tiles of a row: the whole row up to kMaxTile bytes, else equal parts, in whole 128-byte lines, of
-// which kGoodStages fit the ring beside the teacher's lists of K entries (K = 0: tokens), one less
-// for long lists.
-struct Tiling {
-    int tile_vecs, tiles;
-};
-Tiling tile_row(int64_t V, int dtype, int K) {
-    const int64_t nv = V / (dtype == DG_BF16 ? 8 : 4);
-    if (nv * 16 <= kMaxTile) return Tiling{(int)((nv + 7) / 8 * 8 > 0 ? (nv + 7) / 8 * 8 : 8), 1};
-    const int stages = good_stages(K);
-    int most = kDynamicBytes / stages - K * kListBytes;
-    if (most < kMinTile) most = kDynamicBytes / (stages - 1) - K * kListBytes;
-    const int64_t limit = most / 128 * 8;  // vectors
-    const int64_t n = (nv + limit - 1) / limit;
-    const int64_t per = ((nv + n - 1) / n + 7) / 8 * 8;
-    return Tiling{(int)per, (int)((nv + per - 1) / per)};
-}
+static_assert(sizeof(Shared) <= kSharedBytes, "");
 
 struct Kernel {
     const void *fn;
@@ -959,7 +929,7 @@ cudaError_t allow_shared(const void *fn, int index) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || (dev < kMaxDevices && set[index][dev].load(std::memory_order_acquire))) return e;
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynamicBytes);
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
     if (e == cudaSuccess && dev < kMaxDevices) set[index][dev].store(1, std::memory_order_release);
     return e;
 }
@@ -969,12 +939,11 @@ cudaError_t launch_pass(RowLossArgs a, bool chained, RowLossHead head, RowLossPa
                         cudaStream_t stream) {
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorNoDevice;
-    const Tiling tl = tile_row(a.V, a.dtype, head == kHeadDistill ? a.K : 0);
+    const int K = head == kHeadDistill ? a.K : 0;
+    const Tiling tl = tile_row(a.V, element_size(a.dtype), K);
     const int64_t total = a.R * tl.tiles;
     const int grid = (int)(total < sms ? total : sms);
-    // a stage: the tile, and for distillation its list of the teacher's entries
-    const int stage = tl.tile_vecs * 16 + (head == kHeadDistill ? a.K * kListBytes : 0);
-    const int stages = kDynamicBytes / stage < kMaxStages ? kDynamicBytes / stage : kMaxStages;
+    const int stages = ring_stages(tl, K);
     Plan plan{stages, tl.tile_vecs, tl.tiles, grid / tl.tiles, grid % tl.tiles, nullptr, nullptr};
     plan.rows = static_cast<RowClose *>(workspace);
     plan.sums = reinterpret_cast<unsigned long long *>(plan.rows + a.R);
@@ -998,7 +967,7 @@ cudaError_t launch_pass(RowLossArgs a, bool chained, RowLossHead head, RowLossPa
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3((unsigned)k.threads);
-    cfg.dynamicSmemBytes = (size_t)stages * stage;
+    cfg.dynamicSmemBytes = (size_t)stages * stage_bytes(tl, K);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     cfg.attrs = attr;
@@ -1017,14 +986,13 @@ cudaError_t launch_pass(RowLossArgs a, bool chained, RowLossHead head, RowLossPa
 // The workspace: the rows' numbers, their sums (the shortest tiles are those of the longest lists, with
 // either number of stages), then three floats per row for a step in two passes.
 size_t exchange_bytes(int64_t R, int64_t V, int dtype) {
-    const int few = tile_row(V, dtype, kFewEntries).tiles, many = tile_row(V, dtype, kMaxTopK).tiles;
+    const int size = element_size(dtype);
+    const int few = tile_row(V, size, kFewEntries).tiles, many = tile_row(V, size, kMaxTopK).tiles;
     const int tiles = few > many ? few : many;
     return (size_t)R * (sizeof(RowClose) + 8 * (size_t)tiles);
 }
 
 }  // namespace
-
-bool row_is_one_tile(int64_t V, int dtype) { return tile_row(V, dtype, 0).tiles == 1; }
 
 size_t row_loss_workspace_bytes(int64_t R, int64_t V, int dtype) {
     return exchange_bytes(R, V, dtype) + (size_t)R * 3 * sizeof(float);
@@ -1032,15 +1000,10 @@ size_t row_loss_workspace_bytes(int64_t R, int64_t V, int dtype) {
 
 cudaError_t launch_row_loss(const RowLossArgs &a, RowLossHead head, RowLossPass pass, void *workspace,
                             cudaStream_t stream, bool chained) {
-    const Tiling tl = tile_row(a.V, a.dtype, head == kHeadDistill ? a.K : 0);
-    const int sms = device_sm_count();
+    const int sms = device_sm_count(), K = head == kHeadDistill ? a.K : 0, size = element_size(a.dtype);
     if (sms <= 0) return cudaErrorNoDevice;
-    const int stage = tl.tile_vecs * 16 + (head == kHeadDistill ? a.K * kListBytes : 0);
-    const int stages = kDynamicBytes / stage < kMaxStages ? kDynamicBytes / stage : kMaxStages;
-    // A step keeps a row's tiles in the rings until the row is complete: a CTA must have room for its
-    // share of one row and the next.  Longer rows are read twice.
-    const int64_t grid = a.R * tl.tiles < sms ? a.R * tl.tiles : sms;
-    if (pass != kPassStep || (tl.tiles + grid - 1) / grid + 2 <= stages) 
+    if (!workspace && takes_workspace(a.V, size, head, pass)) return cudaErrorInvalidValue;
+    if (pass != kPassStep || !reads_twice(tile_row(a.V, size, K), K, a.R, sms))
         return launch_pass(a, chained, head, pass, workspace, stream);
     RowLossArgs f = a;
     float *saved = reinterpret_cast<float *>(static_cast<char *>(workspace) + exchange_bytes(a.R, a.V, a.dtype));

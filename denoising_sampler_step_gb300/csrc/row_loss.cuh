@@ -8,20 +8,11 @@
 #include <cmath>
 
 #include "../../include/dgsamp.h"
+#include "row_loss_plan.h"
 
 namespace dg {
 
-// What a row's loss is taken from.
-enum RowLossHead {
-    kHeadToken = 0,   // the log-probability of one token per row
-    kHeadDistill = 1  // a teacher's top logits
-};
-// Which passes a call makes over a row.
-enum RowLossPass {
-    kPassForward = 1,   // statistics and losses
-    kPassBackward = 2,  // the gradient from the statistics a forward call saved
-    kPassStep = 3       // both in one call
-};
+inline int element_size(int dtype) { return dtype == DG_BF16 ? 2 : 4; }
 
 // log2(e) / T.  One float's rounding of it, up to 2^-24, puts a row's log-sum-exp off by that times its
 // mean (m - x) / T, and every row's in the same direction, which a sequence's sum of log-probabilities
@@ -73,9 +64,7 @@ struct RowLossArgs {
 };
 
 size_t row_loss_workspace_bytes(int64_t R, int64_t V, int dtype);
-// Whether a row of V entries stays whole in one SM's shared memory: only the distillation's backward
-// pass needs the workspace then.
-bool row_is_one_tile(int64_t V, int dtype);
+// Takes the workspace where takes_workspace says so, and refuses to start without one there.
 // chained: the kernel before it on the stream is one of row_loss.cu's.
 cudaError_t launch_row_loss(const RowLossArgs &a, RowLossHead head, RowLossPass pass, void *workspace,
                             cudaStream_t stream, bool chained = false);
@@ -109,7 +98,5 @@ struct RowTopKArgs {
 };
 size_t row_topk_workspace_bytes(int64_t R, int64_t V, int K, int dtype);
 cudaError_t launch_row_topk(const RowTopKArgs &a, void *workspace, cudaStream_t stream);
-
-constexpr int kMaxTopK = 1024;
 
 }  // namespace dg
