@@ -52,7 +52,12 @@ namespace {
 
 using namespace vocab;
 
-// Below this ln p_0 the bucket's probability is no normal fp32 number and its term is left out.
+// Entries down to here are masked (both types' lowest finite values and -inf): a bucket of such entries alone
+// has no distribution of its own, and its term is left out.
+constexpr float kMasked = -3.38e38f;
+// q_0 is a difference from 1 of what teacher_lse and the teacher's logits give, each rounded to fp32, and known
+// to about (|teacher_lse| + 4) 2^-22.  Times an ln p_0 below this (a vocabulary masked by, say, -1e4 in teacher
+// and student alike) such a rest would be a loss of its own, so there it counts as 0.
 constexpr float kTailFloor = -87.0f;
 
 struct Plan {
@@ -64,14 +69,15 @@ struct Plan {
     struct RowClose *rows;     // [R] published rows
 };
 
-// What the gradient of a row needs: g_v = scale exp((x_v - m) / T), and at the special entries
+// What the gradient of a row needs: g_v = scale exp((x_v - base) / T), and at the special entries
 // coef (mass p_v - q_v) with p_v = inv_s exp((x_v - m) / T) and, over a teacher's entries,
 // ln q = (t - off) / T + log_scale (a token: q = 1, mass 1, and the sign in coef).
+// base is m, but the bucket's own maximum where there is a bucket: p_0 may be far below 1, and a scale over
+// exp((x_v - m) / T) would have to hold q_0 / p_0, past fp32's range, times what has vanished in it.
 // It is published as four 64-bit words, none of which is ever 0 (there yet: all four are not): a
-// maximum or offset of 0 is -0, 1 / s is no 0, and the last holds a 1.
+// maximum, base or offset of 0 is -0, and 1 / s is no 0.
 struct __align__(16) RowClose {
-    float m, scale, inv_s, coef, mass, off, log_scale;
-    uint32_t flag;
+    float m, scale, inv_s, coef, mass, off, log_scale, base;
 };
 __device__ __forceinline__ float never_zero(float v) { return v == 0.0f ? -0.0f : v; }
 
@@ -144,14 +150,26 @@ __device__ __forceinline__ float teacher_terms(const RowLossArgs &a, const MaxSu
     cl->mass = teacher.s > 0.0f ? 1.0f : 0.0f;
     return 0.0f;
 }
-// And with the student's ln p_0 of the bucket: the gradient's scale over it, without 1 / s.
-__device__ __forceinline__ float bucket_scale(const RowLossArgs &a, float logp0, float q_rest, RowClose *cl) {
-    float factor = cl->mass;
-    if (a.teacher_lse && logp0 > kTailFloor) {
-        cl->mass += q_rest;
-        factor = cl->mass - q_rest * exp_fast(-logp0);
-    }
-    return cl->coef * factor;
+// And with the student's p_0 of the bucket: the scale and base of the gradient outside the teacher's entries.
+// tail_m and tail_s are the bucket's own maximum and sum, so p_v = p_0 exp((x_v - tail_m) / T) / tail_s there,
+// and the gradient coef p_v (M - q_0 / p_0), M = sum of q_k and q_0, has no quotient.  Returns what of q_rest
+// counts as q_0.
+__device__ __forceinline__ float bucket_terms(const RowLossArgs &a, float teacher_lse, float logp0, float p0,
+                                              float tail_m, float tail_s, float q_rest, RowClose *cl) {
+    cl->base = cl->m;
+    cl->scale = cl->coef * cl->mass * cl->inv_s;
+    if (!a.teacher_lse || !(tail_m > kMasked && logp0 > -INFINITY)) return 0.0f;
+    if (logp0 < kTailFloor && q_rest <= (fabsf(teacher_lse) + 4.0f) * 0x1p-22f) q_rest = 0.0f;
+    cl->mass += q_rest;
+    cl->base = never_zero(tail_m);
+    cl->scale = cl->coef * fmaf(cl->mass, p0, -q_rest) / tail_s;
+    return q_rest;
+}
+
+// What rounding lost of sum = a + b.
+__device__ __forceinline__ float lost_by_sum(float a, float b, float sum) {
+    const float bb = sum - a;
+    return (a - (sum - bb)) + (b - bb);
 }
 
 // Two words of a row's numbers, in the order in which they lie in memory.
@@ -163,7 +181,7 @@ __device__ __forceinline__ void publish(RowClose *out, const RowClose &cl) {
                  "l"(two_words(cl.inv_s, cl.coef))
                  : "memory");
     asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(reinterpret_cast<char *>(out) + 16),
-                 "l"(two_words(cl.mass, cl.off)), "l"(two_words(cl.log_scale, __uint_as_float(cl.flag)))
+                 "l"(two_words(cl.mass, cl.off)), "l"(two_words(cl.log_scale, cl.base))
                  : "memory");
 }
 // Whether the row is there; then *cl holds it.
@@ -176,7 +194,7 @@ __device__ __forceinline__ bool look_up(const RowClose *in, RowClose *cl) {
                  : "memory");
     auto lo = [](unsigned long long v) { return __uint_as_float((uint32_t)v); };
     auto hi = [](unsigned long long v) { return __uint_as_float((uint32_t)(v >> 32)); };
-    *cl = RowClose{lo(w[0]), hi(w[0]), lo(w[1]), hi(w[1]), lo(w[2]), hi(w[2]), lo(w[3]), 1u};
+    *cl = RowClose{lo(w[0]), hi(w[0]), lo(w[1]), hi(w[1]), lo(w[2]), hi(w[2]), lo(w[3]), hi(w[3])};
     return w[0] && w[1] && w[2] && w[3];
 }
 
@@ -185,7 +203,7 @@ __device__ __forceinline__ RowClose close_saved(const RowLossArgs &a, float lse)
     RowClose cl{};
     cl.m = never_zero(finite_max(lse * a.T));
     cl.inv_s = expf(-fmaf(lse, a.T, -lse * a.T) / a.T);
-    cl.flag = 1;
+    cl.base = cl.m;
     return cl;
 }
 __device__ __forceinline__ RowClose close_token(const RowLossArgs &a, float w, float lse) {
@@ -224,15 +242,11 @@ __device__ __forceinline__ unsigned long long poll_sum(const unsigned long long 
 // them 2,048 x 262,144 bf16 rows took 324 us instead of 317).
 template <bool TWO>
 __device__ __forceinline__ float log_prob(float x, float m, float T, float lns, float inv_s, bool once, float *low) {
-    auto lost = [](float a, float b, float sum) {  // of sum = a + b
-        const float bb = sum - a;
-        return (a - (sum - bb)) + (b - bb);
-    };
     const float d = x - m, q = d / T, r = q - lns;
     *low = 0.0f;
     if (!(fabsf(r) < INFINITY)) return r;
     if (!once) return TWO ? r + (((q - r) - lns) - 5e-8f * (1.0f - inv_s)) : r;
-    const float e = lost(q, -lns, r) + (fmaf(-q, T, d) + lost(x, -m, d)) / T -
+    const float e = lost_by_sum(q, -lns, r) + (fmaf(-q, T, d) + lost_by_sum(x, -m, d)) / T -
                     (TWO ? 5e-8f * (1.0f - inv_s) : 0.0f);
     const float p = r + e;
     *low = e - (p - r);
@@ -501,7 +515,6 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
             const T *x = static_cast<const T *>(a.logits) + row * a.ldl;
             float A = 0.0f, old = 0.0f, ref = 0.0f, x_tok = 0.0f, teacher_lse = 0.0f, spread = 0.0f, q_rest = 0.0f;
             RowClose cl{};
-            cl.flag = 1;
             MaxSum top = none, teacher = none;
             const int32_t *idx = a.indices + row * a.ldk;
             const float *tl = a.teacher + row * a.ldk;
@@ -601,15 +614,17 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
                 cl.coef = -dlogp * w * inv_T;
                 cl.mass = 1.0f;
                 cl.scale = cl.coef * cl.inv_s;
+                cl.base = cl.m;
             } else {
+                float part = 0.0f;
                 if (a.teacher_lse) {
                     // near 1 from the ratio of the sums: the logarithms' difference would round it off
-                    const float part = rest.s * exp_below(rest.m, cl.m, sums_c);
+                    part = rest.s * exp_below(rest.m, cl.m, sums_c);
                     logp0 = part > 1e-3f * st.s ? logf(part / st.s)
                             : rest.s > 0.0f     ? (rest.m - m) / a.T + logf(rest.s) - lns
                                                 : -INFINITY;
                 }
-                cl.scale = bucket_scale(a, logp0, q_rest, &cl) * cl.inv_s;
+                q_rest = bucket_terms(a, teacher_lse, logp0, part / st.s, rest.m, rest.s, q_rest, &cl);
             }
             if (kBackward) {
                 if (SPLIT) {
@@ -629,7 +644,7 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
                        fmaf(teacher.s, log_share + (m - finite_max(top.m)) / a.T + lns, spread);
             }
             if (kDistill) {
-                if (a.teacher_lse && q_rest > 0.0f && logp0 > kTailFloor) loss += q_rest * (logf(q_rest) - logp0);
+                if (q_rest > 0.0f) loss += q_rest * (logf(q_rest) - logp0);
                 loss *= a.T * a.T;
             }
             if (lane == 0) {
@@ -720,7 +735,7 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
                     const uint32_t taken = kDistill ? sh.tail_taken[slot]
                                                     : here && at_tok >= t.len ? 1u << (at_tok - t.len) : 0u;
                     if (lane < t.end - t.len && !(taken >> lane & 1))
-                        g[t.len + lane] = from_f32<T>(cl.scale * p_of(to_f32(x[t.len + lane])));
+                        g[t.len + lane] = from_f32<T>(cl.scale * exp_below(to_f32(x[t.len + lane]), cl.base, c));
                     if (!wait(sh.done[slot], lap)) return;
                     if (kDistill) {
 #pragma unroll 1
@@ -779,8 +794,8 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
         each_tile(sh.full, [&](int slot, uint32_t lap) {
             if (kForward && !wait(sh.ready[slot], lap)) return;
             const uint4 *vecs = stage(slot);
-            const float m = sh.close[slot].m, scale = sh.close[slot].scale;
-            const f32x2 minus_m = pair(-m, -m), scales = pair(scale, scale);
+            const float base = sh.close[slot].base, scale = sh.close[slot].scale;
+            const f32x2 minus_base = pair(-base, -base), scales = pair(scale, scale);
             uint4 *gv = reinterpret_cast<uint4 *>(tile_g(sh.tile[slot]));
             const int nvecs = sh.tile[slot].len / N;
 #pragma unroll 1
@@ -795,7 +810,7 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
                         f32x2 p[N / 2];
                         Vec<T>::pairs(in[i], p);
 #pragma unroll
-                        for (int e = 0; e < N / 2; ++e) p[e] = mul2(exp_below2(p[e], minus_m, cc), scales);
+                        for (int e = 0; e < N / 2; ++e) p[e] = mul2(exp_below2(p[e], minus_base, cc), scales);
                         gv[v0 + i * kThreads] = Vec<T>::pack(p);
                     }
             }
@@ -823,8 +838,13 @@ __global__ void __launch_bounds__(32 * kCloseWarps) row_close_kernel(const RowLo
         fold(teacher, one, c);
     }
     teacher = warp_merge(teacher, c);
-    const float q_rest = teacher_terms(a, teacher, a.teacher_lse ? a.teacher_lse[row] : 0.0f, w, &cl);
-    cl.scale = bucket_scale(a, a.teacher_lse ? a.tail_logp[row] : 0.0f, q_rest, &cl) * cl.inv_s;
+    const float teacher_lse = a.teacher_lse ? a.teacher_lse[row] : 0.0f;
+    const float q_rest = teacher_terms(a, teacher, teacher_lse, w, &cl);
+    // the bucket's log-sum-exp stands for its maximum, with a sum of 1 but for what the roundings lost
+    const float lse = a.lse[row], logp0 = a.teacher_lse ? a.tail_logp[row] : 0.0f;
+    const float tail = lse + logp0, tail_m = tail * a.T;
+    const float lost = fmaf(tail, a.T, -tail_m) / a.T + lost_by_sum(lse, logp0, tail);
+    bucket_terms(a, teacher_lse, logp0, expf(logp0), tail_m, expf(lost), q_rest, &cl);
     if (lane == 0) rows[row] = cl;
 }
 

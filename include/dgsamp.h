@@ -624,8 +624,10 @@ dg_status dg_token_logp_backward(const void *logits, int32_t dtype, int64_t R, i
  *   q_k = exp(teacher_k / T - teacher_lse), q_0 = max(0, 1 - sum q)  (teacher_lse given)
  *   loss = T^2 [ sum_k q_k (ln q_k - ln p_k)  +  q_0 (ln q_0 - ln p_0) ]
  * With teacher_lse the entries outside the teacher's form one bucket, p_0 = the student's
- * probability of all of them (the second term; left out where ln p_0 is below -87: no fp32
- * probability, as when all of them are masked).  Terms with q = 0 are 0.
+ * probability of all of them (the second term; left out where there are none or all of them are
+ * masked, by -inf or the type's lowest value).  Terms with q = 0 are 0.  q_0 is 1 less a sum of fp32
+ * numbers; where ln p_0 is below -87, a q_0 of no more than (|teacher_lse| + 4) 2^-22, which that
+ * difference's roundings can be alone, counts as 0.
  *   grad[r, v] = weight_r T (M p_v - q_v)        on the teacher's entries, M = sum_k q_k + q_0
  *   grad[r, v] = weight_r T p_v (M - q_0 / p_0)  elsewhere
  *

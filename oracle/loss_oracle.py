@@ -77,18 +77,21 @@ def distill_loss(x, indices, teacher, teacher_lse=None, T: float = 1.0, weight=N
             q0 = max(0.0, 1.0 - q.sum())
         pos = q > 0
         loss = np.sum(q[pos] * (np.log(q[pos]) - (z[at] - lse)[pos]))
-        p0 = p[~inside].sum()
         mass, share = q.sum(), 0.0
         if teacher_lse is not None:
             rest = z[~inside]
             logp0 = _logsumexp(rest) - lse if rest.size and np.max(rest) > -np.inf else -np.inf
             out["tail_logp"][r] = logp0
-            if logp0 > -87.0:      # else the student has no mass there (in fp32) and the term is left out
+            # a bucket of masked entries (-inf, or the lowest value of fp32 or bf16) alone is left out
+            if rest.size and np.max(rest) * T > -3.38e38 and logp0 > -np.inf:
+                if logp0 < -87.0 and q0 <= (abs(float(teacher_lse[r])) + 4.0) * 2.0 ** -22:
+                    q0 = 0.0       # what rounding leaves of 1 - sum q in fp32
                 mass += q0
-                share = q0 / p0
+                share = np.zeros(V)
+                share[~inside] = q0 * np.exp(rest - _logsumexp(rest))       # q_0 p_v / p_0
                 if q0 > 0:
                     loss += q0 * (np.log(q0) - logp0)
-        g = p * (mass - share)
+        g = p * mass - share
         g[at] = mass * p[at] - q
         out["loss"][r], out["lse"][r], out["grad"][r] = T * T * loss, lse, w[r] * T * g
     return out
