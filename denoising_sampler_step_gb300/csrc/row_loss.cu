@@ -53,12 +53,12 @@ namespace {
 using namespace vocab;
 
 // Entries down to here are masked (both types' lowest finite values and -inf): a bucket of such entries alone
-// has no distribution of its own, and its term is left out.
+// has no distribution of its own, and its term is left out.  (Times T below 1: ln p_0 stays a finite fp32 number.)
 constexpr float kMasked = -3.38e38f;
 // q_0 is a difference from 1 of what teacher_lse and the teacher's logits give, each rounded to fp32, and known
 // to about (|teacher_lse| + 4) 2^-22.  Times an ln p_0 below this (a vocabulary masked by, say, -1e4 in teacher
 // and student alike) such a rest would be a loss of its own, so there it counts as 0.
-constexpr float kTailFloor = -87.0f;
+constexpr float kTailFloor = -87.0f, kExpTailFloor = 1.64581145e-38f;  // and e to it
 
 struct Plan {
     int stages;      // of the ring
@@ -150,19 +150,21 @@ __device__ __forceinline__ float teacher_terms(const RowLossArgs &a, const MaxSu
     cl->mass = teacher.s > 0.0f ? 1.0f : 0.0f;
     return 0.0f;
 }
-// And with the student's p_0 of the bucket: the scale and base of the gradient outside the teacher's entries.
-// tail_m and tail_s are the bucket's own maximum and sum, so p_v = p_0 exp((x_v - tail_m) / T) / tail_s there,
-// and the gradient coef p_v (M - q_0 / p_0), M = sum of q_k and q_0, has no quotient.  Returns what of q_rest
-// counts as q_0.
-__device__ __forceinline__ float bucket_terms(const RowLossArgs &a, float teacher_lse, float logp0, float p0,
+// And with the student's p_0 = part / s of the bucket: the scale and base of the gradient outside the teacher's
+// entries.  tail_m and tail_s are the bucket's own maximum and sum, so p_v = p_0 exp((x_v - tail_m) / T) / tail_s
+// there, and the gradient is coef p_v (M - q_0 / p_0), M = sum of q_k and q_0, without that quotient (and exactly
+// 0 where p_0 = q_0 = 1).  Returns what of q_rest counts as q_0.  (One division, and not the exact one, on the way
+// to a published row: with two exact ones a step of 2,048 x 262,144 fp32 rows, K = 128, took 645 us, not 632.)
+// far: ln p_0 is below kTailFloor.
+__device__ __forceinline__ float bucket_terms(const RowLossArgs &a, float teacher_lse, bool far, float part, float s,
                                               float tail_m, float tail_s, float q_rest, RowClose *cl) {
     cl->base = cl->m;
     cl->scale = cl->coef * cl->mass * cl->inv_s;
-    if (!a.teacher_lse || !(tail_m > kMasked && logp0 > -INFINITY)) return 0.0f;
-    if (logp0 < kTailFloor && q_rest <= (fabsf(teacher_lse) + 4.0f) * 0x1p-22f) q_rest = 0.0f;
+    if (!a.teacher_lse || !(tail_m > kMasked * fminf(a.T, 1.0f))) return 0.0f;
+    if (far && q_rest <= (fabsf(teacher_lse) + 4.0f) * 0x1p-22f) q_rest = 0.0f;
     cl->mass += q_rest;
     cl->base = never_zero(tail_m);
-    cl->scale = cl->coef * fmaf(cl->mass, p0, -q_rest) / tail_s;
+    cl->scale = cl->coef * __fdividef(fmaf(cl->mass, part, -q_rest * s), s * tail_s);
     return q_rest;
 }
 
@@ -587,7 +589,7 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
             cl.m = never_zero(finite_max(m));
             cl.inv_s = 1.0f / st.s;
             const float lns = logf(st.s);
-            float logp = 0.0f, logp0 = 0.0f, loss = 0.0f, kl = 0.0f, dlogp = 0.0f;
+            float logp = 0.0f, logp0 = 0.0f, part = 0.0f, loss = 0.0f, kl = 0.0f, dlogp = 0.0f;
             bool clipped = false;
             // (little before the row is published: the other CTAs wait)
             if (HEAD == kHeadToken) {
@@ -616,15 +618,8 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
                 cl.scale = cl.coef * cl.inv_s;
                 cl.base = cl.m;
             } else {
-                float part = 0.0f;
-                if (a.teacher_lse) {
-                    // near 1 from the ratio of the sums: the logarithms' difference would round it off
-                    part = rest.s * exp_below(rest.m, cl.m, sums_c);
-                    logp0 = part > 1e-3f * st.s ? logf(part / st.s)
-                            : rest.s > 0.0f     ? (rest.m - m) / a.T + logf(rest.s) - lns
-                                                : -INFINITY;
-                }
-                q_rest = bucket_terms(a, teacher_lse, logp0, part / st.s, rest.m, rest.s, q_rest, &cl);
+                part = rest.s * exp_below(rest.m, cl.m, sums_c);
+                q_rest = bucket_terms(a, teacher_lse, part < kExpTailFloor * st.s, part, st.s, rest.m, rest.s, q_rest, &cl);
             }
             if (kBackward) {
                 if (SPLIT) {
@@ -637,6 +632,12 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
                 __syncwarp();
             }
             if (!SPLIT) arrive(kBackward ? sh.ready[slot] : sh.empty[slot]);
+            if (kDistill && a.teacher_lse) {
+                // near 1 from the ratio of the sums: the logarithms' difference would round it off
+                logp0 = part > 1e-3f * st.s ? logf(part / st.s)
+                        : rest.s > 0.0f     ? (rest.m - m) / a.T + logf(rest.s) - lns
+                                            : -INFINITY;
+            }
             if (kDistill && teacher.s > 0.0f) {
                 // q_k = e_k share with e_k = exp((t_k - t_max) / T)
                 const float log_share = a.teacher_lse ? teacher.m / a.T - teacher_lse : cl.log_scale;
@@ -844,7 +845,7 @@ __global__ void __launch_bounds__(32 * kCloseWarps) row_close_kernel(const RowLo
     const float lse = a.lse[row], logp0 = a.teacher_lse ? a.tail_logp[row] : 0.0f;
     const float tail = lse + logp0, tail_m = tail * a.T;
     const float lost = fmaf(tail, a.T, -tail_m) / a.T + lost_by_sum(lse, logp0, tail);
-    bucket_terms(a, teacher_lse, logp0, expf(logp0), tail_m, expf(lost), q_rest, &cl);
+    bucket_terms(a, teacher_lse, logp0 < kTailFloor, expf(logp0), 1.0f, tail_m, expf(lost), q_rest, &cl);
     if (lane == 0) rows[row] = cl;
 }
 

@@ -83,7 +83,7 @@ def distill_loss(x, indices, teacher, teacher_lse=None, T: float = 1.0, weight=N
             logp0 = _logsumexp(rest) - lse if rest.size and np.max(rest) > -np.inf else -np.inf
             out["tail_logp"][r] = logp0
             # a bucket of masked entries (-inf, or the lowest value of fp32 or bf16) alone is left out
-            if rest.size and np.max(rest) * T > -3.38e38 and logp0 > -np.inf:
+            if rest.size and np.max(rest) * T > -3.38e38 * min(T, 1.0):
                 if logp0 < -87.0 and q0 <= (abs(float(teacher_lse[r])) + 4.0) * 2.0 ** -22:
                     q0 = 0.0       # what rounding leaves of 1 - sum q in fp32
                 mass += q0
