@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
                 if (!kBackward && a.keep_low) dlogp = low;
                 if (a.policy) {
                     const float ratio = exp_fast(logp - old);
-                    const float raw = ratio * A;
+                    const float raw = A != 0.0f ? ratio * A : 0.0f;  // (also where the ratio is infinite)
                     const float cut = fminf(fmaxf(ratio, 1.0f - a.clip_low), 1.0f + a.clip_high) * A;
                     clipped = raw > cut;
                     loss = -(clipped ? cut : raw);
@@ -609,8 +609,10 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
                         const float d = ref - logp;
                         const float e = expm1f(d);
                         kl = e - d;
-                        loss = fmaf(a.kl_coef, kl, loss);
-                        dlogp = fmaf(-a.kl_coef, e, dlogp);
+                        if (a.kl_coef != 0.0f) {
+                            loss = fmaf(a.kl_coef, kl, loss);
+                            dlogp = fmaf(-a.kl_coef, e, dlogp);
+                        }
                     }
                 }
                 cl.coef = -dlogp * w * inv_T;

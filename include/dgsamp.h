@@ -657,6 +657,7 @@ dg_status dg_distill_loss_backward(const void *logits, int32_t dtype, int64_t R,
  *   ratio = exp(logp - old_logp),  d = ref_logp - logp
  *   loss  = -min(ratio A, clip(ratio, 1 - clip_low, 1 + clip_high) A) + kl_coef (e^d - 1 - d)
  *   dlogp = [ratio A <= clipped ratio A] (-ratio A) - kl_coef (e^d - 1)
+ * A term whose factor A or kl_coef is 0 is 0, also where its exponential leaves fp32's range.
  *
  *   token (the sampled actions), old_logp, advantage A [R]; ref_logp [R] or NULL (no KL term)
  *   loss, logp, lse, kl (e^d - 1 - d), dlogp [R] fp32, clipped [R] uint8 (1 where the clipped branch
