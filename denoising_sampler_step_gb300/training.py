@@ -8,6 +8,9 @@ logits with the binding's own calls (`grad=True`, weights in `weight`).
 
 `mask` [R] (bool or any type: nonzero counts) leaves rows out: their logits are not read, their
 loss is 0 and their gradient 0.
+
+The functions differentiate once and in the logits alone.  Another argument that requires a gradient
+is an error (detach it), and so is `create_graph=True`: what would be lost is not lost in silence.
 """
 from __future__ import annotations
 
@@ -26,6 +29,21 @@ def _upstream(g: torch.Tensor, weight: torch.Tensor | None) -> torch.Tensor:
     return g.float().contiguous()
 
 
+def _constants(**tensors) -> None:
+    """Refuses arguments whose gradient would be dropped."""
+    for name, t in tensors.items():
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} requires a gradient, and the loss is differentiable in the logits alone: "
+                             f"pass {name}.detach()")
+
+
+def _first_order() -> None:
+    """Refuses a backward pass that is to be differentiated (autograd records it only then)."""
+    if torch.is_grad_enabled():
+        raise RuntimeError("the losses on logits have first derivatives only: with create_graph=True their "
+                           "gradient would count as a constant")
+
+
 class _TokenLogp(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, token, temperature, weight):
@@ -36,6 +54,7 @@ class _TokenLogp(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, g):
+        _first_order()
         logits, token, lse, weight = ctx.saved_tensors
         grad = B.dg_token_logp_backward(logits, token, lse, _upstream(g, weight), temperature=ctx.temperature)
         return grad, None, None, None
@@ -52,6 +71,7 @@ class _Distill(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, g):
+        _first_order()
         logits, indices, teacher, teacher_lse, lse, tail_logp, weight = ctx.saved_tensors
         grad = B.dg_distill_loss_backward(logits, indices, teacher, lse, _upstream(g, weight),
                                           teacher_lse=teacher_lse, tail_logp=tail_logp,
@@ -72,6 +92,7 @@ class _Policy(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, g, *_):
+        _first_order()
         logits, token, lse, dlogp, weight = ctx.saved_tensors
         grad = B.dg_token_logp_backward(logits, token, lse, dlogp, scale=_upstream(g, weight),
                                         temperature=ctx.temperature)
@@ -90,6 +111,7 @@ class _Preference(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, g, _):
+        _first_order()
         logits, token, seq_start, lse, dlogp = ctx.saved_tensors
         # the pair each row belongs to (rows in no pair have dlogp 0, whatever their scale)
         rows = torch.arange(logits.shape[0], dtype=torch.int32, device=logits.device)
@@ -109,6 +131,7 @@ def distill_loss(logits: torch.Tensor, indices: torch.Tensor, teacher: torch.Ten
                  teacher_lse: torch.Tensor | None = None, temperature: float = 1.0,
                  mask: torch.Tensor | None = None) -> torch.Tensor:
     """Distillation loss per row [R] from a teacher's top logits (binding.dg_distill_loss)."""
+    _constants(teacher=teacher, teacher_lse=teacher_lse)
     return _Distill.apply(logits, indices, teacher, teacher_lse, temperature, _weight(mask))
 
 
@@ -117,6 +140,7 @@ def policy_loss(logits: torch.Tensor, token: torch.Tensor, old_logp: torch.Tenso
                 kl_coef: float = 0.0, temperature: float = 1.0,
                 mask: torch.Tensor | None = None) -> tuple[torch.Tensor, dict]:
     """(loss per row [R], {logp, kl, clipped}) of the clipped policy loss (binding.dg_policy_loss)."""
+    _constants(old_logp=old_logp, advantage=advantage, ref_logp=ref_logp)
     loss, logp, kl, clipped = _Policy.apply(logits, token, old_logp, advantage, ref_logp, clip_low, clip_high,
                                             kl_coef, temperature, _weight(mask))
     return loss, {"logp": logp, "kl": kl, "clipped": clipped}
@@ -127,4 +151,5 @@ def preference_loss(logits: torch.Tensor, token: torch.Tensor, ref_logp: torch.T
                     temperature: float = 1.0, weight: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """(loss per pair [P], log ratios per sequence [2P]) of the preference loss
     (binding.dg_preference_loss); `weight` [R] masks tokens or normalises by length."""
+    _constants(ref_logp=ref_logp, weight=weight)
     return _Preference.apply(logits, token, ref_logp, seq_start, beta, label_smoothing, temperature, weight)
