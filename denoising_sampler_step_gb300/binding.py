@@ -668,16 +668,23 @@ def loss_workspace(R: int, V: int, device, dtype: torch.dtype = torch.float32) -
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def _memory(ws: torch.Tensor, device) -> tuple:
+    """(pointer, bytes) of a workspace tensor of any type."""
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on {device}, got strides {ws.stride()} on {ws.device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _loss_ws(ws, R: int, V: int, code: int, device, stream, always: bool = False) -> tuple:
     """(tensor, pointer, bytes) of the caller's workspace, of a new one (its memory stays with the stream
     that uses it), or of none where the call needs none."""
+    if not always and not dg_row_loss_needs_workspace(V, code):
+        return None, None, 0
     if ws is None:
-        if not always and not dg_row_loss_needs_workspace(V, code):
-            return None, None, 0
         n = max(16, dg_row_loss_workspace_size(R, V, code))
         with _on(stream):
             ws = torch.empty(n, dtype=torch.uint8, device=device)
-    return ws, ws.data_ptr(), ws.numel()
+    return (ws, *_memory(ws, device))
 
 
 def dg_row_topk_workspace_size(R: int, V: int, K: int, dtype: int = DG_F32) -> int:
@@ -706,8 +713,9 @@ def dg_row_topk(logits: torch.Tensor, K: int, temperature: float = 1.0, lse: boo
     if ws is None:
         with _on(stream):
             ws = topk_workspace(R, V, K, dev, logits.dtype)
+    ws_ptr, ws_bytes = _memory(ws, dev)
     _check(lib.dg_row_topk(x, code, R, V, ld, K, temperature, o["values"].data_ptr(), o["indices"].data_ptr(), ldk,
-                           _vec(o.get("lse"), R, torch.float32, dev, "lse"), ws.data_ptr(), ws.numel(),
+                           _vec(o.get("lse"), R, torch.float32, dev, "lse"), ws_ptr, ws_bytes,
                            _stream(stream)), "dg_row_topk")
     return o
 
