@@ -575,6 +575,9 @@ def _logits(t: torch.Tensor) -> tuple:
         raise TypeError(f"logits must be float32 or bfloat16, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError("logits must be on the GPU")
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"logits are on {t.device}, and the kernels would run on the current device, "
+                         f"cuda:{torch._C._cuda_getDevice()}: use torch.cuda.device(logits.device)")
     if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
         raise ValueError("logits must be [R, V] with unit column stride")
     R, V = t.shape
