@@ -98,7 +98,9 @@ using namespace dg;
 extern "C" {
 
 size_t dg_row_topk_workspace_size(int64_t R, int64_t V, int32_t K, int32_t dtype) {
-    if (R < 1 || V < 1 || K < 1 || K > kMaxTopK || K > V || (dtype != DG_F32 && dtype != DG_BF16)) return 0;
+    if (R < 1 || R > (1LL << 28) || V < 1 || V > 0x7ffffff0LL || K < 1 || K > kMaxTopK || K > V ||
+        (dtype != DG_F32 && dtype != DG_BF16))
+        return 0;
     return row_topk_workspace_bytes(R, V, K, dtype);
 }
 
@@ -122,6 +124,7 @@ dg_status dg_row_topk(const void *logits, int32_t dtype, int64_t R, int64_t V, i
     if (K < 1 || K > V || ldk < K) return fail(DG_ERR_INVALID_ARG, "%s: need 1 <= K <= V and ldk >= K", what);
     if (K > kMaxTopK) return fail(DG_ERR_UNSUPPORTED, "%s: K = %d is above %d", what, K, kMaxTopK);
     if (ldk > (1LL << 31)) return fail(DG_ERR_UNSUPPORTED, "%s: ldk too large", what);
+    if (!row_topk_fits(R, V, dtype)) return fail(DG_ERR_UNSUPPORTED, "%s: more than 16 TiB of rows", what);
     if (R == 0) return DG_OK;
     if (!values || !indices) return fail(DG_ERR_INVALID_ARG, "%s: an output pointer is NULL", what);
     const size_t need = row_topk_workspace_bytes(R, V, K, dtype);

@@ -96,6 +96,8 @@ struct RowTopKArgs {
     int64_t ldk;
     float *lse;  // [R] or NULL
 };
+// Whether the rows' 8 KB units can be counted in 32 bits (16 TiB of logits).
+bool row_topk_fits(int64_t R, int64_t V, int dtype);
 size_t row_topk_workspace_bytes(int64_t R, int64_t V, int K, int dtype);
 cudaError_t launch_row_topk(const RowTopKArgs &a, void *workspace, cudaStream_t stream);
 

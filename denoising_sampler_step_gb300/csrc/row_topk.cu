@@ -831,9 +831,9 @@ constexpr size_t kDynamic = kStages * kTileBytes + sizeof(Shared);
 bool layout(int64_t R, int64_t V, int K, int dtype, Layout *l) {
     const int sms = device_sm_count();
     if (sms <= 0) return false;
-    const int64_t unit = kUnitBytes / (dtype == DG_BF16 ? 2 : 4);
+    const int64_t unit = kUnitBytes / element_size(dtype);
     const int64_t per_row = (V + unit - 1) / unit, units = R * per_row;
-    if (units > INT32_MAX) return false;
+    if (!row_topk_fits(R, V, dtype)) return false;
     l->units_per_row = (int)per_row;
     l->units = (int)units;
     // a piece of a row costs a selection and K candidates to merge: no fewer than kMinUnits units,
@@ -887,6 +887,11 @@ cudaError_t launch(const RowTopKArgs &a, const Layout &lay, void *ws, cudaStream
 }
 
 }  // namespace
+
+bool row_topk_fits(int64_t R, int64_t V, int dtype) {
+    const int64_t unit = kUnitBytes / element_size(dtype);
+    return R * ((V + unit - 1) / unit) <= INT32_MAX;
+}
 
 size_t row_topk_workspace_bytes(int64_t R, int64_t V, int K, int dtype) {
     Layout l;
