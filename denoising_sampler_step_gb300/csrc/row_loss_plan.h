@@ -35,21 +35,19 @@ constexpr int kMaxTile = 64 * 1024;
 // 7 stages 423; K = 1,024 493 and 534.
 constexpr int kFewEntries = 256;
 constexpr int good_stages(int K) { return K > kFewEntries ? 5 : 7; }
-constexpr int kMinTile = 24 * 1024;
+// Bytes that a list of K entries (K = 0: tokens) leaves a tile beside it.
+constexpr int tile_bytes(int K) { return kRingBytes / good_stages(K) - K * kListBytes; }
+static_assert(tile_bytes(kFewEntries) >= 24 * 1024 && tile_bytes(kMaxTopK) >= 24 * 1024, "tiles of fewer bytes are slower");
 
 // Tiles of a row: the whole row up to kMaxTile bytes, else equal parts, in whole 128-byte lines, of
-// which kGoodStages fit the ring beside the teacher's lists of K entries (K = 0: tokens), one less
-// for long lists.
+// which good_stages(K) fit the ring beside their lists.
 struct Tiling {
     int tile_vecs, tiles;
 };
 inline Tiling tile_row(int64_t V, int element_size, int K) {
     const int64_t nv = V * element_size / 16;
     if (nv * 16 <= kMaxTile) return Tiling{(int)((nv + 7) / 8 * 8 > 0 ? (nv + 7) / 8 * 8 : 8), 1};
-    const int stages = good_stages(K);
-    int most = kRingBytes / stages - K * kListBytes;
-    if (most < kMinTile) most = kRingBytes / (stages - 1) - K * kListBytes;
-    const int64_t limit = most / 128 * 8;  // vectors
+    const int64_t limit = tile_bytes(K) / 128 * 8;  // vectors
     const int64_t n = (nv + limit - 1) / limit;
     const int64_t per = ((nv + n - 1) / n + 7) / 8 * 8;
     return Tiling{(int)per, (int)((nv + per - 1) / per)};

@@ -23,6 +23,8 @@ static void plan(long V, int size, int K) {
     const long vecs = V * size / 16;
     check((long)t.tile_vecs * t.tiles >= vecs && (long)t.tile_vecs * (t.tiles - 1) <= vecs, "tiles", V, size, K, 0);
     check((t.tiles == 1) == (tile_row(V, size, 0).tiles == 1), "one tile whatever K", V, size, K, 0);
+    const int few = tile_row(V, size, kFewEntries).tiles, many = tile_row(V, size, kMaxTopK).tiles;
+    check(t.tiles <= (few > many ? few : many), "more sums than the workspace holds", V, size, K, 0);
     const int stages = ring_stages(t, K);
     check(stages >= 2 && stages * stage_bytes(t, K) <= kRingBytes, "stages", V, size, K, 0);
     for (int sms : {1, 2, 76, 152})
