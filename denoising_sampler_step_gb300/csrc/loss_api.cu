@@ -25,7 +25,10 @@ dg_status check_rows(const char *what, const void *logits, int32_t dtype, int64_
     if (V > 0x7ffffff0LL || R > (1LL << 28) || ldl > kMaxElements / (R + 1))
         return fail(DG_ERR_UNSUPPORTED, "%s: V, R or ldl too large", what);
     if (R > 0 && (!aligned16(logits) || (ldl * element_size(dtype)) % 16 != 0))
-        return fail(DG_ERR_UNSUPPORTED, "%s: logits rows must start on 16-byte boundaries", what);
+        return fail(DG_ERR_UNSUPPORTED,
+                    "%s: logits rows must start on 16-byte boundaries: pad the row stride to a multiple of %d "
+                    "elements (V stays; columns at V and past it are not read)",
+                    what, 16 / element_size(dtype));
     return DG_OK;
 }
 
@@ -37,7 +40,9 @@ dg_status check_grad(const char *what, const void *logits, int32_t dtype, int64_
     if (ldg < V) return fail(DG_ERR_INVALID_ARG, "%s: need ldg >= V", what);
     if (ldg > kMaxElements / (R + 1)) return fail(DG_ERR_UNSUPPORTED, "%s: ldg too large", what);
     if (!aligned16(grad) || (ldg * size) % 16 != 0)
-        return fail(DG_ERR_UNSUPPORTED, "%s: grad rows must start on 16-byte boundaries", what);
+        return fail(DG_ERR_UNSUPPORTED,
+                    "%s: grad rows must start on 16-byte boundaries: pad the row stride to a multiple of %d elements",
+                    what, 16 / element_size(dtype));
     if (grad == logits && (ldg == ldl || R <= 1)) return DG_OK;
     const uintptr_t x0 = reinterpret_cast<uintptr_t>(logits), g0 = reinterpret_cast<uintptr_t>(grad);
     const uintptr_t x1 = x0 + (uintptr_t)(((R - 1) * ldl + V) * size);
