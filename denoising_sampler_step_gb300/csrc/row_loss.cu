@@ -15,8 +15,8 @@
 // leaves the memory idle.  Rows of up to kMaxTile bytes are one tile and need no exchange.
 //
 // Measured, 1,024 rows of 262,144 entries, against a plain copy's 6,780 GB/s: policy loss fp32 forward
-// 101%, step 89%, backward 97%; bf16 82%, 85%, 89%; distillation, K = 64, fp32 94%, 88%, 94%, bf16 74%,
-// 82%, 91%; a step with K = 512 77%, with K = 1,024 64% (each tile's share of the teacher's entries is
+// 101%, step 88%, backward 97%; bf16 82%, 83%, 88%; distillation, K = 64 with the bucket, fp32 94%, 87%, 95%,
+// bf16 74%, 81%, 91%; a step with K = 512 77%, with K = 1,024 64% (each tile's share of the teacher's entries is
 // found by looking at all of them).  What is left in a step: reads and writes that alternate, and in bf16
 // the folding warps, which have twice the entries per byte.
 //

@@ -554,7 +554,10 @@ dg_status dg_sampler_loop_step_e4m3(const float *logits, int32_t n_req, int32_t 
  *   A token or index at or past V leaves its row or entry out as well, and dg_get_device_status
  *   reports it (DG_ERR_INVALID_ARG).
  *   Statistics, losses and sums are fp32 or wider whatever dtype is; a bf16 gradient is rounded
- *   once.  Results are bitwise reproducible.  -inf and the type's lowest finite value are allowed
+ *   once.  Exponentials are the hardware's power of two (relative error 2^-22).  Log-sum-exps and the
+ *   losses' terms are within some 1e-7 of their size of the exact ones, up to twice as far as an fp32
+ *   log_softmax's: token log-probabilities take log2(e) / T in two floats (dg_token_logp and dg_preference_loss also
+ *   round ln p once), distillation and the top logits' lse in one.  Results are bitwise reproducible.  -inf and the type's lowest finite value are allowed
  *   in the logits (masked vocabulary); a row whose logits are all -inf has no distribution and
  *   gives NaN.  NaN and +inf logits are undefined in rows that are read.
  */
