@@ -56,9 +56,9 @@ using namespace vocab;
 // has no distribution of its own, and its term is left out.  (Times T below 1: ln p_0 stays a finite fp32 number.)
 constexpr float kMasked = -3.38e38f;
 // q_0 is a difference from 1 of what teacher_lse and the teacher's logits give, each rounded to fp32, and known
-// to about (|teacher_lse| + 4) 2^-22.  Times an ln p_0 below this (a vocabulary masked by, say, -1e4 in teacher
+// to about (|teacher_lse| + 4) 2^-22.  Times an ln p_0 below -87 (a vocabulary masked by, say, -1e4 in teacher
 // and student alike) such a rest would be a loss of its own, so there it counts as 0.
-constexpr float kTailFloor = -87.0f, kExpTailFloor = 1.64581145e-38f;  // and e to it
+constexpr float kTailFloor = 0x1p60f * 1.64581143e-38f;  // (2^60 e^-87: see bucket_terms)
 
 struct Plan {
     int stages;      // of the ring
@@ -155,12 +155,13 @@ __device__ __forceinline__ float teacher_terms(const RowLossArgs &a, const MaxSu
 // there, and the gradient is coef p_v (M - q_0 / p_0), M = sum of q_k and q_0, without that quotient (and exactly
 // 0 where p_0 = q_0 = 1).  Returns what of q_rest counts as q_0.  (One division, and not the exact one, on the way
 // to a published row: with two exact ones a step of 2,048 x 262,144 fp32 rows, K = 128, took 645 us, not 632.)
-// far: ln p_0 is below kTailFloor.
-__device__ __forceinline__ float bucket_terms(const RowLossArgs &a, float teacher_lse, bool far, float part, float s,
+// c = log2(e) / T.  p_0 against its floor in 2^60ths: part itself has vanished some ln(V) above it.
+__device__ __forceinline__ float bucket_terms(const RowLossArgs &a, float c, float teacher_lse, float part, float s,
                                               float tail_m, float tail_s, float q_rest, RowClose *cl) {
     cl->base = cl->m;
     cl->scale = cl->coef * cl->mass * cl->inv_s;
     if (!a.teacher_lse || !(tail_m > kMasked * fminf(a.T, 1.0f))) return 0.0f;
+    const bool far = ex2_approx(fmaf(tail_m - cl->m, c, 60.0f)) * tail_s < kTailFloor * s;
     if (far && q_rest <= (fabsf(teacher_lse) + 4.0f) * 0x1p-22f) q_rest = 0.0f;
     cl->mass += q_rest;
     cl->base = never_zero(tail_m);
@@ -621,7 +622,7 @@ __global__ void __launch_bounds__(Roles<HEAD, PASS, SPLIT>::kThreads, 1)
                 cl.base = cl.m;
             } else {
                 part = rest.s * exp_below(rest.m, cl.m, sums_c);
-                q_rest = bucket_terms(a, teacher_lse, part < kExpTailFloor * st.s, part, st.s, rest.m, rest.s, q_rest, &cl);
+                q_rest = bucket_terms(a, c, teacher_lse, part, st.s, rest.m, rest.s, q_rest, &cl);
             }
             if (kBackward) {
                 if (SPLIT) {
@@ -847,7 +848,7 @@ __global__ void __launch_bounds__(32 * kCloseWarps) row_close_kernel(const RowLo
     const float lse = a.lse[row], logp0 = a.teacher_lse ? a.tail_logp[row] : 0.0f;
     const float tail = lse + logp0, tail_m = tail * a.T;
     const float lost = fmaf(tail, a.T, -tail_m) / a.T + lost_by_sum(lse, logp0, tail);
-    bucket_terms(a, teacher_lse, logp0 < kTailFloor, expf(logp0), 1.0f, tail_m, expf(lost), q_rest, &cl);
+    bucket_terms(a, c, teacher_lse, expf(logp0), 1.0f, tail_m, expf(lost), q_rest, &cl);
     if (lane == 0) rows[row] = cl;
 }
 

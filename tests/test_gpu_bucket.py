@@ -139,3 +139,26 @@ def test_a_mask_that_teacher_and_student_share(B, low, dtype):
     near(o["grad"], np.zeros((4, V)), 4 * EQ, "gradient")
     g = B.dg_distill_loss_backward(x, i32(idx), f32(t), o["lse"], teacher_lse=f32(lse), tail_logp=o["tail_logp"])
     near(g, np.zeros((4, V)), 4 * EQ, "gradient from the saved values")
+
+
+@pytest.mark.parametrize("target,kept", [(-80.0, True), (-86.0, True), (-88.0, False), (-100.0, False)])
+def test_a_small_rest_counts_down_to_its_floor(B, target, kept):
+    """q_0 = 15 u, which roundings of 1 - q could be: a term of the loss above ln p_0 = -87, also where every entry of
+    the bucket is below fp32's range on its own, and none below."""
+    V = 262144
+    x = np.full((2, V), target - np.log(V - 1))
+    x[0, 5] = x[1, V - 1] = 0.0
+    x, xf = place(x, "f32")
+    idx, t, lse = np.array([[5], [V - 1]], np.int32), np.full((2, 1), -15 * U, np.float32), np.zeros(2, np.float32)
+    want = L.distill_loss(xf, idx, t, lse)
+    assert (want["loss"] > 4e-5).all() if kept else (np.abs(want["loss"]) < 1e-5).all()
+    # q_0 is off by the power of two's 4 u and two roundings, times |ln q_0 - ln p_0|
+    tol = 6 * U * (14 + np.abs(target)) + 8 * U if kept else 30 * U
+    o = B.dg_distill_loss(x, i32(idx), f32(t), f32(lse), grad=True)
+    near(o["loss"], want["loss"], tol, "loss")
+    g = B.dg_distill_loss_backward(x, i32(idx), f32(t), o["lse"], teacher_lse=f32(lse), tail_logp=o["tail_logp"])
+    for v in (o["grad"], g):
+        near(v.double().sum(1), np.zeros(2), 8 * U, "sum of the gradient")
+        tail = v.double().clone()
+        tail[[0, 1], idx[:, 0].tolist()] = 0
+        near(tail.sum(1), [-15 * U if kept else 0.0] * 2, 7 * U if kept else U, "the bucket's gradient")
