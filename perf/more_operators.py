@@ -1,0 +1,366 @@
+"""The operators on either side of a model: between the canvas and its first layer, and between its
+last layer and the logits, as cases to be timed and compared.
+
+Three operators share one hidden stream [R, d] (fp32 or bf16) and one embedding table [V, d]:
+
+* embed  the rows of the table at the canvas' tokens times gamma (fp32 or bf16 entries, or E4M3 codes
+         with one scale per row; a negative token is padding, its row 0), and the table's gradient from
+         that of the rows, a sum over each token's positions ("gradient"), which overwrites a whole
+         gradient or adds to one ("accumulate");
+* norm   h = x + residual, y = h / rms(h) (offset + weight), y in fp32, bf16 or as E4M3 codes with one
+         scale per row, and its gradient with that of the weight;
+* head   logits from E4M3 codes on both sides, with one scale per position and one per vocabulary row.
+
+A case's "pass" says which direction one run() takes.  `own` selects the framework's calls; otherwise the
+operators run in a plain form of elementary torch operations in fp32.
+"""
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "e4m3": torch.uint8}
+SIZE = {"f32": 4, "bf16": 2, "e4m3": 1}
+EPS = 1e-6
+
+
+# --------------------------------------------------------------------------- cases
+
+def listed():
+    return [
+        # the tiny configuration's 16 positions: launch latency
+        dict(name="embed tiny", op="embed", R=16, V=4096, d=256, table="bf16", dtype="bf16", tokens="uniform",
+             padded=0.0, **{"pass": "forward"}),
+        # 32 canvases of 256 positions from the 8-bit table
+        dict(name="embed batch", op="embed", R=8192, V=262144, d=2816, table="e4m3", dtype="bf16", tokens="uniform",
+             padded=0.0, **{"pass": "forward"}),
+        # one canvas added to a gradient that micro-batches share
+        dict(name="embed gradient canvas", op="embed", R=256, V=262144, d=2816, table="f32", dtype="f32",
+             tokens="uniform", padded=0.0, accumulate=True, **{"pass": "gradient"}),
+        # 32 canvases in the training type, half of the positions one and the same token, a gradient from
+        # nothing: every row of it is written
+        dict(name="embed gradient batch", op="embed", R=8192, V=262144, d=2816, table="bf16", dtype="bf16",
+             tokens="masked", padded=0.0, accumulate=False, **{"pass": "gradient"}),
+        # a packed batch of text with padding, odd sizes throughout
+        dict(name="embed gradient ragged", op="embed", R=20001, V=32003, d=1001, table="f32", dtype="bf16",
+             tokens="text", padded=0.1, accumulate=True, **{"pass": "gradient"}),
+        # one position while serving: latency counts
+        dict(name="norm one position", op="norm", R=1, d=2816, dtype="bf16", residual="bf16", out="e4m3",
+             offset=1.0, **{"pass": "forward"}),
+        # 32 canvases, the residual stream carried in fp32, 8 bits for the head
+        dict(name="norm batch", op="norm", R=8192, d=2816, dtype="bf16", residual="f32", out="e4m3", offset=1.0,
+             **{"pass": "forward"}),
+        # the same batch in the training type, the residual stream's own gradient added
+        dict(name="norm gradient batch", op="norm", R=8192, d=2816, dtype="bf16", residual="bf16", out="bf16",
+             offset=1.0, **{"pass": "gradient"}),
+        # odd sizes in fp32, no residual stream
+        dict(name="norm gradient ragged", op="norm", R=3001, d=1153, dtype="f32", residual="none", out="f32",
+             offset=0.0, **{"pass": "gradient"}),
+        # one position while serving: the table is read for a single row of logits
+        dict(name="head one position", op="head", R=1, V=262144, d=2816, out="f32", **{"pass": "forward"}),
+        # one canvas
+        dict(name="head canvas", op="head", R=256, V=262144, d=2816, out="f32", **{"pass": "forward"}),
+        # eight canvases, logits in the losses' type: the largest
+        dict(name="head batch", op="head", R=2048, V=262144, d=2816, out="bf16", **{"pass": "forward"}),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["embed", "embed", "norm", "norm", "head"])
+    if op == "norm":
+        R = _log_int(rng, 1, 8192)
+        back = rng.random() < 0.5
+        dtype = rng.choice(["f32", "bf16"])
+        return {**dict(op=op, R=R, d=_log_int(rng, 64, min(8192, 8192 * 2816 // R)), dtype=dtype,
+                       residual=rng.choice(["none", dtype, "f32"]),
+                       out=dtype if back else rng.choice(["f32", "bf16", "e4m3"]), offset=rng.choice([0.0, 1.0])),
+                "pass": "gradient" if back else "forward"}
+    if op == "head":
+        R = _log_int(rng, 1, 2048)
+        return {**dict(op=op, R=R, V=_log_int(rng, 1000, 262144), d=_log_int(rng, 64, 2816),
+                       out=rng.choice(["f32", "bf16"]) if R <= 1024 else "bf16"), "pass": "forward"}
+    back = rng.random() < 0.6
+    c = dict(op=op, R=_log_int(rng, 1, 20001), V=_log_int(rng, 1000, 262144), d=_log_int(rng, 64, 1024),
+             table=rng.choice(["f32", "bf16"] if back else ["f32", "bf16", "e4m3"]), dtype=rng.choice(["f32", "bf16"]),
+             tokens=rng.choice(["uniform", "text", "masked"]), padded=rng.choice([0.0, round(rng.uniform(0.02, 0.5), 2)]))
+    if back:
+        c["accumulate"] = rng.random() < 0.5
+    return {**c, "pass": "gradient" if back else "forward"}
+
+
+# --------------------------------------------------------------------------- inputs
+
+def _gamma(d):
+    """The embedding's normaliser: the square root of the hidden size as a bf16 number."""
+    return float(torch.tensor(math.sqrt(d)).bfloat16())
+
+
+def _padded(x, dtype):
+    """x in storage whose rows start on 16-byte boundaries."""
+    R, n = x.shape
+    per = 16 // SIZE[dtype]
+    buf = torch.zeros(R, (n + per - 1) // per * per, dtype=DTYPES[dtype], device="cuda")
+    buf[:, :n] = x
+    return buf[:, :n]
+
+
+def _empty(R, n, dtype):
+    per = 16 // SIZE[dtype]
+    return torch.zeros(R, (n + per - 1) // per * per, dtype=DTYPES[dtype], device="cuda")[:, :n]
+
+
+def _codes(g, R, n):
+    """E4M3 codes of numbers whose rows reach 448 somewhere, as a quantiser by rows leaves them."""
+    out = _empty(R, n, "e4m3")
+    step = max(1, (1 << 26) // n)
+    for i in range(0, R, step):
+        x = torch.randn(min(step, R - i), n, generator=g, device="cuda")
+        x *= 448.0 / x.abs().amax(1, keepdim=True)
+        out[i:i + step] = x.clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8)
+    return out
+
+
+def _tokens(g, case):
+    R, V, kind = case["R"], case["V"], case["tokens"]
+    if kind == "text":  # frequencies falling like 1 / rank, over a shuffled vocabulary
+        rank = torch.exp(torch.rand(R, generator=g, device="cuda") * math.log(V + 1.0)).long().clamp(1, V) - 1
+        tok = torch.randperm(V, generator=g, device="cuda")[rank]
+    else:
+        tok = torch.randint(V, (R,), generator=g, device="cuda")
+    if kind == "masked":  # about half of the positions hold one token
+        one = torch.randint(V, (1,), generator=g, device="cuda")
+        tok = torch.where(torch.rand(R, generator=g, device="cuda") < 0.5, one, tok)
+    pad = torch.rand(R, generator=g, device="cuda") < case["padded"]
+    return torch.where(pad, -1, tok).to(torch.int32)
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    R, d, op, back = case["R"], case["d"], case["op"], case["pass"] == "gradient"
+    s = {"case": case}
+    rnd = lambda *shape: torch.randn(*shape, generator=g, device="cuda")  # noqa: E731
+    if op == "embed":
+        V = case["V"]
+        s["token"] = _tokens(g, case)
+        if back:
+            s["grad"] = _padded(0.02 * rnd(R, d), case["dtype"])
+            s["table_grad"] = _empty(V, d, case["table"])
+            if case["accumulate"]:  # what earlier micro-batches left there
+                s["table_grad"].copy_(0.01 * rnd(1, d) * (1.0 + rnd(V, 1)))
+            return s
+        if case["table"] == "e4m3":
+            s["table"] = _codes(g, V, d)
+            s["scale"] = 1e-4 + 2e-4 * torch.rand(V, generator=g, device="cuda")
+        else:
+            s["table"] = _empty(V, d, case["table"])
+            s["table"].copy_(0.02 * rnd(V, d))
+        s["out"] = _empty(R, d, case["dtype"])
+    elif op == "norm":
+        # rows of sizes that differ, with a few columns far larger than the others
+        size = torch.exp(rnd(R, 1)) * torch.where(torch.rand(1, d, generator=g, device="cuda") < 0.01, 20.0, 1.0)
+        s["x"] = _padded(size * rnd(R, d), case["dtype"])
+        s["weight"] = (1.0 - case["offset"] + 0.3 * rnd(d)).to(DTYPES["f32" if case["dtype"] == "f32" else "bf16"])
+        if back:
+            s["rstd"] = (s["x"].float().square().mean(1) + EPS).rsqrt()
+            s["grad"] = _padded(rnd(R, d), case["out"])
+            if case["residual"] != "none":
+                s["grad_hidden"] = _padded(rnd(R, d), case["residual"])
+            s["out"] = {"grad": _empty(R, d, case["dtype"]), "grad_weight": torch.zeros_like(s["weight"])}
+            return s
+        s["out"] = {"out": _empty(R, d, case["out"]), "rstd": torch.zeros(R, device="cuda")}
+        if case["residual"] != "none":
+            s["residual"] = _padded(size * rnd(R, d), case["residual"])
+            s["out"]["hidden"] = _empty(R, d, case["residual"])
+        if case["out"] == "e4m3":
+            s["out"]["scale"] = torch.zeros(R, device="cuda")
+    else:
+        V = case["V"]
+        s["x"], s["table"] = _codes(g, R, d), _codes(g, V, d)
+        s["x_scale"] = 0.01 + 0.01 * torch.rand(R, generator=g, device="cuda")
+        s["scale"] = 1e-4 + 2e-4 * torch.rand(V, generator=g, device="cuda")
+        s["out"] = _empty(R, V, case["out"])
+    return s
+
+
+# --------------------------------------------------------------------------- one pass
+
+def run(s):
+    c = s["case"]
+    if own:
+        return _run_own(s, c)
+    if c["op"] == "embed":
+        return _plain_embed(s, c) if c["pass"] == "forward" else _plain_embed_gradient(s, c)
+    if c["op"] == "norm":
+        return _plain_norm(s, c) if c["pass"] == "forward" else _plain_norm_gradient(s, c)
+    return _plain_head(s, c)
+
+
+def _values(o):
+    """The codes as the values they stand for, without their scale."""
+    return {k: v.view(torch.float8_e4m3fn) if v.dtype == torch.uint8 else v for k, v in o.items()}
+
+
+def _run_own(s, c):
+    from denoising_sampler_step_gb300 import binding as B
+
+    if c["op"] == "head":
+        return B.dg_head_e4m3(s["x"], s["x_scale"], s["table"], s["scale"], out=s["out"])
+    if c["op"] == "norm":
+        if c["pass"] == "forward":
+            return _values(B.dg_rms_norm(s["x"], s["weight"], residual=s.get("residual"), eps=EPS,
+                                         weight_offset=c["offset"], out=s["out"]))
+        if "ws" not in s:
+            s["ws"] = B.norm_workspace(c["R"], c["d"], s["x"].device)
+        return B.dg_rms_norm_backward(s["grad"], s["x"], s["rstd"], s["weight"], weight_offset=c["offset"],
+                                      grad_hidden=s.get("grad_hidden"), ws=s["ws"], out=s["out"])
+    if c["pass"] == "forward":
+        return B.dg_token_embed(s["table"], s["token"], _gamma(c["d"]), scale=s.get("scale"), out=s["out"])
+    if "ws" not in s:
+        s["ws"] = B.embed_workspace(c["R"], c["V"], c["d"], s["token"].device)
+    return B.dg_token_embed_backward(s["grad"], s["token"], c["V"], _gamma(c["d"]), accumulate=c["accumulate"],
+                                     ws=s["ws"], out=s["table_grad"])
+
+
+def _plain_embed(s, c):
+    on, tok = s["token"] >= 0, s["token"].clamp(min=0).long()
+    rows = s["table"][tok]
+    if c["table"] == "e4m3":
+        rows = rows.view(torch.float8_e4m3fn).float() * s["scale"][tok][:, None]
+    rows = rows.float() * _gamma(c["d"])
+    return torch.where(on[:, None], rows, 0.0).to(DTYPES[c["dtype"]])
+
+
+def _plain_embed_gradient(s, c):
+    on, tok = s["token"] >= 0, s["token"].clamp(min=0).long()
+    rows = torch.where(on[:, None], s["grad"].float(), 0.0)
+    total = torch.zeros(c["V"], c["d"], device="cuda").index_add_(0, tok, rows).mul_(_gamma(c["d"]))
+    if c["accumulate"]:
+        total += s["table_grad"]
+    return s["table_grad"].copy_(total)
+
+
+def _plain_norm(s, c):
+    h = s["x"].float()
+    o = {}
+    if c["residual"] != "none":
+        h = h + s["residual"].float()
+        o["hidden"] = h.to(DTYPES[c["residual"]])
+    o["rstd"] = 1.0 / ((h * h).mean(1) + EPS).sqrt()
+    y = h * o["rstd"][:, None] * (c["offset"] + s["weight"].float())
+    if c["out"] == "e4m3":
+        o["scale"] = y.abs().amax(1) / 448.0
+        y = (y / o["scale"][:, None]).clamp(-448.0, 448.0)
+        o["out"] = y.to(torch.float8_e4m3fn)
+    else:
+        o["out"] = y.to(DTYPES[c["out"]])
+    return o
+
+
+def _plain_norm_gradient(s, c):
+    g = s["grad"].float()
+    xh = s["x"].float() * s["rstd"][:, None]
+    gw = g * (c["offset"] + s["weight"].float())
+    dh = s["rstd"][:, None] * (gw - xh * (gw * xh).mean(1, keepdim=True))
+    if c["residual"] != "none":
+        dh = dh + s["grad_hidden"].float()
+    return {"grad": dh.to(DTYPES[c["dtype"]]), "grad_weight": (g * xh).sum(0).to(s["weight"].dtype)}
+
+
+def _plain_head(s, c):
+    x, w = s["x"].view(torch.float8_e4m3fn).float(), s["table"].view(torch.float8_e4m3fn).float()
+    return ((x @ w.T) * s["scale"] * s["x_scale"][:, None]).to(DTYPES[c["out"]])
+
+
+# --------------------------------------------------------------------------- cost
+
+def _present(case):
+    """How many positions hold a token, and about how many different ones."""
+    n = case["R"] * (1.0 - case["padded"])
+    V = case["V"]
+    if case["tokens"] == "text":
+        # a token of rank k has share ln(1 + 1/k) / ln(V + 1)
+        k = torch.arange(1, V + 1, dtype=torch.float64)
+        share = torch.log1p(1.0 / k) / math.log(V + 1.0)
+        return n, float((1.0 - (1.0 - share) ** n).sum())
+    free = n if case["tokens"] == "uniform" else 0.5 * n
+    return n, min(n, V * (1.0 - (1.0 - 1.0 / V) ** free) + (0.0 if case["tokens"] == "uniform" else 1.0))
+
+
+def work(case):
+    R, d = case["R"], case["d"]
+    if case["op"] == "embed":
+        n, rows = _present(case)
+        t, e = SIZE[case["table"]], SIZE[case["dtype"]]
+        if case["pass"] == "forward":
+            return {"bytes": rows * (d * t + 4) + R * (d * e + 4), "flops": 2 * n * d}
+        table = 2 * rows * d * t if case["accumulate"] else case["V"] * d * t
+        return {"bytes": n * d * e + 4 * R + table, "flops": n * d}
+    if case["op"] == "norm":
+        x, r, o = SIZE[case["dtype"]], SIZE.get(case["residual"], 0), SIZE[case["out"]]
+        w = 4 if case["dtype"] == "f32" else 2
+        if case["pass"] == "forward":
+            return {"bytes": R * d * (x + 2 * r + o) + 8 * R + w * d, "flops": 8 * R * d}
+        return {"bytes": R * d * (2 * x + r + o) + 4 * R + 2 * w * d, "flops": 12 * R * d}
+    V = case["V"]
+    return {"bytes": (R + V) * (d + 4) + R * V * SIZE[case["out"]], "flops": 2 * R * V * d}
+
+
+# --------------------------------------------------------------------------- 64 bits
+
+def _decode(codes):
+    """E4M3 codes by the format's definition: sign, four bits of exponent (bias 7), three of mantissa."""
+    c = torch.arange(256, device="cuda")
+    e, m = (c >> 3) & 15, (c & 7).double()
+    v = torch.where(e == 0, m / 8.0 * 2.0 ** -6, (1.0 + m / 8.0) * torch.exp2(e.double() - 7.0))
+    return torch.where(c >= 128, -v, v)[codes.long()]
+
+
+def exact(case, seed):
+    """The operators from their definitions in float64; gradients by differentiating them."""
+    s = prepare(case, seed)
+    R, d, back = case["R"], case["d"], case["pass"] == "gradient"
+    if case["op"] == "embed":
+        tok = s["token"].long()
+        at = torch.nonzero(tok >= 0)[:, 0]
+        if back:
+            total = torch.zeros(case["V"], d, dtype=torch.float64, device="cuda")
+            total.index_put_((tok[at],), s["grad"].double()[at] * _gamma(d), accumulate=True)
+            return total.add_(s["table_grad"]) if case["accumulate"] else total
+        out = torch.zeros(R, d, dtype=torch.float64, device="cuda")
+        rows = s["table"][tok[at]]
+        rows = _decode(rows) * s["scale"].double()[tok[at], None] if case["table"] == "e4m3" else rows.double()
+        out[at] = _gamma(d) * rows
+        return out
+    if case["op"] == "norm":
+        w = s["weight"].double() + case["offset"]
+        if back:
+            # the saved rstd is what the definition says of h
+            h, w = s["x"].double().requires_grad_(True), w.requires_grad_(True)
+            y = h * (h.square().mean(1, keepdim=True) + EPS) ** -0.5 * w
+            gh, gw = torch.autograd.grad((y * s["grad"].double()).sum(), (h, w))
+            if case["residual"] != "none":
+                gh = gh + s["grad_hidden"].double()
+            return {"grad": gh, "grad_weight": gw}
+        h, o = s["x"].double(), {}
+        if case["residual"] != "none":
+            h = h + s["residual"].double()
+            o["hidden"] = h
+        o["rstd"] = (h.square().sum(1) / d + EPS) ** -0.5
+        y = h * w * o["rstd"][:, None]
+        if case["out"] == "e4m3":
+            o["scale"] = y.abs().max(1).values / 448.0
+            y = y / o["scale"][:, None]
+        o["out"] = y
+        return o
+    out = torch.empty(R, case["V"], dtype=torch.float64, device="cuda")
+    x = _decode(s["x"]) * s["x_scale"].double()[:, None]
+    for i in range(0, case["V"], 16384):
+        w = slice(i, min(case["V"], i + 16384))
+        out[:, w] = x @ (_decode(s["table"][w]) * s["scale"][w].double()[:, None]).T
+    return out
