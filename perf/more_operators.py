@@ -238,11 +238,13 @@ def _plain_embed(s, c):
 
 def _plain_embed_gradient(s, c):
     on, tok = s["token"] >= 0, s["token"].clamp(min=0).long()
-    rows = torch.where(on[:, None], s["grad"].float(), 0.0)
-    total = torch.zeros(c["V"], c["d"], device="cuda").index_add_(0, tok, rows).mul_(_gamma(c["d"]))
-    if c["accumulate"]:
-        total += s["table_grad"]
-    return s["table_grad"].copy_(total)
+    rows = torch.where(on[:, None], s["grad"].float(), 0.0) * _gamma(c["d"])
+    if c["table"] == "f32":
+        total = s["table_grad"] if c["accumulate"] else s["table_grad"].zero_()
+        return total.index_add_(0, tok, rows)
+    # a bf16 gradient is summed in fp32 and rounded once
+    total = s["table_grad"].float() if c["accumulate"] else torch.zeros(c["V"], c["d"], device="cuda")
+    return s["table_grad"].copy_(total.index_add_(0, tok, rows))
 
 
 def _plain_norm(s, c):
