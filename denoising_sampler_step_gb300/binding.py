@@ -117,9 +117,28 @@ lib.dg_policy_loss.restype = ctypes.c_int
 lib.dg_preference_loss.argtypes = _ROWS + [_p, _p, _p, _i32, _f32, _f32, _f32] + [_p] * 8 + [_i64, _p, _sz, _p]
 lib.dg_preference_loss.restype = ctypes.c_int
 
-# element types of the loss calls' logits and gradients (dg_dtype)
-DG_F32, DG_BF16 = 0, 1
+lib.dg_token_embed.argtypes = [_p, _i32, _p, _i64, _i64, _i64, _i64, _i64, _i64, _p, _i64, _f32, _p, _i32, _i64, _p]
+lib.dg_token_embed.restype = ctypes.c_int
+lib.dg_token_embed_backward.argtypes = [_p, _i32, _i64, _i64, _i64, _p, _i64, _i64, _i64, _f32, _p, _i32, _i64, _i64,
+                                        _i32, _p, _sz, _p]
+lib.dg_token_embed_backward.restype = ctypes.c_int
+lib.dg_token_embed_backward_workspace_size.argtypes = [_i64, _i64, _i64]
+lib.dg_token_embed_backward_workspace_size.restype = _sz
+lib.dg_rms_norm.argtypes = [_p, _i32, _i64, _i64, _i64, _p, _i32, _i64, _p, _i32, _f32, _f32, _p, _i32, _i64, _p, _i32,
+                            _i64, _p, _p, _p]
+lib.dg_rms_norm.restype = ctypes.c_int
+lib.dg_rms_norm_backward.argtypes = [_p, _i32, _i64, _i64, _i64, _p, _i32, _i64, _p, _p, _i32, _f32, _p, _i32, _i64, _p,
+                                     _i64, _p, _p, _sz, _p]
+lib.dg_rms_norm_backward.restype = ctypes.c_int
+lib.dg_rms_norm_backward_workspace_size.argtypes = [_i64, _i64]
+lib.dg_rms_norm_backward_workspace_size.restype = _sz
+lib.dg_head_e4m3.argtypes = [_p, _i64, _p, _i64, _i64, _p, _p, _i64, _i64, _p, _i32, _i64, _p]
+lib.dg_head_e4m3.restype = ctypes.c_int
+
+# element types of logits, gradients and the hidden stream's matrices (dg_dtype)
+DG_F32, DG_BF16, DG_E4M3 = 0, 1, 2
 _DTYPE = {torch.float32: DG_F32, torch.bfloat16: DG_BF16}
+_DTYPE_CODES = {**_DTYPE, torch.uint8: DG_E4M3}
 
 STATUS = {0: "DG_OK", 1: "DG_ERR_INVALID_ARG", 2: "DG_ERR_UNSUPPORTED", 3: "DG_ERR_CUDA", 4: "DG_ERR_TIMEOUT"}
 
@@ -863,3 +882,209 @@ def dg_preference_loss(logits: torch.Tensor, token: torch.Tensor, ref_logp: torc
                                   _vec(o["dlogp"], R, f32, dev, "dlogp"), g, ldg, ws_ptr, ws_bytes, _stream(stream)),
            "dg_preference_loss")
     return o
+
+
+# --------------------------------------------------------------------------- the hidden stream
+#
+# Common to the calls below: matrices [R, d] in fp32 or bf16 with unit column stride and any row stride;
+# E4M3 codes are uint8 and go with a contiguous fp32 vector of scales.  All tensors are on the current
+# device; `out` holds preallocated outputs, and the ones it lacks are allocated.
+
+def _matrix(t: torch.Tensor, R: int, d: int, name: str, device, types=_DTYPE) -> tuple:
+    """(pointer, dtype code, row stride) of an [R, d] matrix on `device`."""
+    code = types.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} has type {t.dtype}: need one of {', '.join(map(str, types))}")
+    if t.shape != (R, d) or (d > 1 and t.stride(1) != 1) or t.device != device:
+        raise ValueError(f"{name} must be [{R}, {d}] with unit column stride on {device}, "
+                         f"got {list(t.shape)} with strides {list(t.stride())} on {t.device}")
+    return t.data_ptr(), code, t.stride(0) if R > 1 else (d + 15) // 16 * 16
+
+
+def _here(t: torch.Tensor, name: str):
+    """The device of a matrix whose device the kernels will run on."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, and the kernels would run on the current device, "
+                         f"cuda:{torch._C._cuda_getDevice()}: use torch.cuda.device({name}.device)")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    return t.device
+
+
+def _new_rows(R: int, d: int, dtype, device, stream) -> torch.Tensor:
+    """An uninitialised [R, d] matrix whose rows start on 16-byte boundaries."""
+    per = 16 // dtype.itemsize
+    with _on(stream):
+        return _new((R, (d + per - 1) // per * per), dtype, device)[:, :d]
+
+
+def _scratch(n: int, device, stream) -> torch.Tensor:
+    with _on(stream):
+        return _new((max(16, n) + 15) // 16 * 16, torch.uint8, device)
+
+
+def dg_token_embed_backward_workspace_size(R: int, vocab_len: int, d: int) -> int:
+    return int(lib.dg_token_embed_backward_workspace_size(R, vocab_len, d))
+
+
+def embed_workspace(R: int, vocab_len: int, d: int, device) -> torch.Tensor:
+    """A workspace tensor large enough for dg_token_embed_backward."""
+    return _scratch(dg_token_embed_backward_workspace_size(R, vocab_len, d), device, None)
+
+
+def dg_token_embed(table: torch.Tensor, token: torch.Tensor, gamma: float = 1.0, scale: torch.Tensor | None = None,
+                   vocab_start: int = 0, vocab_end: int | None = None, V: int | None = None,
+                   out: torch.Tensor | None = None, dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
+    """gamma times the table's rows at `token` [R] (int32; negative: padding, a row of zeros) -> [R, d].
+    table: fp32 or bf16 [rows_pad, d], or E4M3 codes with the row scales `scale`; row j is vocabulary entry
+    vocab_start + j (the whole table by default), and tokens outside [vocab_start, vocab_end) give zeros.
+    dtype: of a new output (default: the table's, bf16 for codes)."""
+    device = _here(table, "table")
+    rows, d = table.shape
+    vocab_end = vocab_start + rows if vocab_end is None else vocab_end
+    V = vocab_end if V is None else V
+    R = token.shape[0] if token.dim() == 1 else -1
+    tok = _vec(token, R, torch.int32, device, "token")
+    tp, tc, ldw = _matrix(table, rows, d, "table", device, _DTYPE_CODES)
+    if out is None:
+        dtype = dtype if dtype is not None else torch.bfloat16 if tc == DG_E4M3 else table.dtype
+        out = _new_rows(R, d, dtype, device, stream)
+    op, oc, ldo = _matrix(out, R, d, "out", device)
+    _check(lib.dg_token_embed(tp, tc, _vec(scale, rows, torch.float32, device, "scale"), V, vocab_start, vocab_end,
+                              rows, ldw, d, tok, R, gamma, op, oc, ldo, _stream(stream)), "dg_token_embed")
+    return out
+
+
+def dg_token_embed_backward(grad: torch.Tensor, token: torch.Tensor, V: int, gamma: float = 1.0,
+                            vocab_start: int = 0, vocab_end: int | None = None, accumulate: bool = False,
+                            ws: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                            dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
+    """The gradient [rows, d] of dg_token_embed's table (fp32 or bf16) from that of its rows [R, d]: every row
+    of [vocab_start, vocab_end) is written, or with accumulate=True the sums are added to `out`.
+    dtype: of a new gradient (default: grad's)."""
+    device = _here(grad, "grad")
+    R, d = grad.shape
+    vocab_end = V if vocab_end is None else vocab_end
+    gp, gc, ldg = _matrix(grad, R, d, "grad", device)
+    tok = _vec(token, R, torch.int32, device, "token")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs `out`, the gradient to add to")
+        out = _new_rows(max(0, vocab_end - vocab_start), d, grad.dtype if dtype is None else dtype, device, stream)
+    rows = out.shape[0]
+    tp, tc, ldt = _matrix(out, rows, d, "out", device)
+    if ws is None and R > 0:
+        ws = _scratch(dg_token_embed_backward_workspace_size(R, max(0, vocab_end - vocab_start), d), device, stream)
+    wp, wn = (None, 0) if ws is None else _memory(ws, device)
+    _check(lib.dg_token_embed_backward(gp, gc, R, d, ldg, tok, V, vocab_start, vocab_end, gamma, tp, tc, rows, ldt,
+                                       bool(accumulate), wp, wn, _stream(stream)), "dg_token_embed_backward")
+    return out
+
+
+def dg_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                eps: float = 1e-6, weight_offset: float = 0.0, dtype: torch.dtype | None = None,
+                out: dict | None = None, stream=None) -> dict:
+    """h = x + residual, y = h / rms(h) * (weight_offset + weight) -> dict out (y), rstd [R], with a residual
+    hidden (h), with dtype=torch.uint8 scale [R] beside the E4M3 codes in out.
+    dtype: of a new out (default: x's); hidden has the residual's type.  `out` may hold x or residual themselves
+    as hidden or as out: they are replaced."""
+    device = _here(x, "x")
+    R, d = x.shape
+    xp, xc, ldx = _matrix(x, R, d, "x", device)
+    o = {} if out is None else out
+    y = o.get("out")
+    if y is None:
+        y = o["out"] = _new_rows(R, d, x.dtype if dtype is None else dtype, device, stream)
+    yp, yc, ldy = _matrix(y, R, d, "out", device, _DTYPE_CODES)
+    rp = hp = sp = wp = None
+    rc = ldr = hc = ldh = wc = 0
+    if residual is not None:
+        rp, rc, ldr = _matrix(residual, R, d, "residual", device)
+        if "hidden" not in o:
+            o["hidden"] = _new_rows(R, d, residual.dtype, device, stream)
+    if o.get("hidden") is not None:
+        hp, hc, ldh = _matrix(o["hidden"], R, d, "hidden", device)
+    if "rstd" not in o:
+        with _on(stream):
+            o["rstd"] = _new(R, torch.float32, device)
+    if yc == DG_E4M3:
+        if "scale" not in o:
+            with _on(stream):
+                o["scale"] = _new(R, torch.float32, device)
+        sp = _vec(o["scale"], R, torch.float32, device, "scale")
+    if weight is not None:
+        wc = _DTYPE.get(weight.dtype, -1)
+        wp = _vec(weight, d, weight.dtype, device, "weight")
+    _check(lib.dg_rms_norm(xp, xc, R, d, ldx, rp, rc, ldr, wp, wc, weight_offset, eps, hp, hc, ldh, yp, yc, ldy, sp,
+                           _vec(o["rstd"], R, torch.float32, device, "rstd"), _stream(stream)), "dg_rms_norm")
+    return o
+
+
+def dg_rms_norm_backward_workspace_size(R: int, d: int) -> int:
+    return int(lib.dg_rms_norm_backward_workspace_size(R, d))
+
+
+def norm_workspace(R: int, d: int, device) -> torch.Tensor:
+    """A workspace tensor large enough for dg_rms_norm_backward."""
+    return _scratch(dg_rms_norm_backward_workspace_size(R, d), device, None)
+
+
+def dg_rms_norm_backward(grad: torch.Tensor, hidden: torch.Tensor, rstd: torch.Tensor,
+                         weight: torch.Tensor | None = None, weight_offset: float = 0.0,
+                         grad_hidden: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                         out: dict | None = None, stream=None) -> dict:
+    """Gradients of dg_rms_norm from that of y (and of h: grad_hidden), the hidden and rstd it wrote (without a
+    residual: x) -> dict grad (of x and of residual alike, in hidden's type) and, with a weight, grad_weight (in
+    its type; out={"grad_weight": None} leaves it out).  grad may replace any of the three matrices."""
+    device = _here(grad, "grad")
+    R, d = grad.shape
+    gp, gc, ldg = _matrix(grad, R, d, "grad", device)
+    hp, hc, ldh = _matrix(hidden, R, d, "hidden", device)
+    o = {} if out is None else out
+    if "grad" not in o:
+        o["grad"] = _new_rows(R, d, hidden.dtype, device, stream)
+    if o["grad"].dtype is not hidden.dtype:
+        raise TypeError(f"out['grad'] must have hidden's type, {hidden.dtype}")
+    xp, _, ldx = _matrix(o["grad"], R, d, "out['grad']", device)
+    up = wp = dp = wsp = None
+    uc = ldu = wc = wn = 0
+    if grad_hidden is not None:
+        up, uc, ldu = _matrix(grad_hidden, R, d, "grad_hidden", device)
+    if weight is not None:
+        wc = _DTYPE.get(weight.dtype, -1)
+        wp = _vec(weight, d, weight.dtype, device, "weight")
+        if "grad_weight" not in o:
+            with _on(stream):
+                o["grad_weight"] = _new(d, weight.dtype, device)
+    if o.get("grad_weight") is not None:
+        if weight is None:
+            raise ValueError("grad_weight needs a weight")
+        dp = _vec(o["grad_weight"], d, weight.dtype, device, "grad_weight")
+        if ws is None and R > 0:
+            ws = _scratch(dg_rms_norm_backward_workspace_size(R, d), device, stream)
+        wsp, wn = (None, 0) if ws is None else _memory(ws, device)
+    _check(lib.dg_rms_norm_backward(gp, gc, R, d, ldg, hp, hc, ldh, _vec(rstd, R, torch.float32, device, "rstd"), wp,
+                                    wc, weight_offset, up, uc, ldu, xp, ldx, dp, wsp, wn, _stream(stream)),
+           "dg_rms_norm_backward")
+    return o
+
+
+def dg_head_e4m3(X: torch.Tensor, x_scale: torch.Tensor, Q: torch.Tensor, scale: torch.Tensor,
+                 out: torch.Tensor | None = None, dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
+    """Logits [R, V] = x_scale scale (X Q^T) of E4M3 codes X [R, d] (dg_rms_norm's) and Q [V, d]
+    (dg_quantize_e4m3's), in fp32 or bf16; rows of all three start on 16-byte boundaries."""
+    device = _here(X, "X")
+    R, d = X.shape
+    V = Q.shape[0]
+    codes = {torch.uint8: DG_E4M3}
+    xp, _, ldx = _matrix(X, R, d, "X", device, codes)
+    qp, _, ldq = _matrix(Q, V, d, "Q", device, codes)
+    if out is None:
+        out = _new_rows(R, V, dtype, device, stream)
+    lp, lc, ldl = _matrix(out, R, V, "out", device)
+    _check(lib.dg_head_e4m3(xp, ldx, _vec(x_scale, R, torch.float32, device, "x_scale"), R, d, qp,
+                            _vec(scale, V, torch.float32, device, "scale"), V, ldq, lp, lc, ldl, _stream(stream)),
+           "dg_head_e4m3")
+    return out

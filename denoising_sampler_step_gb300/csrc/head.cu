@@ -1,0 +1,338 @@
+// Logits of the tied 8-bit head: logits[r, v] = sx[r] sw[v] sum_k X[r, k] Q[v, k], both operands E4M3
+// codes, one scale per position and one per vocabulary row (applied to the fp32 sum).
+//
+// The vocabulary is the M side of the product and the positions its N side: a tcgen05 CTA pair
+// (cta_group::2) multiplies 256 vocabulary rows (128 in each CTA) by up to 256 positions (half of them
+// in each CTA's shared memory), K = 32 per instruction, 128 per ring slot.  So a single position costs
+// an N of 32, a table row is read once per 256 positions, and the accumulator's lanes are consecutive
+// vocabulary entries: a warp stores 32 of them per position straight from its registers.  The pairs are
+// persistent: two accumulators in TMEM (2 x 256 columns) let the stores of one tile run under the next
+// tile's product.
+//
+// Bound by HBM up to some 300 positions (table + logits), by the E4M3 MMA rate above.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "dg_common.cuh"
+#include "dg_internal.h"
+#include "hidden.cuh"
+
+namespace dg {
+
+namespace {
+
+constexpr int kTileV = 256;                 // vocabulary rows of a pair's tile
+constexpr int kRowsCta = kTileV / 2;        // of them in each CTA
+constexpr int kMaxTileR = 256;              // positions of a tile
+constexpr int kBlockK = 128;                // codes per ring slot and row: one 128-byte swizzle atom
+constexpr int kWBytes = kRowsCta * kBlockK;
+constexpr int kMaxStages = 12;
+constexpr int kEpilogueWarps = 8;           // two per TMEM lane quarter
+constexpr int kWarpLoad = kEpilogueWarps, kWarpMma = kEpilogueWarps + 1;
+constexpr int kThreads = (kEpilogueWarps + 2) * 32;
+constexpr int kTmemCols = 512;
+constexpr int kSmemLimit = 232448;          // shared memory of a CTA
+constexpr int kBarrierBytes = 512;
+
+struct HeadParams {
+    const float *x_scale, *w_scale;
+    void *logits;
+    int64_t ldl, tiles;
+    int R, V, tile_r, r_tiles, k_blocks, k_tail;  // k_tail: MMAs of the last block
+    int stages, stage_bytes;
+    uint32_t idesc;
+    int stream_table;  // each table byte is read once: leave L2 first
+};
+
+// Instruction descriptor of kind::f8f6f4 with E4M3 A and B, fp32 accumulator, both K-major.
+constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// One arrival, with release at cluster scope, on a barrier of any CTA of the cluster.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void store_logit(float *p, float v) { *p = v; }
+
+// The 32 columns (positions) of a chunk that this lane holds for its vocabulary entry v.
+__device__ __forceinline__ void store_chunk(const HeadParams &p, float *logits, const uint32_t (&acc)[32], int row0, int v,
+                                            float sw) {
+    if (v >= p.V) return;
+    float *dst = logits + (int64_t)row0 * p.ldl + v;
+    const int n = min(32, p.R - row0);
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+        if (c < n) store_logit(dst + c * p.ldl, __uint_as_float(acc[c]) * sw * __ldg(p.x_scale + row0 + c));
+}
+
+// bf16: neighbouring lanes swap a value so that each writes two vocabulary entries of one position
+// (half the stores; rows start on 16-byte boundaries, so the pair is 4-byte aligned).
+__device__ __forceinline__ void store_chunk(const HeadParams &p, __nv_bfloat16 *logits, const uint32_t (&acc)[32],
+                                            int row0, int v, float sw) {
+    const int odd = v & 1, v0 = v - odd;
+    const int n = min(32, p.R - row0);
+    __nv_bfloat16 *dst = logits + (int64_t)(row0 + odd) * p.ldl + v0;
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+        const float s0 = c < n ? __ldg(p.x_scale + row0 + c) : 0.0f;
+        const float s1 = c + 1 < n ? __ldg(p.x_scale + row0 + c + 1) : 0.0f;
+        const float a = __uint_as_float(acc[c]) * sw * s0, b = __uint_as_float(acc[c + 1]) * sw * s1;
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+        if (c + odd < n) {
+            __nv_bfloat16 *q = dst + c * p.ldl;
+            const float lo = odd ? got : a, hi = odd ? b : got;
+            if (v0 + 1 < p.V)
+                *reinterpret_cast<__nv_bfloat162 *>(q) = __floats2bfloat162_rn(lo, hi);
+            else if (v0 < p.V)
+                *q = __float2bfloat16_rn(lo);
+        }
+    }
+}
+
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    head_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const HeadParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem_raw);  // the even CTA's: both CTAs' tiles have landed
+    uint64_t *empty = full + kMaxStages;                      // the slot's products are done
+    uint64_t *acc_full = empty + kMaxStages;                  // a tile's products are done
+    uint64_t *acc_empty = acc_full + 2;                       // the even CTA's: the accumulator has been read
+    uint64_t *drained = acc_empty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const uint32_t ring = (smem_u32(smem_raw) + kBarrierBytes + 1023u) & ~1023u;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&acc_full[b]), 1);
+            mbar_init(smem_u32(&acc_empty[b]), 2 * kEpilogueWarps);
+        }
+        mbar_init(smem_u32(drained), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&tm_x);
+        prefetch_tmap(&tm_w);
+    }
+    __syncwarp();
+    if (warp == 0) tmem_alloc_pair<kTmemCols>(smem_u32(tmem_slot));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    cluster_sync_all();  // the peer's barriers exist before any copy or commit reaches them
+    const uint32_t tmem_base = *tmem_slot;
+    bool ok = true;  // false once this thread gave up on a wait
+
+    if (warp == kWarpLoad) {
+        if (lane == 0) {
+            const uint32_t x_bytes = (uint32_t)(p.tile_r / 2) * kBlockK;
+            const uint32_t lead_full = map_to_cta(smem_u32(&full[0]), 0);
+            const uint64_t w_policy = p.stream_table ? l2_policy_evict_first() : l2_policy_evict_normal();
+            const uint64_t x_policy = l2_policy_evict_normal();
+            int s = 0;
+            uint32_t use = 0;
+            for (int64_t t = pair; t < p.tiles && ok; t += pairs) {
+                const int v0 = (int)(t / p.r_tiles) * kTileV + (int)rank * kRowsCta;
+                const int r0 = (int)(t % p.r_tiles) * p.tile_r + (int)rank * (p.tile_r / 2);
+                for (int k = 0; k < p.k_blocks; ++k) {
+                    if (use > 0 && !mbar_wait(smem_u32(&empty[s]), (use - 1) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * (kWBytes + x_bytes));
+                    const uint32_t at = ring + (uint32_t)s * p.stage_bytes, bar = lead_full + 8u * (uint32_t)s;
+                    tma_load_2d_pair_hint(at, &tm_w, bar, k * kBlockK, v0, w_policy);
+                    tma_load_2d_pair_hint(at + kWBytes, &tm_x, bar, k * kBlockK, r0, x_policy);
+                    if (++s == p.stages) {
+                        s = 0;
+                        ++use;
+                    }
+                }
+            }
+        }
+    } else if (warp == kWarpMma) {
+        if (lane == 0 && rank == 0) {
+            int s = 0, n = 0;
+            uint32_t ph = 0;
+            for (int64_t t = pair; t < p.tiles && ok; t += pairs, ++n) {
+                const int b = n & 1;
+                if (n >= 2 && !mbar_wait_cluster(smem_u32(&acc_empty[b]), (uint32_t)((n >> 1) - 1) & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (uint32_t)b * 256u;
+                for (int k = 0; k < p.k_blocks; ++k) {
+                    if (!mbar_wait_cluster(smem_u32(&full[s]), ph, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t at = ring + (uint32_t)s * p.stage_bytes;
+                    const uint64_t a = smem_desc(at, 16, 1024, 2), x = smem_desc(at + kWBytes, 16, 1024, 2);
+                    const int steps = k + 1 < p.k_blocks ? kBlockK / 32 : p.k_tail;
+                    for (int j = 0; j < steps; ++j)  // 32 bytes further along both operands' rows
+                        umma_e4m3_pair(d_tmem, a + 2 * j, x + 2 * j, p.idesc, (k | j) != 0);
+                    umma_commit_pair(smem_u32(&empty[s]), 3);
+                    if (++s == p.stages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+                if (ok) umma_commit_pair(smem_u32(&acc_full[b]), 3);
+            }
+            if (!ok) {  // products in flight finish before the pair's shared memory is given up
+                umma_commit_pair(smem_u32(drained), 1);
+                drain_wait(smem_u32(drained), 0);
+            }
+        }
+    } else {
+        const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes, and every other chunk of columns
+        const uint32_t lead_empty = map_to_cta(smem_u32(&acc_empty[0]), 0);
+        T *logits = static_cast<T *>(p.logits);
+        int n = 0;
+        for (int64_t t = pair; t < p.tiles; t += pairs, ++n) {
+            const int b = n & 1;
+            const int v = (int)(t / p.r_tiles) * kTileV + (int)rank * kRowsCta + quarter * 32 + lane;
+            const int r0 = (int)(t % p.r_tiles) * p.tile_r;
+            const float sw = v < p.V ? __ldg(p.w_scale + v) : 0.0f;
+            ok = mbar_wait(smem_u32(&acc_full[b]), (uint32_t)(n >> 1) & 1, abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const uint32_t at = tmem_base + (uint32_t)b * 256u + ((uint32_t)(quarter * 32) << 16);
+#pragma unroll 1
+            for (int c = half * 32; c < p.tile_r && r0 + c < p.R; c += 64) {
+                uint32_t acc[32];
+                tmem_ld_32x32b_x32(at + c, acc);
+                tmem_ld_wait();
+                store_chunk(p, logits, acc, r0 + c, v, sw);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(lead_empty + 8u * (uint32_t)b);
+        }
+    }
+
+    __syncthreads();
+    if (*abort_flag) {
+        // loads in flight land within microseconds; the even CTA's barriers count the odd CTA's too
+        const unsigned long long t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+    }
+    tc_fence_before();
+    cluster_sync_all();  // neither CTA leaves while the other may still read from it or signal it
+    if (warp == 0) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair<kTmemCols>(tmem_base);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    });
+    return fn;
+}
+
+cudaError_t ensure_head_attributes() {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<int> done[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(head_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(head_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    if (e == cudaSuccess && dev < kMaxDevices) done[dev].store(1, std::memory_order_release);
+    return e;
+}
+
+// Rows of codes [rows, d] as boxes of kBlockK columns by `box` rows; what lies past either end is 0.
+bool encode_codes(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *tm, const uint8_t *codes, int64_t rows,
+                  int64_t d, int64_t ld, int box) {
+    const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld};
+    const cuuint32_t boxes[2] = {(cuuint32_t)kBlockK, (cuuint32_t)box};
+    const cuuint32_t estr[2] = {1, 1};
+    return encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes), dims, strides, boxes, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t launch_head_e4m3(const uint8_t *X, int64_t ldx, const float *x_scale, int64_t R, int64_t d,
+                             const uint8_t *Q, int64_t ldq, const float *scale, int64_t V, void *logits, int dtype,
+                             int64_t ldl, cudaStream_t stream, const char **msg) {
+    *msg = "head";
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) {
+        *msg = "cuTensorMapEncodeTiled is not available from the driver";
+        return cudaErrorNotSupported;
+    }
+    HeadParams p{};
+    p.R = (int)R;
+    p.V = (int)V;
+    p.r_tiles = (int)((R + kMaxTileR - 1) / kMaxTileR);
+    p.tile_r = (int)(((R + p.r_tiles - 1) / p.r_tiles + 31) / 32 * 32);
+    p.tiles = (V + kTileV - 1) / kTileV * p.r_tiles;
+    p.k_blocks = (int)((d + kBlockK - 1) / kBlockK);
+    p.k_tail = (int)((d - (int64_t)(p.k_blocks - 1) * kBlockK + 31) / 32);
+    p.stage_bytes = kWBytes + p.tile_r / 2 * kBlockK;
+    p.stages = std::min(kMaxStages, (kSmemLimit - kBarrierBytes - 1024) / p.stage_bytes);
+    p.idesc = idesc_e4m3_f32(kTileV, p.tile_r);
+    p.stream_table = p.r_tiles == 1;
+    p.x_scale = x_scale;
+    p.w_scale = scale;
+    p.logits = logits;
+    p.ldl = ldl;
+    CUtensorMap tm_x, tm_w;
+    if (!encode_codes(encode, &tm_x, X, R, d, ldx, p.tile_r / 2) || !encode_codes(encode, &tm_w, Q, V, d, ldq, kRowsCta)) {
+        *msg = "a tensor map of the head's codes could not be encoded";
+        return cudaErrorInvalidValue;
+    }
+    const cudaError_t e = ensure_head_attributes();
+    if (e != cudaSuccess) return e;
+    const int64_t pairs = std::min<int64_t>(p.tiles, std::max(1, device_sm_count() / 2));
+    const int smem = kBarrierBytes + 1024 + p.stages * p.stage_bytes;
+    if (dtype == DG_BF16)
+        head_kernel<__nv_bfloat16><<<(unsigned)(2 * pairs), kThreads, smem, stream>>>(tm_x, tm_w, p);
+    else
+        head_kernel<float><<<(unsigned)(2 * pairs), kThreads, smem, stream>>>(tm_x, tm_w, p);
+    return cudaGetLastError();
+}
+
+}  // namespace dg

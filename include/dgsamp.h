@@ -575,10 +575,11 @@ size_t dg_row_loss_workspace_size(int64_t R, int64_t V, int32_t dtype);
  */
 int32_t dg_row_loss_needs_workspace(int64_t V, int32_t dtype);
 
-/* Element type of logits and gradients. */
+/* Element type of logits and gradients, and of the hidden stream's matrices (E4M3 codes: where a call says so). */
 typedef enum dg_dtype {
     DG_F32 = 0,
-    DG_BF16 = 1
+    DG_BF16 = 1,
+    DG_E4M3 = 2
 } dg_dtype;
 
 /*
@@ -693,6 +694,117 @@ dg_status dg_preference_loss(const void *logits, int32_t dtype, int64_t R, int64
                              const float *pair_weight, float *loss, float *log_ratio, float *logp, float *lse,
                              float *dlogp, void *grad, int64_t ldg, void *workspace, size_t workspace_bytes,
                              dg_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------------------
+ * The hidden stream on either side of a model: the canvas' embeddings before its first layer, norms,
+ * and the logits after its last one.  [P2]'s prepare_inputs() embeds the canvas and adds what comes of the
+ * soft embedding E; the tied table that embeds also makes the logits that the step samples from.
+ *
+ * Conventions of this part:
+ *   matrices   row-major, `ld` elements between rows, any width d >= 1, any alignment of their entries'
+ *              size (rows on 16-byte boundaries are faster; the head requires them).  Columns at d and past
+ *              it are neither read nor written.  An output that overlaps an input is DG_ERR_INVALID_ARG,
+ *              but where a call says that it may replace one.
+ *   dtypes     DG_F32 or DG_BF16, and DG_E4M3 with fp32 scales where named: a value is scale times its code's.
+ *   Sums and statistics are fp32, outputs are rounded once, results are bitwise reproducible.
+ */
+
+/*
+ * Embedding lookup with scaling: out[r] = gamma W[t - vocab_start] for t = token[r] in
+ * [vocab_start, vocab_end), else a row of zeros.
+ *
+ *   table   [rows_pad, ldw], row j = vocabulary entry vocab_start + j (a whole table: 0 and V); rows at
+ *           vocab_end - vocab_start and past it are never read.  DG_F32, DG_BF16, or DG_E4M3 codes with
+ *           scale [rows_pad] fp32 (NULL otherwise)
+ *   token   [R] int32; a negative one is padding.  One at or past V gives zeros too, and
+ *           dg_get_device_status reports it (DG_ERR_INVALID_ARG).  Slices of one vocabulary add up to the
+ *           whole lookup ([P1] "The fix": ranks hold contiguous ranges).
+ *   out     [R, ldo] of out_dtype (DG_F32 or DG_BF16)
+ * Requires 0 <= vocab_start <= vocab_end <= V < 2^31 - 16, vocab_end - vocab_start <= rows_pad,
+ * R <= 2^28, d < 2^30 (sizes: DG_ERR_UNSUPPORTED).  R == 0 queues nothing.
+ */
+dg_status dg_token_embed(const void *table, int32_t dtype, const float *scale, int64_t V, int64_t vocab_start,
+                         int64_t vocab_end, int64_t rows_pad, int64_t ldw, int64_t d, const int32_t *token,
+                         int64_t R, float gamma, void *out, int32_t out_dtype, int64_t ldo, dg_stream_t stream);
+
+/*
+ * The table's gradient from that of the rows, the positions put in order of their tokens and each token's
+ * summed in order of position:
+ *   grad_table[v - vocab_start] (+)= gamma * (sum over {r : token[r] = v} of grad[r])
+ *   grad        [R, ldg] of dtype; rows without a table row here are not read
+ *   grad_table  [rows_pad, ldt] of table_dtype.  accumulate == 0: every row of the slice is written (zeros
+ *               where a token does not occur).  Else the sum, in fp32, is added to what is there, and rows of
+ *               tokens that do not occur are neither read nor written.
+ *   workspace   at least dg_token_embed_backward_workspace_size bytes, 16-byte aligned, its contents on
+ *               entry do not matter; calls that may overlap on the GPU need one each
+ * Tokens and sizes as dg_token_embed.  R == 0 clears the slice, or queues nothing with accumulate.
+ */
+dg_status dg_token_embed_backward(const void *grad, int32_t dtype, int64_t R, int64_t d, int64_t ldg,
+                                  const int32_t *token, int64_t V, int64_t vocab_start, int64_t vocab_end,
+                                  float gamma, void *grad_table, int32_t table_dtype, int64_t rows_pad, int64_t ldt,
+                                  int32_t accumulate, void *workspace, size_t workspace_bytes, dg_stream_t stream);
+
+/* Bytes of workspace dg_token_embed_backward needs for a slice of vocab_len entries (0 for an invalid shape). */
+size_t dg_token_embed_backward_workspace_size(int64_t R, int64_t vocab_len, int64_t d);
+
+/*
+ * Root-mean-square norm with the residual's addition:
+ *   h = x + residual,  rstd = 1 / sqrt(mean(h^2) + eps),  y = h rstd (weight_offset + weight)
+ *
+ *   x         [R, ldx] of dtype
+ *   residual  [R, ldr] of residual_dtype, or NULL (h = x)
+ *   weight    [d] of weight_dtype, or NULL: y = h rstd
+ *   hidden    [R, ldh] of hidden_dtype: h rounded once (y is taken of the unrounded one), or NULL.  It may
+ *             replace x or residual (same pointer, type and stride).
+ *   out       [R, ldo] of out_dtype: y.  It may replace x or residual likewise (not hidden).  DG_E4M3: out_scale [R] fp32 =
+ *             max|y| / 448 and codes e4m3(y / out_scale), ties to even, as dg_quantize_e4m3 (a row of zeros:
+ *             scale 0, codes 0): what dg_head_e4m3 takes.  A row with an infinity or NaN has NaN or infinity as its scale.
+ *   rstd      [R] fp32 or NULL: what the backward pass takes
+ * Requires 1 <= d <= 32768 (above: DG_ERR_UNSUPPORTED), eps >= 0 and finite, weight_offset finite, R <= 2^28.
+ */
+dg_status dg_rms_norm(const void *x, int32_t dtype, int64_t R, int64_t d, int64_t ldx, const void *residual,
+                      int32_t residual_dtype, int64_t ldr, const void *weight, int32_t weight_dtype,
+                      float weight_offset, float eps, void *hidden, int32_t hidden_dtype, int64_t ldh, void *out,
+                      int32_t out_dtype, int64_t ldo, float *out_scale, float *rstd, dg_stream_t stream);
+
+/*
+ * Its gradient, from that of y and (the stream that goes on) of h:
+ *   dh = grad_hidden + rstd (g - xh mean(g xh)),  g = grad (weight_offset + weight),  xh = hidden rstd
+ *   grad_weight = sum over the rows of grad xh
+ *   grad         [R, ldg] of dtype: the gradient of y
+ *   hidden       [R, ldh] of hidden_dtype, rstd [R]: what the forward pass wrote (or x, without a residual)
+ *   grad_hidden  [R, ldu] of grad_hidden_dtype, or NULL (0)
+ *   grad_x       [R, ldx] of hidden_dtype: dh, the gradient of x and of residual alike.  It may replace
+ *                grad, hidden or grad_hidden (same pointer, type and stride).
+ *   grad_weight  [d] of weight_dtype, or NULL; without a weight it has to be NULL
+ *   workspace    at least dg_rms_norm_backward_workspace_size bytes, 16-byte aligned, its contents on entry do not
+ *                matter; may be NULL without grad_weight
+ * Sizes as dg_rms_norm.  R == 0 writes zeros to grad_weight.
+ */
+dg_status dg_rms_norm_backward(const void *grad, int32_t dtype, int64_t R, int64_t d, int64_t ldg,
+                               const void *hidden, int32_t hidden_dtype, int64_t ldh, const float *rstd,
+                               const void *weight, int32_t weight_dtype, float weight_offset,
+                               const void *grad_hidden, int32_t grad_hidden_dtype, int64_t ldu, void *grad_x,
+                               int64_t ldx, void *grad_weight, void *workspace, size_t workspace_bytes,
+                               dg_stream_t stream);
+
+/* Bytes of workspace dg_rms_norm_backward needs on the current device (0 for an invalid shape). */
+size_t dg_rms_norm_backward_workspace_size(int64_t R, int64_t d);
+
+/*
+ * The tied head over an 8-bit table: logits[r, v] = x_scale[r] scale[v] sum_k e4m3(X[r, k]) e4m3(Q[v, k]).
+ *   X        [R, ldx] E4M3 codes, x_scale [R] fp32 (dg_rms_norm's 8-bit output)
+ *   Q        [V, ldq] E4M3 codes, scale [V] fp32 (dg_quantize_e4m3's)
+ *   logits   [R, ldl] of dtype (DG_F32: what the sampler's calls take; DG_BF16)
+ * The product runs on the tensor cores, whose fp32 sums the scales multiply.  NaN codes (0x7F, 0xFF) make NaN.
+ * Requires X, Q and logits 16-byte aligned with row strides of whole 16 bytes (else DG_ERR_UNSUPPORTED); any
+ * V and d; columns at d and past it are not read, whatever they hold.  R <= 2^28, d < 2^24.
+ * R == 0 queues nothing.
+ */
+dg_status dg_head_e4m3(const uint8_t *X, int64_t ldx, const float *x_scale, int64_t R, int64_t d, const uint8_t *Q,
+                       const float *scale, int64_t V, int64_t ldq, void *logits, int32_t dtype, int64_t ldl,
+                       dg_stream_t stream);
 
 #ifdef __cplusplus
 }
