@@ -988,8 +988,8 @@ def dg_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: t
                 out: dict | None = None, stream=None) -> dict:
     """h = x + residual, y = h / rms(h) * (weight_offset + weight) -> dict out (y), rstd [R], with a residual
     hidden (h), with dtype=torch.uint8 scale [R] beside the E4M3 codes in out.
-    dtype: of a new out (default: x's); hidden has the residual's type.  `out` may hold x or residual themselves
-    as hidden or as out: they are replaced."""
+    dtype: of a new out (default: x's); hidden has the residual's type, and out={"hidden": None} leaves it out.
+    `out` may hold x or residual themselves as hidden or as out: they are replaced."""
     device = _here(x, "x")
     R, d = x.shape
     xp, xc, ldx = _matrix(x, R, d, "x", device)

@@ -1,7 +1,7 @@
 """A small training run over the sampler: `python -m denoising_sampler_step_gb300.finetune`.
 
-The "model" is one hidden vector per canvas position times a fixed embedding table, so that its
-logits are what the sampler's calls take; what is trained is the hidden vectors.  Three stages, as
+The first runs' "model" is one hidden vector per canvas position times a fixed embedding table, so that its
+logits are what the sampler's calls take; what is trained is the hidden vectors.  Three stages (`run`), as
 a diffusion model's sampler is tuned in earnest:
 
 1. distillation: a teacher's logits are reduced to their top entries (dg_row_topk), and the student
@@ -9,6 +9,10 @@ a diffusion model's sampler is tuned in earnest:
 2. policy: candidates are drawn from the student with the sampler's own draw (dg_row_sample), whose
    log-probabilities are the behaviour policy's, and rewarded (training.policy_loss);
 3. preference: canvases of rewarded and of unrewarded tokens form pairs (training.preference_loss).
+
+A last run (`denoise`) trains what lies before the hidden vectors: the table that embeds a noised canvas
+(training.token_embed) and the norm's weight (training.rms_norm), by the likelihood of the clean tokens
+(training.token_logp).
 """
 from __future__ import annotations
 
@@ -92,6 +96,36 @@ def run(steps: int = 60, K: int = 64, seed: int = 0, log=print) -> dict:
     return report
 
 
+def denoise(steps: int = 60, noise: float = 0.3, seed: int = 0, log=print) -> dict:
+    """Trains a tied table and a norm to name a canvas' clean tokens from a noised one (a share `noise` of its
+    positions hold one mask token, some are padding) and a self-conditioning signal."""
+    wl = inputs.WORKLOADS["tiny"]
+    V, d, gamma = wl.V, wl.d, wl.gamma
+    R = 4 * wl.R
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    table = (torch.randn(V, d, generator=g, device="cuda") / d ** 0.5).requires_grad_(True)
+    weight = torch.ones(d, device="cuda", requires_grad=True)
+    clean = torch.randint(V - 1, (R,), generator=g, device="cuda").to(torch.int32)
+    signal = 0.1 * torch.randn(R, d, generator=g, device="cuda")
+    noised = torch.where(torch.rand(R, generator=g, device="cuda") < noise, V - 1, clean)
+    noised[-wl.R // 4:] = -1                  # padding: no embedding, no loss
+    opt = torch.optim.Adam([table, weight], lr=0.005)
+    losses = []
+    for _ in range(steps):
+        opt.zero_grad()
+        x = training.token_embed(table, noised.to(torch.int32), gamma)
+        y, _ = training.rms_norm(x, weight, residual=signal)
+        logp = training.token_logp(y @ table.T, clean, mask=noised >= 0)
+        loss = -logp.sum() / (noised >= 0).sum()
+        loss.backward()
+        opt.step()
+        losses.append(loss.detach())
+    B.dg_get_device_status()
+    report = {"denoise": (float(losses[0]), float(losses[-1]))}
+    log(f"denoising      loss per position   {report['denoise'][0]:.4f} -> {report['denoise'][1]:.4f} nats")
+    return report
+
+
 def main() -> None:
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=60)
@@ -99,6 +133,7 @@ def main() -> None:
     ap.add_argument("--seed", type=int, default=0)
     a = ap.parse_args()
     run(a.steps, a.top, a.seed)
+    denoise(a.steps, seed=a.seed)
 
 
 if __name__ == "__main__":

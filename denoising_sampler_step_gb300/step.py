@@ -3,7 +3,7 @@ run it (inputs already on the device, or inputs copied from pinned host memory a
 results copied back, all on one stream).
 
 PyTorch only provides the memory and the stream; each step is one call of
-dg_sampler_step in libdgsamp.
+dg_sampler_step in libdgsamp.  TiedEnds holds what lies between the step and a model's layers.
 """
 from __future__ import annotations
 
@@ -169,3 +169,47 @@ class SamplerLoop(SamplerStep):
                                    stream=stream, two_pass=self.two_pass)
         self.offset += 1
         return o
+
+
+class TiedEnds:
+    """The two ends of a model around the sampler step, over the step's own table: what a denoising step does
+    before the model's first layer and after its last one.  Buffers for R positions, resident; each method is a
+    few calls on one stream and can be captured into a CUDA graph.
+
+    W: the bf16 table [V, d], or with `scale` its E4M3 codes.  The head multiplies 8-bit codes, so a bf16 table
+    is quantised once here (`Q`, `scale`) and kept for the lookup.  gamma: the embedding's normaliser.
+    norm_in, norm_out: weights [d] of the first layer's norm and of the one before the head."""
+
+    def __init__(self, W: torch.Tensor, R: int, gamma: float, norm_in: torch.Tensor, norm_out: torch.Tensor,
+                 scale: torch.Tensor | None = None, eps: float = 1e-6, weight_offset: float = 0.0,
+                 logits_dtype: torch.dtype = torch.float32):
+        self.W, self.w_scale = W, scale
+        self.Q, self.scale = (W, scale) if scale is not None else B.dg_quantize_e4m3(W)
+        self.gamma, self.eps, self.weight_offset = float(gamma), float(eps), float(weight_offset)
+        self.norm_in, self.norm_out = norm_in, norm_out
+        V, d = W.shape
+        dev = W.device
+
+        def rows(n, dtype):
+            per = 16 // dtype.itemsize
+            return torch.empty((R, (n + per - 1) // per * per), dtype=dtype, device=dev)[:, :n]
+
+        f32 = dict(dtype=torch.float32, device=dev)
+        self.embedded = rows(d, torch.bfloat16)
+        self.first = {"hidden": rows(d, torch.float32), "out": rows(d, torch.bfloat16), "rstd": torch.empty(R, **f32)}
+        self.last = {"hidden": None, "out": rows(d, torch.uint8), "scale": torch.empty(R, **f32), "rstd": torch.empty(R, **f32)}
+        self.logits_out = rows(V, logits_dtype)
+
+    def inputs(self, token: torch.Tensor, signal: torch.Tensor, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+        """(h [R, d] fp32, its norm in bf16): the canvas' embeddings plus the self-conditioning signal [R, d]
+        (fp32: what the model makes of the previous step's soft embedding E, zeros at the first step)."""
+        B.dg_token_embed(self.W, token, self.gamma, scale=self.w_scale, out=self.embedded, stream=stream)
+        o = B.dg_rms_norm(self.embedded, self.norm_in, residual=signal, eps=self.eps,
+                          weight_offset=self.weight_offset, out=self.first, stream=stream)
+        return o["hidden"], o["out"]
+
+    def logits(self, x: torch.Tensor, residual: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Logits [R, V] of the hidden stream (plus the last layer's output): the norm in 8 bits and the head."""
+        o = B.dg_rms_norm(x, self.norm_out, residual=residual, eps=self.eps, weight_offset=self.weight_offset,
+                          out=self.last, stream=stream)
+        return B.dg_head_e4m3(o["out"], o["scale"], self.Q, self.scale, out=self.logits_out, stream=stream)

@@ -1,4 +1,5 @@
-"""The losses on the sampler's logits as differentiable functions.
+"""The losses on the sampler's logits, and the embedding and norm of the hidden stream before a model, as
+differentiable functions.
 
 Each function returns one loss per row (or pair) and can stand in any autograd expression of the
 logits: the forward pass is one call of the library (losses and the log-sum-exp), the backward
@@ -9,8 +10,9 @@ logits with the binding's own calls (`grad=True`, weights in `weight`).
 `mask` [R] (bool or any type: nonzero counts) leaves rows out: their logits are not read, their
 loss is 0 and their gradient 0.
 
-The functions differentiate once and in the logits alone.  Another argument that requires a gradient
-is an error (detach it), and so is `create_graph=True`: what would be lost is not lost in silence.
+The losses differentiate once and in the logits alone, token_embed in the table, rms_norm in its matrices and
+weight.  Another argument that requires a gradient is an error (detach it), and so is `create_graph=True`: what
+would be lost is not lost in silence.
 """
 from __future__ import annotations
 
@@ -40,8 +42,51 @@ def _constants(**tensors) -> None:
 def _first_order() -> None:
     """Refuses a backward pass that is to be differentiated (autograd records it only then)."""
     if torch.is_grad_enabled():
-        raise RuntimeError("the losses on logits have first derivatives only: with create_graph=True their "
+        raise RuntimeError("the functions of this module have first derivatives only: with create_graph=True their "
                            "gradient would count as a constant")
+
+
+def _rows(g: torch.Tensor) -> torch.Tensor:
+    """An upstream gradient with unit column stride (a sum's comes expanded)."""
+    return g if g.stride(1) == 1 and (g.shape[0] <= 1 or g.stride(0) >= g.shape[1]) else g.contiguous()
+
+
+class _TokenEmbed(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, table, token, gamma, dtype):
+        ctx.save_for_backward(token)
+        ctx.gamma, ctx.V, ctx.dtype = gamma, table.shape[0], table.dtype
+        return B.dg_token_embed(table, token, gamma, dtype=dtype)
+
+    @staticmethod
+    def backward(ctx, g):
+        _first_order()
+        token, = ctx.saved_tensors
+        return B.dg_token_embed_backward(_rows(g), token, ctx.V, ctx.gamma, dtype=ctx.dtype), None, None, None
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps, weight_offset, dtype):
+        o = B.dg_rms_norm(x, weight, residual=residual, eps=eps, weight_offset=weight_offset, dtype=dtype)
+        hidden = o.get("hidden", x)
+        ctx.save_for_backward(hidden, weight, o["rstd"])
+        ctx.weight_offset, ctx.types = weight_offset, (x.dtype, None if residual is None else residual.dtype)
+        ctx.set_materialize_grads(False)
+        return o["out"], (None if residual is None else hidden)
+
+    @staticmethod
+    def backward(ctx, g, gh):
+        _first_order()
+        hidden, weight, rstd = ctx.saved_tensors
+        if g is None:  # y was not used
+            g = torch.zeros_like(hidden)
+        out = {} if weight is not None and ctx.needs_input_grad[2] else {"grad_weight": None}
+        o = B.dg_rms_norm_backward(_rows(g), hidden, rstd, weight, ctx.weight_offset,
+                                   grad_hidden=None if gh is None else _rows(gh), out=out)
+        x_type, r_type = ctx.types
+        return (o["grad"].to(x_type), None if r_type is None else o["grad"].to(r_type), o.get("grad_weight"),
+                None, None, None)
 
 
 class _TokenLogp(torch.autograd.Function):
@@ -153,3 +198,20 @@ def preference_loss(logits: torch.Tensor, token: torch.Tensor, ref_logp: torch.T
     (binding.dg_preference_loss); `weight` [R] masks tokens or normalises by length."""
     _constants(ref_logp=ref_logp, weight=weight)
     return _Preference.apply(logits, token, ref_logp, seq_start, beta, label_smoothing, temperature, weight)
+
+
+def token_embed(table: torch.Tensor, token: torch.Tensor, gamma: float = 1.0,
+                dtype: torch.dtype | None = None) -> torch.Tensor:
+    """gamma times the rows of `table` [V, d] (fp32 or bf16) at `token` [R] (int32; negative: padding, a row of
+    zeros), differentiable in the table (binding.dg_token_embed).  The gradient has the table's type and size."""
+    return _TokenEmbed.apply(table, token, gamma, dtype)
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+             eps: float = 1e-6, weight_offset: float = 0.0,
+             dtype: torch.dtype | None = None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """(y, h) with h = x + residual and y = h / rms(h) (weight_offset + weight), differentiable in all three
+    (binding.dg_rms_norm); h is None without a residual."""
+    if dtype is not None and not dtype.is_floating_point:
+        raise TypeError("8-bit outputs are not differentiable: use binding.dg_rms_norm")
+    return _RmsNorm.apply(x, residual, weight, eps, weight_offset, dtype)
