@@ -57,7 +57,8 @@ def test_a_denoising_loop_with_both_ends(B, ends):
     denoise(e, loop, canvas, budgets, 3, seen)
     W = np64(e.W) if e.w_scale is None else e4m3_decode(e.Q.cpu().numpy()) * np64(e.scale)[:, None]
     Q = e4m3_decode(e.Q.cpu().numpy())
-    assert not torch.equal(seen[0]["canvas"], seen[2]["canvas"])
+    # (a model that is the identity names its own tokens; what changes from step to step is E)
+    assert not seen[0]["E"].any() and seen[1]["E"].any() and not torch.equal(seen[0]["logits"], seen[1]["logits"])
     for o in seen:
         ref = H.token_embed(W, o["canvas"].cpu().numpy(), e.gamma)
         close(o["x"], ref, (3 * U + 2.0 ** -8) * np.abs(ref))
