@@ -37,6 +37,7 @@ constexpr int kWarpLoad = kEpilogueWarps, kWarpMma = kEpilogueWarps + 1;
 constexpr int kThreads = (kEpilogueWarps + 2) * 32;
 constexpr int kTmemCols = 512;
 constexpr int kSmemLimit = 232448;          // shared memory of a CTA
+constexpr int kResidentBytes = 96 * 1024;   // a CTA's half of the positions, at most, to stay in it
 constexpr int kBarrierBytes = 512;
 
 struct HeadParams {
@@ -44,7 +45,7 @@ struct HeadParams {
     void *logits;
     int64_t ldl, tiles;
     int R, V, tile_r, r_tiles, k_blocks, k_tail;  // k_tail: MMAs of the last block
-    int stages, stage_bytes;
+    int stages, stage_bytes, resident_bytes;
     uint32_t idesc;
     int stream_table;  // each table byte is read once: leave L2 first
 };
@@ -64,35 +65,42 @@ __device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc,
         : "memory");
 }
 
+// True in one lane of a converged warp.  The compiler then knows that a single thread issues what follows: with
+// `lane == 0` in its place an instruction took 120 cycles to issue, a ring slot's four as long as their products.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
 // One arrival, with release at cluster scope, on a barrier of any CTA of the cluster.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void store_logit(float *p, float v) { *p = v; }
-
-// The 32 columns (positions) of a chunk that this lane holds for its vocabulary entry v.
+// The 32 columns (positions) of a chunk that this lane holds for its vocabulary entry v; sx: lane c holds the
+// scale of position row0 + c.
 __device__ __forceinline__ void store_chunk(const HeadParams &p, float *logits, const uint32_t (&acc)[32], int row0, int v,
-                                            float sw) {
-    if (v >= p.V) return;
+                                            float sw, float sx) {
     float *dst = logits + (int64_t)row0 * p.ldl + v;
-    const int n = min(32, p.R - row0);
+    const int n = v < p.V ? min(32, p.R - row0) : 0;
 #pragma unroll
-    for (int c = 0; c < 32; ++c)
-        if (c < n) store_logit(dst + c * p.ldl, __uint_as_float(acc[c]) * sw * __ldg(p.x_scale + row0 + c));
+    for (int c = 0; c < 32; ++c) {
+        const float s = __shfl_sync(0xffffffffu, sx, c);
+        if (c < n) dst[c * p.ldl] = __uint_as_float(acc[c]) * sw * s;
+    }
 }
 
 // bf16: neighbouring lanes swap a value so that each writes two vocabulary entries of one position
 // (half the stores; rows start on 16-byte boundaries, so the pair is 4-byte aligned).
 __device__ __forceinline__ void store_chunk(const HeadParams &p, __nv_bfloat16 *logits, const uint32_t (&acc)[32],
-                                            int row0, int v, float sw) {
+                                            int row0, int v, float sw, float sx) {
     const int odd = v & 1, v0 = v - odd;
     const int n = min(32, p.R - row0);
     __nv_bfloat16 *dst = logits + (int64_t)(row0 + odd) * p.ldl + v0;
 #pragma unroll
     for (int c = 0; c < 32; c += 2) {
-        const float s0 = c < n ? __ldg(p.x_scale + row0 + c) : 0.0f;
-        const float s1 = c + 1 < n ? __ldg(p.x_scale + row0 + c + 1) : 0.0f;
+        const float s0 = __shfl_sync(0xffffffffu, sx, c), s1 = __shfl_sync(0xffffffffu, sx, c + 1);
         const float a = __uint_as_float(acc[c]) * sw * s0, b = __uint_as_float(acc[c + 1]) * sw * s1;
         const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
         if (c + odd < n) {
@@ -115,9 +123,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t *acc_full = empty + kMaxStages;                  // a tile's products are done
     uint64_t *acc_empty = acc_full + 2;                       // the even CTA's: the accumulator has been read
     uint64_t *drained = acc_empty + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
+    uint64_t *x_full = drained + 1;                           // the even CTA's: the resident positions have landed
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(x_full + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    const uint32_t ring = (smem_u32(smem_raw) + kBarrierBytes + 1023u) & ~1023u;
+    const uint32_t resident = (smem_u32(smem_raw) + kBarrierBytes + 1023u) & ~1023u;
+    const uint32_t ring = resident + p.resident_bytes;
+    const uint32_t x_bytes = (uint32_t)(p.tile_r / 2) * kBlockK;  // a CTA's half of the positions, per block
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -133,6 +144,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&acc_empty[b]), 2 * kEpilogueWarps);
         }
         mbar_init(smem_u32(drained), 1);
+        mbar_init(smem_u32(x_full), 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&tm_x);
@@ -148,11 +160,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;  // false once this thread gave up on a wait
 
     if (warp == kWarpLoad) {
-        if (lane == 0) {
-            const uint32_t x_bytes = (uint32_t)(p.tile_r / 2) * kBlockK;
+        if (elect_one()) {
             const uint32_t lead_full = map_to_cta(smem_u32(&full[0]), 0);
             const uint64_t w_policy = p.stream_table ? l2_policy_evict_first() : l2_policy_evict_normal();
             const uint64_t x_policy = l2_policy_evict_normal();
+            const bool keep = p.resident_bytes > 0;
+            if (keep && pair < p.tiles) {
+                const uint32_t bar = map_to_cta(smem_u32(x_full), 0);
+                if (rank == 0) mbar_arrive_expect_tx(smem_u32(x_full), 2 * x_bytes * (uint32_t)p.k_blocks);
+                for (int k = 0; k < p.k_blocks; ++k)
+                    tma_load_2d_pair_hint(resident + k * x_bytes, &tm_x, bar, k * kBlockK, (int)rank * (p.tile_r / 2),
+                                          x_policy);
+            }
+            const uint32_t slot_bytes = 2 * (kWBytes + (keep ? 0u : x_bytes));
             int s = 0;
             uint32_t use = 0;
             for (int64_t t = pair; t < p.tiles && ok; t += pairs) {
@@ -163,10 +183,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * (kWBytes + x_bytes));
+                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), slot_bytes);
                     const uint32_t at = ring + (uint32_t)s * p.stage_bytes, bar = lead_full + 8u * (uint32_t)s;
                     tma_load_2d_pair_hint(at, &tm_w, bar, k * kBlockK, v0, w_policy);
-                    tma_load_2d_pair_hint(at + kWBytes, &tm_x, bar, k * kBlockK, r0, x_policy);
+                    if (!keep) tma_load_2d_pair_hint(at + kWBytes, &tm_x, bar, k * kBlockK, r0, x_policy);
                     if (++s == p.stages) {
                         s = 0;
                         ++use;
@@ -175,28 +195,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == kWarpMma) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0 && elect_one()) {
+            const bool keep = p.resident_bytes > 0;
             int s = 0, n = 0;
             uint32_t ph = 0;
+            if (keep && pair < p.tiles) ok = mbar_wait(smem_u32(x_full), 0, abort_flag);
             for (int64_t t = pair; t < p.tiles && ok; t += pairs, ++n) {
                 const int b = n & 1;
-                if (n >= 2 && !mbar_wait_cluster(smem_u32(&acc_empty[b]), (uint32_t)((n >> 1) - 1) & 1, abort_flag)) {
+                if (n >= 2 && !mbar_wait(smem_u32(&acc_empty[b]), (uint32_t)((n >> 1) - 1) & 1, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)b * 256u;
                 for (int k = 0; k < p.k_blocks; ++k) {
-                    if (!mbar_wait_cluster(smem_u32(&full[s]), ph, abort_flag)) {
+                    if (!mbar_wait(smem_u32(&full[s]), ph, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t at = ring + (uint32_t)s * p.stage_bytes;
-                    const uint64_t a = smem_desc(at, 16, 1024, 2), x = smem_desc(at + kWBytes, 16, 1024, 2);
-                    const int steps = k + 1 < p.k_blocks ? kBlockK / 32 : p.k_tail;
-                    for (int j = 0; j < steps; ++j)  // 32 bytes further along both operands' rows
-                        umma_e4m3_pair(d_tmem, a + 2 * j, x + 2 * j, p.idesc, (k | j) != 0);
+                    const uint64_t a = smem_desc(at, 16, 1024, 2);
+                    const uint64_t x = smem_desc(keep ? resident + k * x_bytes : at + kWBytes, 16, 1024, 2);
+                    // 32 codes a step: 32 bytes further along both operands' rows
+                    if (k + 1 < p.k_blocks || p.k_tail == kBlockK / 32) {
+#pragma unroll
+                        for (int j = 0; j < kBlockK / 32; ++j)
+                            umma_e4m3_pair(d_tmem, a + 2 * j, x + 2 * j, p.idesc, (k | j) != 0);
+                    } else {
+                        for (int j = 0; j < p.k_tail; ++j)
+                            umma_e4m3_pair(d_tmem, a + 2 * j, x + 2 * j, p.idesc, (k | j) != 0);
+                    }
                     umma_commit_pair(smem_u32(&empty[s]), 3);
                     if (++s == p.stages) {
                         s = 0;
@@ -214,12 +243,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes, and every other chunk of columns
         const uint32_t lead_empty = map_to_cta(smem_u32(&acc_empty[0]), 0);
         T *logits = static_cast<T *>(p.logits);
+        // a tile's scales are loaded while the tile before it is stored: a load takes thousands of cycles
+        // beside the ring's traffic
+        float sx[4], sx_next[4], sw, sw_next = 0.0f;
+        auto load_scales = [&](int64_t t) {
+            const int v = (int)(t / p.r_tiles) * kTileV + (int)rank * kRowsCta + quarter * 32 + lane;
+            const int r = (int)(t % p.r_tiles) * p.tile_r + half * 32 + lane;
+            sw_next = t < p.tiles && v < p.V ? __ldg(p.w_scale + v) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sx_next[i] = t < p.tiles && r + 64 * i < p.R ? __ldg(p.x_scale + r + 64 * i) : 0.0f;
+        };
+        load_scales(pair);
         int n = 0;
         for (int64_t t = pair; t < p.tiles; t += pairs, ++n) {
             const int b = n & 1;
             const int v = (int)(t / p.r_tiles) * kTileV + (int)rank * kRowsCta + quarter * 32 + lane;
             const int r0 = (int)(t % p.r_tiles) * p.tile_r;
-            const float sw = v < p.V ? __ldg(p.w_scale + v) : 0.0f;
+            sw = sw_next;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sx[i] = sx_next[i];
+            load_scales(t + pairs);
             ok = mbar_wait(smem_u32(&acc_full[b]), (uint32_t)(n >> 1) & 1, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
@@ -229,7 +272,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 uint32_t acc[32];
                 tmem_ld_32x32b_x32(at + c, acc);
                 tmem_ld_wait();
-                store_chunk(p, logits, acc, r0 + c, v, sw);
+                store_chunk(p, logits, acc, r0 + c, v, sw, c < 64 ? sx[0] : c < 128 ? sx[1] : c < 192 ? sx[2] : sx[3]);
             }
             tc_fence_before();
             __syncwarp();
@@ -311,8 +354,11 @@ cudaError_t launch_head_e4m3(const uint8_t *X, int64_t ldx, const float *x_scale
     p.tiles = (V + kTileV - 1) / kTileV * p.r_tiles;
     p.k_blocks = (int)((d + kBlockK - 1) / kBlockK);
     p.k_tail = (int)((d - (int64_t)(p.k_blocks - 1) * kBlockK + 31) / 32);
-    p.stage_bytes = kWBytes + p.tile_r / 2 * kBlockK;
-    p.stages = std::min(kMaxStages, (kSmemLimit - kBarrierBytes - 1024) / p.stage_bytes);
+    // the positions' codes are the same for every tile where one tile holds them all
+    const int x_bytes = p.tile_r / 2 * kBlockK;
+    p.resident_bytes = p.r_tiles == 1 && p.k_blocks <= kResidentBytes / x_bytes ? p.k_blocks * x_bytes : 0;
+    p.stage_bytes = kWBytes + (p.resident_bytes ? 0 : x_bytes);
+    p.stages = std::min(kMaxStages, (kSmemLimit - kBarrierBytes - 1024 - p.resident_bytes) / p.stage_bytes);
     p.idesc = idesc_e4m3_f32(kTileV, p.tile_r);
     p.stream_table = p.r_tiles == 1;
     p.x_scale = x_scale;
@@ -327,7 +373,7 @@ cudaError_t launch_head_e4m3(const uint8_t *X, int64_t ldx, const float *x_scale
     const cudaError_t e = ensure_head_attributes();
     if (e != cudaSuccess) return e;
     const int64_t pairs = std::min<int64_t>(p.tiles, std::max(1, device_sm_count() / 2));
-    const int smem = kBarrierBytes + 1024 + p.stages * p.stage_bytes;
+    const int smem = kBarrierBytes + 1024 + p.resident_bytes + p.stages * p.stage_bytes;
     if (dtype == DG_BF16)
         head_kernel<__nv_bfloat16><<<(unsigned)(2 * pairs), kThreads, smem, stream>>>(tm_x, tm_w, p);
     else
