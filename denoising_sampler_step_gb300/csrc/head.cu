@@ -26,11 +26,12 @@ namespace dg {
 
 namespace {
 
-constexpr int kTileV = 256;                 // vocabulary rows of a pair's tile
-constexpr int kRowsCta = kTileV / 2;        // of them in each CTA
+constexpr int kTileV = 256;                 // vocabulary rows of a pair's product
+constexpr int kRowsCta = kTileV / 2;        // of them in each CTA; a tile takes the first rows_cta of these
+constexpr int kMinRows = 32;
 constexpr int kMaxTileR = 256;              // positions of a tile
-constexpr int kBlockK = 128;                // codes per ring slot and row: one 128-byte swizzle atom
-constexpr int kWBytes = kRowsCta * kBlockK;
+constexpr int kBlockK = 128;                // codes of a block and row: one 128-byte swizzle atom
+constexpr int kSlotBlocks = 2;              // blocks of a ring slot, one load for the two of either operand
 constexpr int kMaxStages = 12;
 constexpr int kEpilogueWarps = 8;           // two per TMEM lane quarter
 constexpr int kWarpLoad = kEpilogueWarps, kWarpMma = kEpilogueWarps + 1;
@@ -44,10 +45,13 @@ struct HeadParams {
     const float *x_scale, *w_scale;
     void *logits;
     int64_t ldl, tiles;
-    int R, V, tile_r, r_tiles, k_blocks, k_tail;  // k_tail: MMAs of the last block
+    int rows_cta;
+    int R, V, tile_r, r_tiles, k_blocks, k_steps;  // blocks and steps of 32 that cover d
+    int full_blocks;  // of them those that lie wholly below d
     int stages, stage_bytes, resident_bytes;
     uint32_t idesc;
-    int stream_table;  // each table byte is read once: leave L2 first
+    int stream_table;   // each table byte is read once: leave L2 first
+    int stream_logits;  // the logits do not stay in L2 either way
 };
 
 // Instruction descriptor of kind::f8f6f4 with E4M3 A and B, fp32 accumulator, both K-major.
@@ -78,24 +82,28 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// The 32 columns (positions) of a chunk that this lane holds for its vocabulary entry v; sx: lane c holds the
-// scale of position row0 + c.
+// The 32 columns (positions) of a chunk that this lane holds for its vocabulary entry v; the first `live` lanes
+// have one; sx: lane c holds the scale of position row0 + c.
 __device__ __forceinline__ void store_chunk(const HeadParams &p, float *logits, const uint32_t (&acc)[32], int row0, int v,
-                                            float sw, float sx) {
+                                            int lane, int live, float sw, float sx, uint64_t policy) {
     float *dst = logits + (int64_t)row0 * p.ldl + v;
-    const int n = v < p.V ? min(32, p.R - row0) : 0;
+    const int n = lane < live ? min(32, p.R - row0) : 0;
 #pragma unroll
     for (int c = 0; c < 32; ++c) {
         const float s = __shfl_sync(0xffffffffu, sx, c);
-        if (c < n) dst[c * p.ldl] = __uint_as_float(acc[c]) * sw * s;
+        if (c < n)
+            asm volatile("st.global.L2::cache_hint.f32 [%0], %1, %2;" ::"l"(dst + c * p.ldl),
+                         "f"(__uint_as_float(acc[c]) * sw * s), "l"(policy)
+                         : "memory");
     }
 }
 
 // bf16: neighbouring lanes swap a value so that each writes two vocabulary entries of one position
 // (half the stores; rows start on 16-byte boundaries, so the pair is 4-byte aligned).
 __device__ __forceinline__ void store_chunk(const HeadParams &p, __nv_bfloat16 *logits, const uint32_t (&acc)[32],
-                                            int row0, int v, float sw, float sx) {
-    const int odd = v & 1, v0 = v - odd;
+                                            int row0, int v, int lane, int live, float sw, float sx,
+                                            uint64_t policy) {
+    const int odd = lane & 1, v0 = v - odd;
     const int n = min(32, p.R - row0);
     __nv_bfloat16 *dst = logits + (int64_t)(row0 + odd) * p.ldl + v0;
 #pragma unroll
@@ -106,9 +114,10 @@ __device__ __forceinline__ void store_chunk(const HeadParams &p, __nv_bfloat16 *
         if (c + odd < n) {
             __nv_bfloat16 *q = dst + c * p.ldl;
             const float lo = odd ? got : a, hi = odd ? b : got;
-            if (v0 + 1 < p.V)
-                *reinterpret_cast<__nv_bfloat162 *>(q) = __floats2bfloat162_rn(lo, hi);
-            else if (v0 < p.V)
+            if (lane - odd + 1 < live)
+                asm volatile("st.global.L2::cache_hint.b32 [%0], %1, %2;" ::"l"(q), "r"(hidden::pack_bf16(lo, hi)), "l"(policy)
+                             : "memory");
+            else if (lane - odd < live)
                 *q = __float2bfloat16_rn(lo);
         }
     }
@@ -116,19 +125,21 @@ __device__ __forceinline__ void store_chunk(const HeadParams &p, __nv_bfloat16 *
 
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    head_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const HeadParams p) {
+    head_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                const __grid_constant__ CUtensorMap tm_x2, const __grid_constant__ CUtensorMap tm_w2, const HeadParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem_raw);  // the even CTA's: both CTAs' tiles have landed
     uint64_t *empty = full + kMaxStages;                      // the slot's products are done
     uint64_t *acc_full = empty + kMaxStages;                  // a tile's products are done
     uint64_t *acc_empty = acc_full + 2;                       // the even CTA's: the accumulator has been read
     uint64_t *drained = acc_empty + 2;
-    uint64_t *x_full = drained + 1;                           // the even CTA's: the resident positions have landed
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(x_full + 1);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const uint32_t resident = (smem_u32(smem_raw) + kBarrierBytes + 1023u) & ~1023u;
     const uint32_t ring = resident + p.resident_bytes;
-    const uint32_t x_bytes = (uint32_t)(p.tile_r / 2) * kBlockK;  // a CTA's half of the positions, per block
+    // a CTA's half of the positions and its table rows, per block
+    const uint32_t x_bytes = (uint32_t)(p.tile_r / 2) * kBlockK, w_bytes = (uint32_t)p.rows_cta * kBlockK;
+    const int slots = (p.k_blocks + kSlotBlocks - 1) / kSlotBlocks;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -144,7 +155,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&acc_empty[b]), 2 * kEpilogueWarps);
         }
         mbar_init(smem_u32(drained), 1);
-        mbar_init(smem_u32(x_full), 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&tm_x);
@@ -165,28 +175,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint64_t w_policy = p.stream_table ? l2_policy_evict_first() : l2_policy_evict_normal();
             const uint64_t x_policy = l2_policy_evict_normal();
             const bool keep = p.resident_bytes > 0;
-            if (keep && pair < p.tiles) {
-                const uint32_t bar = map_to_cta(smem_u32(x_full), 0);
-                if (rank == 0) mbar_arrive_expect_tx(smem_u32(x_full), 2 * x_bytes * (uint32_t)p.k_blocks);
-                for (int k = 0; k < p.k_blocks; ++k)
-                    tma_load_2d_pair_hint(resident + k * x_bytes, &tm_x, bar, k * kBlockK, (int)rank * (p.tile_r / 2),
-                                          x_policy);
-            }
-            const uint32_t slot_bytes = 2 * (kWBytes + (keep ? 0u : x_bytes));
+            // blocks 2k and 2k + 1 of an operand's rows: one load where both lie wholly below d, else each by
+            // itself, what lies past d as zeros
+            auto load = [&](const void *tm2, const void *tm, uint32_t at, uint32_t block_bytes, uint32_t bar, int k, int row,
+                            uint64_t policy) {
+                if (2 * k + 1 < p.full_blocks) {
+                    tma_load_3d_pair_hint(at, tm2, bar, 0, row, 2 * k, policy);
+                } else {
+                    tma_load_2d_pair_hint(at, tm, bar, 2 * k * kBlockK, row, policy);
+                    if (2 * k + 1 < p.k_blocks)
+                        tma_load_2d_pair_hint(at + block_bytes, tm, bar, (2 * k + 1) * kBlockK, row, policy);
+                }
+            };
             int s = 0;
             uint32_t use = 0;
             for (int64_t t = pair; t < p.tiles && ok; t += pairs) {
-                const int v0 = (int)(t / p.r_tiles) * kTileV + (int)rank * kRowsCta;
+                const int v0 = (int)(t / p.r_tiles) * 2 * p.rows_cta + (int)rank * p.rows_cta;
                 const int r0 = (int)(t % p.r_tiles) * p.tile_r + (int)rank * (p.tile_r / 2);
-                for (int k = 0; k < p.k_blocks; ++k) {
+                for (int k = 0; k < slots; ++k) {
                     if (use > 0 && !mbar_wait(smem_u32(&empty[s]), (use - 1) & 1, abort_flag)) {
                         ok = false;
                         break;
                     }
-                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), slot_bytes);
+                    const bool with_x = !keep || t == pair;  // resident positions come with the first tile's slots
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * (w_bytes + (with_x ? x_bytes : 0)) *
+                                                                      (uint32_t)min(2, p.k_blocks - 2 * k));
                     const uint32_t at = ring + (uint32_t)s * p.stage_bytes, bar = lead_full + 8u * (uint32_t)s;
-                    tma_load_2d_pair_hint(at, &tm_w, bar, k * kBlockK, v0, w_policy);
-                    if (!keep) tma_load_2d_pair_hint(at + kWBytes, &tm_x, bar, k * kBlockK, r0, x_policy);
+                    load(&tm_w2, &tm_w, at, w_bytes, bar, k, v0, w_policy);
+                    if (with_x)
+                        load(&tm_x2, &tm_x, keep ? resident + 2 * k * x_bytes : at + 2 * w_bytes, x_bytes, bar, k, r0,
+                             x_policy);
                     if (++s == p.stages) {
                         s = 0;
                         ++use;
@@ -199,7 +218,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const bool keep = p.resident_bytes > 0;
             int s = 0, n = 0;
             uint32_t ph = 0;
-            if (keep && pair < p.tiles) ok = mbar_wait(smem_u32(x_full), 0, abort_flag);
             for (int64_t t = pair; t < p.tiles && ok; t += pairs, ++n) {
                 const int b = n & 1;
                 if (n >= 2 && !mbar_wait(smem_u32(&acc_empty[b]), (uint32_t)((n >> 1) - 1) & 1, abort_flag)) {
@@ -208,7 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)b * 256u;
-                for (int k = 0; k < p.k_blocks; ++k) {
+                for (int k = 0; k < slots; ++k) {
                     if (!mbar_wait(smem_u32(&full[s]), ph, abort_flag)) {
                         ok = false;
                         break;
@@ -216,15 +234,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     const uint32_t at = ring + (uint32_t)s * p.stage_bytes;
                     const uint64_t a = smem_desc(at, 16, 1024, 2);
-                    const uint64_t x = smem_desc(keep ? resident + k * x_bytes : at + kWBytes, 16, 1024, 2);
+                    const uint64_t x = smem_desc(keep ? resident + 2 * k * x_bytes : at + 2 * w_bytes, 16, 1024, 2);
                     // 32 codes a step: 32 bytes further along both operands' rows
-                    if (k + 1 < p.k_blocks || p.k_tail == kBlockK / 32) {
+                    if (2 * k + 1 < p.full_blocks) {
 #pragma unroll
-                        for (int j = 0; j < kBlockK / 32; ++j)
-                            umma_e4m3_pair(d_tmem, a + 2 * j, x + 2 * j, p.idesc, (k | j) != 0);
+                        for (int j = 0; j < 8; ++j)
+                            umma_e4m3_pair(d_tmem, a + (j / 4) * (w_bytes >> 4) + 2 * (j % 4),
+                                           x + (j / 4) * (x_bytes >> 4) + 2 * (j % 4), p.idesc, (k | j) != 0);
                     } else {
-                        for (int j = 0; j < p.k_tail; ++j)
-                            umma_e4m3_pair(d_tmem, a + 2 * j, x + 2 * j, p.idesc, (k | j) != 0);
+                        const int steps = p.k_steps - 8 * k;  // of the slot, the last one's cover d
+                        for (int j = 0; j < min(8, steps); ++j)
+                            umma_e4m3_pair(d_tmem, a + (j / 4) * (w_bytes >> 4) + 2 * (j % 4),
+                                           x + (j / 4) * (x_bytes >> 4) + 2 * (j % 4), p.idesc, (k | j) != 0);
                     }
                     umma_commit_pair(smem_u32(&empty[s]), 3);
                     if (++s == p.stages) {
@@ -243,13 +264,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes, and every other chunk of columns
         const uint32_t lead_empty = map_to_cta(smem_u32(&acc_empty[0]), 0);
         T *logits = static_cast<T *>(p.logits);
+        const uint64_t policy = p.stream_logits ? l2_policy_evict_first() : l2_policy_evict_normal();
         // a tile's scales are loaded while the tile before it is stored: a load takes thousands of cycles
         // beside the ring's traffic
         float sx[4], sx_next[4], sw, sw_next = 0.0f;
         auto load_scales = [&](int64_t t) {
-            const int v = (int)(t / p.r_tiles) * kTileV + (int)rank * kRowsCta + quarter * 32 + lane;
+            const int v = (int)(t / p.r_tiles) * 2 * p.rows_cta + (int)rank * p.rows_cta + quarter * 32 + lane;
             const int r = (int)(t % p.r_tiles) * p.tile_r + half * 32 + lane;
-            sw_next = t < p.tiles && v < p.V ? __ldg(p.w_scale + v) : 0.0f;
+            sw_next = t < p.tiles && quarter * 32 + lane < p.rows_cta && v < p.V ? __ldg(p.w_scale + v) : 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) sx_next[i] = t < p.tiles && r + 64 * i < p.R ? __ldg(p.x_scale + r + 64 * i) : 0.0f;
         };
@@ -257,8 +279,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int n = 0;
         for (int64_t t = pair; t < p.tiles; t += pairs, ++n) {
             const int b = n & 1;
-            const int v = (int)(t / p.r_tiles) * kTileV + (int)rank * kRowsCta + quarter * 32 + lane;
+            const int v = (int)(t / p.r_tiles) * 2 * p.rows_cta + (int)rank * p.rows_cta + quarter * 32 + lane;
             const int r0 = (int)(t % p.r_tiles) * p.tile_r;
+            const int live = min(p.rows_cta, p.V - (v - quarter * 32 - lane)) - quarter * 32;  // entries of this quarter
             sw = sw_next;
 #pragma unroll
             for (int i = 0; i < 4; ++i) sx[i] = sx_next[i];
@@ -268,11 +291,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t at = tmem_base + (uint32_t)b * 256u + ((uint32_t)(quarter * 32) << 16);
 #pragma unroll 1
-            for (int c = half * 32; c < p.tile_r && r0 + c < p.R; c += 64) {
+            for (int c = half * 32; live > 0 && c < p.tile_r && r0 + c < p.R; c += 64) {
                 uint32_t acc[32];
                 tmem_ld_32x32b_x32(at + c, acc);
                 tmem_ld_wait();
-                store_chunk(p, logits, acc, r0 + c, v, sw, c < 64 ? sx[0] : c < 128 ? sx[1] : c < 192 ? sx[2] : sx[3]);
+                store_chunk(p, logits, acc, r0 + c, v, lane, live, sw, c < 64 ? sx[0] : c < 128 ? sx[1] : c < 192 ? sx[2] : sx[3],
+                            policy);
             }
             tc_fence_before();
             __syncwarp();
@@ -323,16 +347,23 @@ cudaError_t ensure_head_attributes() {
     return e;
 }
 
-// Rows of codes [rows, d] as boxes of kBlockK columns by `box` rows; what lies past either end is 0.
-bool encode_codes(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *tm, const uint8_t *codes, int64_t rows,
-                  int64_t d, int64_t ld, int box) {
-    const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld};
-    const cuuint32_t boxes[2] = {(cuuint32_t)kBlockK, (cuuint32_t)box};
-    const cuuint32_t estr[2] = {1, 1};
-    return encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes), dims, strides, boxes, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+// Rows of codes [rows, d] as boxes of one block by `box` rows (what lies past either end is 0), and, in a view of
+// the blocks that lie wholly below d, of two blocks.
+bool encode_codes(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *tm, CUtensorMap *tm2, const uint8_t *codes,
+                  int64_t rows, int64_t d, int64_t ld, int box) {
+    const int64_t blocks = d / kBlockK;
+    const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows}, dims2[3] = {kBlockK, (cuuint64_t)rows, (cuuint64_t)blocks};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld, kBlockK};
+    const cuuint32_t boxes[3] = {kBlockK, (cuuint32_t)box, kSlotBlocks};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    auto make = [&](CUtensorMap *m, int rank, const cuuint64_t *dim) {
+        return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<uint8_t *>(codes), dim, strides, boxes, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (!make(tm, 2, dims)) return false;
+    *tm2 = *tm;  // (not used with fewer blocks)
+    return blocks < kSlotBlocks || make(tm2, 3, dims2);
 }
 
 }  // namespace
@@ -351,33 +382,45 @@ cudaError_t launch_head_e4m3(const uint8_t *X, int64_t ldx, const float *x_scale
     p.V = (int)V;
     p.r_tiles = (int)((R + kMaxTileR - 1) / kMaxTileR);
     p.tile_r = (int)(((R + p.r_tiles - 1) / p.r_tiles + 31) / 32 * 32);
-    p.tiles = (V + kTileV - 1) / kTileV * p.r_tiles;
+    // as many rounds of tiles as the largest ones take, and no more table rows in a tile than make those rounds
+    // even (whole 32s: a warp stores whole lines of fp32 logits)
+    const int64_t pairs = std::max(1, device_sm_count() / 2);
+    const int64_t rounds = ((V + kTileV - 1) / kTileV * p.r_tiles + pairs - 1) / pairs;
+    const int64_t v_tiles = std::max<int64_t>(1, rounds * pairs / p.r_tiles);
+    p.rows_cta = (int)std::min<int64_t>(kRowsCta, std::max<int64_t>(kMinRows, ((V + 2 * v_tiles - 1) / (2 * v_tiles) + 31) / 32 * 32));
+    p.tiles = (V + 2 * p.rows_cta - 1) / (2 * p.rows_cta) * p.r_tiles;
     p.k_blocks = (int)((d + kBlockK - 1) / kBlockK);
-    p.k_tail = (int)((d - (int64_t)(p.k_blocks - 1) * kBlockK + 31) / 32);
-    // the positions' codes are the same for every tile where one tile holds them all
-    const int x_bytes = p.tile_r / 2 * kBlockK;
-    p.resident_bytes = p.r_tiles == 1 && p.k_blocks <= kResidentBytes / x_bytes ? p.k_blocks * x_bytes : 0;
-    p.stage_bytes = kWBytes + (p.resident_bytes ? 0 : x_bytes);
-    p.stages = std::min(kMaxStages, (kSmemLimit - kBarrierBytes - 1024 - p.resident_bytes) / p.stage_bytes);
+    p.k_steps = (int)((d + 31) / 32);
+    p.full_blocks = (int)(d / kBlockK);
+    // the positions' codes are the same for every tile where one tile holds them all.  A product reads kRowsCta
+    // table rows from where a tile's begin, whatever lies there past the tile's own: the last slot's need room
+    const int slots = (p.k_blocks + kSlotBlocks - 1) / kSlotBlocks;
+    const int x_slot = kSlotBlocks * (p.tile_r / 2) * kBlockK, slack = (kRowsCta - p.rows_cta) * kBlockK;
+    p.resident_bytes = p.r_tiles == 1 && slots <= kResidentBytes / x_slot ? slots * x_slot : 0;
+    p.stage_bytes = kSlotBlocks * p.rows_cta * kBlockK + (p.resident_bytes ? 0 : x_slot);
+    const int fixed = kBarrierBytes + 1024 + p.resident_bytes + slack;
+    p.stages = std::min(kMaxStages, (kSmemLimit - fixed) / p.stage_bytes);
     p.idesc = idesc_e4m3_f32(kTileV, p.tile_r);
     p.stream_table = p.r_tiles == 1;
+    p.stream_logits = R * V * entry_size(dtype) > (64LL << 20);
     p.x_scale = x_scale;
     p.w_scale = scale;
     p.logits = logits;
     p.ldl = ldl;
-    CUtensorMap tm_x, tm_w;
-    if (!encode_codes(encode, &tm_x, X, R, d, ldx, p.tile_r / 2) || !encode_codes(encode, &tm_w, Q, V, d, ldq, kRowsCta)) {
+    CUtensorMap tm_x, tm_w, tm_x2, tm_w2;
+    if (!encode_codes(encode, &tm_x, &tm_x2, X, R, d, ldx, p.tile_r / 2) ||
+        !encode_codes(encode, &tm_w, &tm_w2, Q, V, d, ldq, p.rows_cta)) {
         *msg = "a tensor map of the head's codes could not be encoded";
         return cudaErrorInvalidValue;
     }
     const cudaError_t e = ensure_head_attributes();
     if (e != cudaSuccess) return e;
-    const int64_t pairs = std::min<int64_t>(p.tiles, std::max(1, device_sm_count() / 2));
-    const int smem = kBarrierBytes + 1024 + p.resident_bytes + p.stages * p.stage_bytes;
+    const unsigned grid = 2 * (unsigned)std::min(p.tiles, pairs);
+    const int smem = fixed + p.stages * p.stage_bytes;
     if (dtype == DG_BF16)
-        head_kernel<__nv_bfloat16><<<(unsigned)(2 * pairs), kThreads, smem, stream>>>(tm_x, tm_w, p);
+        head_kernel<__nv_bfloat16><<<grid, kThreads, smem, stream>>>(tm_x, tm_w, tm_x2, tm_w2, p);
     else
-        head_kernel<float><<<(unsigned)(2 * pairs), kThreads, smem, stream>>>(tm_x, tm_w, p);
+        head_kernel<float><<<grid, kThreads, smem, stream>>>(tm_x, tm_w, tm_x2, tm_w2, p);
     return cudaGetLastError();
 }
 

@@ -248,7 +248,7 @@ dg_status dg_head_e4m3(const uint8_t *X, int64_t ldx, const float *x_scale, int6
     t_last_error[0] = 0;
     const char *what = "head";
     if (R < 0 || d < 1 || V < 1) return fail(DG_ERR_INVALID_ARG, "%s: need R >= 0, d >= 1 and V >= 1", what);
-    if (R > kMaxRows || V > kMaxVocab || d >= (1LL << 24)) return fail(DG_ERR_UNSUPPORTED, "%s: R, V or d too large", what);
+    if (R > kMaxRows || V > (1LL << 30) || d >= (1LL << 24)) return fail(DG_ERR_UNSUPPORTED, "%s: R, V or d too large", what);
     const Rows x{const_cast<uint8_t *>(X), ldx, DG_E4M3}, q{const_cast<uint8_t *>(Q), ldq, DG_E4M3}, l{logits, ldl, dtype};
     DG_TRY(check_rows(what, "X", x, R, d, true));
     DG_TRY(check_rows(what, "Q", q, R > 0 ? V : 0, d, true));

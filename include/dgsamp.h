@@ -799,7 +799,7 @@ size_t dg_rms_norm_backward_workspace_size(int64_t R, int64_t d);
  *   logits   [R, ldl] of dtype (DG_F32: what the sampler's calls take; DG_BF16)
  * The product runs on the tensor cores, whose fp32 sums the scales multiply.  NaN codes (0x7F, 0xFF) make NaN.
  * Requires X, Q and logits 16-byte aligned with row strides of whole 16 bytes (else DG_ERR_UNSUPPORTED); any
- * V and d; columns at d and past it are not read, whatever they hold.  R <= 2^28, d < 2^24.
+ * V and d; columns at d and past it are not read, whatever they hold.  R <= 2^28, V <= 2^30, d < 2^24.
  * R == 0 queues nothing.
  */
 dg_status dg_head_e4m3(const uint8_t *X, int64_t ldx, const float *x_scale, int64_t R, int64_t d, const uint8_t *Q,
