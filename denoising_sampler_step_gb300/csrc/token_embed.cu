@@ -6,13 +6,16 @@
 // Forward: a gather, bound by HBM (a table row and an output row per position) and by latency where there
 // are few positions.
 //
-// Backward: the positions are put in order of their tokens by a stable radix sort in one cluster (its
-// keys stay in L2), so that every table row is written by one warp from its positions in order: no
-// atomics on values, results repeat bit for bit.  The sorted positions are cut into units; a warp takes
-// a unit and 256 columns.  A token that ends within the next unit is finished by the warp it began in.
-// One that covers a whole unit and its neighbours (a mask or padding token) leaves one fp32 part per
-// unit, and a last kernel adds its parts in order.
+// Backward: the positions are put in order of their tokens by a stable radix sort, so that every table row is
+// written once, from its positions in order: no atomics on values, results repeat bit for bit.  The sorted
+// positions are cut into units of up to 64; a warp takes a unit and 256 columns.  A token that ends within the
+// next unit is finished by the warp it began in.  One that covers a whole unit and its neighbours (a mask or
+// padding token) leaves one fp32 part per unit, and a last kernel adds its parts in order.  Up to kFewRows
+// positions one kernel does all of it, every CTA for a few columns of all positions, the parts in shared memory.
+// The kernels of a call start while the one before them ends; the order is found while the gradient is cleared.
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "dg_internal.h"
 #include "hidden.cuh"
@@ -86,11 +89,14 @@ void gather_out(const GatherParams &p, unsigned grid, cudaStream_t stream) {
 // ---------------------------------------------------------------- the order of the tokens
 
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
-constexpr int kMaxBins = 256;
+constexpr int kDigitBits = 10, kMaxBins = 1 << kDigitBits;
+constexpr int kSortCtas = 8;                                    // of the cluster that sorts more than a CTA can
+constexpr int kSortMost = kSortCtas * 8 * kSortThreads;         // positions that fit its registers and shared memory
+constexpr int kFarBits = 8;                                     // digits of the sort through global memory
 
 // Where everything lies in the workspace.
 struct SortSpace {
-    int32_t *key[2], *pos[2];  // sorted: [0]
+    int32_t *key[2], *pos[2];  // sorted: [0]; [1]: of the sort through global memory alone
     int2 *list;                // (unit, key) of the tokens that leave parts
     int32_t *count;
     float *parts;              // [unit][0: begun before it, 1: begun in it][part_ld]
@@ -105,27 +111,227 @@ struct SortParams {
     SortSpace s;
 };
 
+__device__ __forceinline__ int32_t token_key(const SortParams &p, int64_t i) {
+    const int64_t t = p.token[i];
+    if (t >= p.V) atomicOr(&g_device_error, kIndexRange);
+    return t >= p.vocab_start && t < p.vocab_end ? (int32_t)(t - p.vocab_start) : p.none;
+}
+
+// Inclusive sum over the lanes.
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += o;
+    }
+    return v;
+}
+
+__device__ __forceinline__ uint32_t cluster_load(const void *local, uint32_t cta) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_to_cta(smem_u32(local), cta)) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_store(const void *local, uint32_t cta, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_cta(smem_u32(local), cta)), "r"(v) : "memory");
+}
+
+// The lanes whose digit of `bits` bits is this lane's; `in`: the lanes that have one.
+__device__ __forceinline__ uint32_t same_digit(uint32_t digit, int bits, uint32_t in) {
+    uint32_t same = in;
+    for (int b = 0; b < bits; ++b) {
+        const uint32_t set = __ballot_sync(0xffffffffu, (digit >> b) & 1);
+        same &= (digit >> b) & 1 ? set : ~set;
+    }
+    return same;
+}
+
+// Shared memory of a CTA's sort: counts by digit and warp, and the items between passes.
+constexpr int kHistPitch = kSortWarps + 2;  // (17 words: a column's rows lie in different banks)
+struct SortShared {
+    uint32_t total[kMaxBins], start[kMaxBins], warp_total[kSortWarps];
+    uint16_t hist[kMaxBins][kHistPitch];
+};
+constexpr size_t sort_shared_bytes(int items) { return sizeof(SortShared) + (size_t)items * kSortThreads * 8; }
+
+// Stable radix sort of up to N items per thread of each CTA of the cluster, least digit first; an item is a key and
+// its position.  Item i of CTA c is i of N * 1024; a warp takes N * 32 of them in a row.  Leaves the CTA's sorted
+// items in key_s and pos_s (N * kSortThreads each).
+template <int N>
+__device__ void sort_items(const SortParams &p, SortShared &sh, int32_t *key_s, int32_t *pos_s, int ctas, int rank) {
+    constexpr int kItems = N * kSortThreads;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int bins = 1 << p.bits;
+    const int local0 = warp * (N * 32) + lane;  // item j of this thread: local0 + 32 j
+    const int64_t first = (int64_t)rank * kItems;
+    int32_t key[N], pos[N];
+    uint32_t in[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int64_t i = first + local0 + 32 * j;
+        pos[j] = (int32_t)i;
+        key[j] = i < p.R ? token_key(p, i) : 0;
+        in[j] = __ballot_sync(0xffffffffu, i < p.R);
+    }
+    const uint32_t lane_bit = 1u << lane;
+    uint32_t *h32 = reinterpret_cast<uint32_t *>(&sh.hist[0][0]);
+    // a digit's 16 pairs of counts are summed by `per` threads
+    const int per = min(16, kSortThreads >> p.bits), pairs = 16 / per;
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const int shift = pass * p.bits;
+        for (int b = threadIdx.x; b < bins * (kHistPitch / 2); b += kSortThreads) h32[b] = 0;
+        __syncthreads();
+        uint32_t below[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const uint32_t dig = (uint32_t)(key[j] >> shift) & (bins - 1);
+            const uint32_t same = same_digit(dig, p.bits, in[j]);
+            const uint32_t less = __popc(same & (lane_bit - 1));
+            below[j] = sh.hist[dig][warp] + less;
+            __syncwarp();
+            if ((in[j] & lane_bit) && less == 0) sh.hist[dig][warp] += (uint16_t)__popc(same);
+            __syncwarp();
+        }
+        __syncthreads();
+        // over the warps of this CTA, then over the CTAs, then over the digits
+        {
+            const int b = threadIdx.x / per, q = threadIdx.x % per;
+            uint32_t sum = 0;
+            if (b < bins)
+                for (int i = 0; i < pairs; ++i) {
+                    const uint32_t c = h32[b * (kHistPitch / 2) + q * pairs + i];
+                    sum += (c & 0xFFFFu) + (c >> 16);
+                }
+            uint32_t upto = sum;
+            for (int off = 1; off < per; off <<= 1) {
+                const uint32_t o = __shfl_up_sync(0xffffffffu, upto, off);
+                if (q >= off) upto += o;
+            }
+            uint32_t run = upto - sum;
+            if (b < bins) {
+                for (int i = 0; i < pairs; ++i) {
+                    uint32_t *h = &h32[b * (kHistPitch / 2) + q * pairs + i];
+                    const uint32_t c = *h, mid = run + (c & 0xFFFFu);
+                    *h = run | mid << 16;
+                    run = mid + (c >> 16);
+                }
+                if (q == per - 1) sh.total[b] = run;
+            }
+        }
+        __syncthreads();
+        uint32_t all = 0, before = 0;
+        if (ctas > 1) {
+            cluster_sync_all();
+            if ((int)threadIdx.x < bins) {
+                uint32_t t[kSortCtas];
+#pragma unroll
+                for (int c = 0; c < kSortCtas; ++c) t[c] = c < ctas ? cluster_load(&sh.total[threadIdx.x], (uint32_t)c) : 0;
+#pragma unroll
+                for (int c = 0; c < kSortCtas; ++c) {
+                    all += t[c];
+                    if (c < rank) before += t[c];
+                }
+            }
+        } else if ((int)threadIdx.x < bins) {
+            all = sh.total[threadIdx.x];
+        }
+        const uint32_t sum = warp_scan(all, lane);
+        if (lane == 31) sh.warp_total[warp] = sum;
+        __syncthreads();
+        const uint32_t w = __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_total[lane] : 0);
+        if ((int)threadIdx.x < bins) sh.start[threadIdx.x] = before + sum - all + w;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (in[j] & lane_bit) {
+                const uint32_t dig = (uint32_t)(key[j] >> shift) & (bins - 1);
+                const uint32_t at = sh.start[dig] + sh.hist[dig][warp] + below[j];
+                if (ctas > 1) {
+                    cluster_store(&key_s[at % kItems], at / kItems, (uint32_t)key[j]);
+                    cluster_store(&pos_s[at % kItems], at / kItems, (uint32_t)pos[j]);
+                } else {
+                    key_s[at] = key[j];
+                    pos_s[at] = pos[j];
+                }
+            }
+        if (ctas > 1) cluster_sync_all();
+        __syncthreads();
+        if (pass + 1 < p.passes) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (in[j] & lane_bit) {
+                    key[j] = key_s[local0 + 32 * j];
+                    pos[j] = pos_s[local0 + 32 * j];
+                }
+            __syncthreads();
+        }
+    }
+}
+
+// The order of up to kFewRows positions by counting, for each, the items before it: T = kSortThreads / kFewRows threads
+// per position compare it with every T-th four of the others.
+constexpr int kFewRows = 512;
+__device__ __forceinline__ void order_few(const SortParams &p, int32_t *unsorted, int32_t *key_s, int32_t *pos_s) {
+    constexpr int T = kSortThreads / kFewRows;
+    for (int i = threadIdx.x; i < kFewRows; i += kSortThreads) unsorted[i] = i < p.R ? token_key(p, i) : INT32_MAX;
+    __syncthreads();
+    const int i = threadIdx.x / T, q = threadIdx.x % T;
+    if (i < p.R) {  // (whole warps or the lanes of whole positions)
+        const int32_t k = unsorted[i];
+        int n = 0;
+        for (int g = q; 4 * g < p.R; g += T) {
+            const int4 o = reinterpret_cast<const int4 *>(unsorted)[g];
+            const int32_t t = 4 * g + 3 < i ? k + 1 : k;  // equal keys count where they come earlier (k < 2^31 - 1)
+            n += (o.x < t) + (o.y < t) + (o.z < t) + (o.w < t);
+            if (g == i / 4) n += (i % 4 > 0 && o.x == k) + (i % 4 > 1 && o.y == k) + (i % 4 > 2 && o.z == k);
+        }
+#pragma unroll
+        for (int off = 1; off < T; off <<= 1) n += __shfl_xor_sync(__activemask(), n, off);
+        if (q == 0) {
+            key_s[n] = k;
+            pos_s[n] = i;
+        }
+    }
+    __syncthreads();
+}
+
+// The sort of up to kSortMost positions, by one CTA or a cluster of them.
+template <int N>
 __global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(const SortParams p) {
-    __shared__ uint32_t hist[kMaxBins][kSortWarps + 1];
-    __shared__ uint32_t total[kMaxBins], start[kMaxBins], warp_total[kMaxBins / 32];
+    extern __shared__ uint4 smem[];
+    SortShared &sh = *reinterpret_cast<SortShared *>(smem);
+    int32_t *key_s = reinterpret_cast<int32_t *>(&sh + 1), *pos_s = key_s + N * kSortThreads;
+    const int rank = (int)blockIdx.x;
+    grid_launch_dependents();
+    if (rank == 0 && threadIdx.x == 0) *p.s.count = 0;
+    sort_items<N>(p, sh, key_s, pos_s, (int)gridDim.x, rank);
+    const int64_t first = (int64_t)rank * (N * kSortThreads);
+    for (int i = threadIdx.x; i < N * kSortThreads && first + i < p.R; i += kSortThreads) {
+        p.s.key[0][first + i] = key_s[i];
+        p.s.pos[0][first + i] = pos_s[i];
+    }
+    // what clears the gradient has completed before this kernel has, and so before the sums begin
+    grid_dependency_wait();
+}
+
+// The sort of more positions: the same by one cluster through global memory.
+__global__ void __launch_bounds__(kSortThreads) sort_far_kernel(const SortParams p) {
+    __shared__ uint32_t hist[1 << kFarBits][kSortWarps + 1];
+    __shared__ uint32_t total[1 << kFarBits], start[1 << kFarBits], warp_total[(1 << kFarBits) / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ctas = (int)gridDim.x, rank = (int)blockIdx.x;  // one cluster
     const int bins = 1 << p.bits;
     const int per = ((p.R + ctas * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
     const int64_t i0 = (int64_t)(rank * kSortWarps + warp) * per;
     const int n = i0 >= p.R ? 0 : (int)min((int64_t)per, p.R - i0);
+    grid_launch_dependents();
     if (rank == 0 && threadIdx.x == 0) *p.s.count = 0;
 
     for (int pass = 0; pass < p.passes; ++pass) {
         // an odd number of passes begins from the tokens into [0], an even one into [1]
         const int to = (p.passes - 1 - pass) & 1;
         const int shift = pass * p.bits;
-        auto key_at = [&](int64_t i) -> int32_t {
-            if (pass > 0) return __ldcg(p.s.key[to ^ 1] + i);
-            const int64_t t = p.token[i];
-            if (t >= p.V) atomicOr(&g_device_error, kIndexRange);
-            return t >= p.vocab_start && t < p.vocab_end ? (int32_t)(t - p.vocab_start) : p.none;
-        };
+        auto key_at = [&](int64_t i) { return pass > 0 ? __ldcg(p.s.key[to ^ 1] + i) : token_key(p, i); };
         for (int b = threadIdx.x; b < bins * (kSortWarps + 1); b += kSortThreads) (&hist[0][0])[b] = 0;
         __syncthreads();
         for (int i = lane; i < (n + 31) / 32 * 32; i += 32) {
@@ -135,37 +341,22 @@ __global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(const SortPar
             __syncwarp();
         }
         __syncthreads();
-        // over the warps of this CTA, then over the CTAs, then over the digits
         for (int b = warp; b < bins; b += kSortWarps) {
-            const uint32_t own = hist[b][lane];
-            uint32_t sum = own;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const uint32_t o = __shfl_up_sync(0xffffffffu, sum, off);
-                if (lane >= off) sum += o;
-            }
+            const uint32_t own = hist[b][lane], sum = warp_scan(own, lane);
             hist[b][lane] = sum - own;
             if (lane == 31) total[b] = sum;
         }
         __syncthreads();
-        if (ctas > 1) cluster_sync_all();
+        cluster_sync_all();
         uint32_t all = 0, before = 0;
-        if ((int)threadIdx.x < bins) {
-            const uint32_t mine = smem_u32(&total[threadIdx.x]);
+        if ((int)threadIdx.x < bins)
             for (int c = 0; c < ctas; ++c) {
-                uint32_t t;
-                asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(t) : "r"(map_to_cta(mine, (uint32_t)c)) : "memory");
+                const uint32_t t = cluster_load(&total[threadIdx.x], (uint32_t)c);
                 all += t;
                 if (c < rank) before += t;
             }
-        }
-        uint32_t sum = all;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const uint32_t o = __shfl_up_sync(0xffffffffu, sum, off);
-            if (lane >= off) sum += o;
-        }
-        if (warp < kMaxBins / 32 && lane == 31) warp_total[warp] = sum;
+        const uint32_t sum = warp_scan(all, lane);
+        if (warp < (1 << kFarBits) / 32 && lane == 31) warp_total[warp] = sum;
         __syncthreads();
         if ((int)threadIdx.x < bins) {
             uint32_t base = before + sum - all;
@@ -178,171 +369,176 @@ __global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(const SortPar
             const int32_t k = in ? key_at(i0 + i) : 0;
             const uint32_t dig = in ? (uint32_t)(k >> shift) & (bins - 1) : 0xFFFFFFFFu;
             const uint32_t same = __match_any_sync(0xffffffffu, dig);
-            const uint32_t below = __popc(same & ((1u << lane) - 1));
+            const uint32_t less = __popc(same & ((1u << lane) - 1));
             uint32_t at = 0;
-            if (in) at = start[dig] + hist[dig][warp] + below;
+            if (in) at = start[dig] + hist[dig][warp] + less;
             __syncwarp();
             if (in) {
-                if (below == 0) hist[dig][warp] += __popc(same);
+                if (less == 0) hist[dig][warp] += __popc(same);
                 p.s.key[to][at] = k;
                 p.s.pos[to][at] = pass > 0 ? __ldcg(p.s.pos[to ^ 1] + i0 + i) : (int32_t)(i0 + i);
             }
             __syncwarp();
         }
         __threadfence();  // the next pass, and the next kernel, read what other CTAs wrote here
-        if (ctas > 1) cluster_sync_all();
+        cluster_sync_all();
         __syncthreads();
     }
+    grid_dependency_wait();
 }
 
 // ---------------------------------------------------------------- the sums
+
+constexpr int kMaxUnit = 64, kMaxSumWarps = 16;
 
 struct SumParams {
     EmbedRows a;
     SortSpace s;
     int32_t none;
     int unit, units, slabs;  // sorted positions of a unit; slabs of 256 columns
+    int unit_warps, cta_units;  // warps of a unit, units of a CTA
     bool wide_grad, wide_table;
 };
 
-__device__ __forceinline__ void load_entry8(float (&v)[8], const float *q, int n, bool wide) {
-    Raw8<float> r;
-    load8(r, q, n, wide);
-    unpack8(v, r);
-}
-__device__ __forceinline__ void load_entry8(float (&v)[8], const __nv_bfloat16 *q, int n, bool wide) {
-    Raw8<__nv_bfloat16> r;
-    load8(r, q, n, wide);
-    unpack8(v, r);
+// What a unit [u0, u1) of sorted positions sums: [lo, hi), of which the first token's part, begun before it, goes to
+// slot 0, and the last one's, going on after it, to slot 1.
+struct UnitRange {
+    int64_t lo, hi;
+    bool part0, part1;
+};
+
+// `key(i)` for i in [u0 - U - 1, u1 + U] gives the sorted key, or -1 outside [0, R).  A token that covers a whole
+// unit and both its neighbouring positions leaves parts: as its positions are consecutive, a unit sees that from
+// itself, the unit before and the unit after.  A shorter one is summed by the unit it begins in.  All lanes take
+// part and get the same answer.
+template <typename Key>
+__device__ __forceinline__ UnitRange unit_range(const Key &key, int64_t u0, int64_t u1, int U, int32_t none, int lane) {
+    UnitRange r{u0, u1, false, false};
+    auto until = [&](int64_t i, int64_t end, auto same) {  // the first position from i on that is not `same`, or end
+        while (true) {
+            const uint32_t other = __ballot_sync(0xffffffffu, i + lane >= end || !same(key(i + lane)));
+            if (other) return i + __ffs(other) - 1;
+            i += 32;
+        }
+    };
+    const int32_t first = key(u0), last = key(u1 - 1);
+    const bool carry = first != none && key(u0 - 1) == first;
+    if (carry) {
+        r.part0 = key(u0 - U - 1) == first || (u1 == u0 + U && key(u1) == first);
+        if (!r.part0) r.lo = until(u0, u1, [&](int32_t k) { return k == first; });
+    }
+    if (last != none && key(u1) == last && !(carry && last == first)) {
+        r.part1 = key(u1 + U) == last;
+        if (!r.part1) r.hi = until(u1, u1 + U, [&](int32_t k) { return k == last; });
+    }
+    if (last == none) r.hi = until(u0, u1, [&](int32_t k) { return k != none; });
+    return r;
 }
 
-// gW[key][c ..] (+)= gamma sum
-template <typename TT>
-__device__ __forceinline__ void write_row(const EmbedRows &a, int32_t key, int c, const float (&sum)[8], bool wide) {
-    TT *dst = static_cast<TT *>(a.table.p) + (int64_t)key * a.table.ld + c;
-    const int n = (int)a.d - c;
+// gW[key][c ..] (+)= gamma sum; old: what is there, with accumulate
+template <typename TT, bool kAdd>
+__device__ __forceinline__ void write_row(const EmbedRows &a, int32_t key, int c, const float (&sum)[8], const Raw8<TT> &old,
+                                          bool wide) {
     float v[8];
+    if constexpr (kAdd) {
+        unpack8(v, old);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-    if (a.accumulate) load_entry8(v, dst, n, wide);
+        for (int j = 0; j < 8; ++j) v[j] += sum[j] * a.gamma;
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = a.accumulate ? v[j] + sum[j] * a.gamma : sum[j] * a.gamma;
-    store8(dst, v, n, wide);
+        for (int j = 0; j < 8; ++j) v[j] = sum[j] * a.gamma;
+    }
+    store8(static_cast<TT *>(a.table.p) + (int64_t)key * a.table.ld + c, v, (int)a.d - c, wide);
 }
 
-constexpr int kSumWarps = 4;
-
-template <typename TG, typename TT>
-__global__ void __launch_bounds__(32 * kSumWarps) sum_rows_kernel(const SumParams p) {
-    const EmbedRows &a = p.a;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * kSumWarps + (threadIdx.x >> 5);
-    const int m = (int)(w / p.slabs), slab = (int)(w % p.slabs);
-    if (m >= p.units) return;
-    const int R = (int)a.R, U = p.unit;
-    const int32_t *key = p.s.key[0], *pos = p.s.pos[0];
-    const int64_t u0 = (int64_t)m * U, u1 = min((int64_t)R, u0 + U);
-    const int32_t first = key[u0], last = key[u1 - 1];
-    if (first == p.none) return;
-
-    // a token begun before this unit: the warp it began in finishes it, unless it covers a whole unit
-    // and both its neighbours (this one or the one before, if any); then each unit leaves its part
-    int64_t lo = u0, hi = u1;
-    bool part0 = false, part1 = false;
-    if (u0 > 0 && key[u0 - 1] == first) {
-        part0 = (u0 > U && key[u0 - U - 1] == first) || (u1 == u0 + U && u1 < R && key[u1] == first);
-        if (!part0) {
-            while (true) {  // the next token's first position, or the unit's end
-                const int64_t i = lo + lane;
-                const uint32_t other = __ballot_sync(0xffffffffu, i >= u1 || key[i] != first);
-                if (other) {
-                    lo += __ffs(other) - 1;
-                    break;
-                }
-                lo += 32;
-            }
-            if (lo >= u1 || key[lo] == p.none) return;
-        }
-    }
-    // a token that goes on past this unit, and began in it
-    if (u1 < R && last != p.none && key[u1] == last && !(last == first && lo == u0 && u0 > 0 && key[u0 - 1] == first)) {
-        part1 = u1 + U < R && key[u1 + U] == last;
-        if (!part1) {
-            while (true) {
-                const int64_t i = hi + lane;
-                const uint32_t other = __ballot_sync(0xffffffffu, i >= R || key[i] != last);
-                if (other) {
-                    hi += __ffs(other) - 1;
-                    break;
-                }
-                hi += 32;
-            }
-        } else if (slab == 0 && lane == 0) {
-            p.s.list[atomicAdd(p.s.count, 1)] = make_int2(m, last);
-        }
-    }
-
-    const int c = slab * 256 + 8 * lane;
-    const int d = (int)a.d;
-    const TG *g = static_cast<const TG *>(a.rows.p);
+// Sums the positions [r.lo, r.hi) of a unit in eight columns from c on: each token's to its row, parts to part(slot).
+// The rows of kAhead positions are in flight at once, and with them the rows that the finished sums are added to.
+template <typename TG, typename TT, bool kAdd, typename Key, typename Pos, typename Part>
+__device__ __forceinline__ void sum_unit(const EmbedRows &a, const Key &key, const Pos &pos, const Part &part, const UnitRange &r,
+                                         int64_t u0, int c, bool wide_grad, bool wide_table) {
+    constexpr int kAhead = 4;
+    const int n = (int)a.d - c;
+    const TG *g = static_cast<const TG *>(a.rows.p) + c;
+    const TT *table = static_cast<const TT *>(a.table.p) + c;
+    const int32_t first = key(u0);
     float acc[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
-    int32_t cur = key[lo];
-    auto flush = [&](bool at_end) {
-        if (c < d) {
-            if ((part0 && cur == first) || (part1 && at_end)) {
-                float *dst = p.s.parts + ((int64_t)m * 2 + (part0 && cur == first ? 0 : 1)) * p.s.part_ld + c;
-                store8(dst, acc, 8, true);
-            } else {
-                write_row<TT>(a, cur, c, acc, p.wide_table);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
-    };
-    constexpr int kAhead = 8;
-    bool done = false;
-    for (int64_t i = lo; i < hi && !done; i += kAhead) {
+    for (int t = 0; t < 8; ++t) acc[t] = 0.0f;
+    for (int64_t i = r.lo; i < r.hi; i += kAhead) {
         Raw8<TG> raw[kAhead];
+        Raw8<TT> old[kAhead];
         int32_t k[kAhead];
+        bool end[kAhead];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            k[j] = i + j < hi ? key[i + j] : p.none;
-            if (k[j] != p.none && c < d) load8(raw[j], g + (int64_t)pos[i + j] * a.rows.ld + c, d - c, p.wide_grad);
-        }
+        for (int j = 0; j < kAhead; ++j)
+            if (i + j < r.hi) {
+                load8(raw[j], g + (int64_t)pos(i + j) * a.rows.ld, n, wide_grad);
+                k[j] = key(i + j);
+                end[j] = i + j + 1 == r.hi || key(i + j + 1) != k[j];
+                if constexpr (kAdd)
+                    if (end[j]) load8(old[j], table + (int64_t)k[j] * a.table.ld, n, wide_table);
+            }
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            if (done) continue;
-            if (k[j] == p.none) {
-                done = true;
-                continue;
-            }
-            if (k[j] != cur) {
-                flush(false);
-                cur = k[j];
-            }
-            if (c < d) {
+        for (int j = 0; j < kAhead; ++j)
+            if (i + j < r.hi) {
                 float v[8];
                 unpack8(v, raw[j]);
 #pragma unroll
                 for (int t = 0; t < 8; ++t) acc[t] += v[t];
+                if (end[j]) {
+                    if (r.part0 && k[j] == first)
+                        part(0, acc);
+                    else if (r.part1 && i + j + 1 == r.hi)
+                        part(1, acc);
+                    else
+                        write_row<TT, kAdd>(a, k[j], c, acc, old[j], wide_table);
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) acc[t] = 0.0f;
+                }
             }
-        }
     }
-    flush(true);
+}
+
+template <typename TG, typename TT, bool kAdd>
+__global__ void __launch_bounds__(32 * kMaxSumWarps) sum_rows_kernel(const SumParams p) {
+    extern __shared__ int32_t near[];  // this CTA's keys, with a unit and one before and after, and positions
+    const EmbedRows &a = p.a;
+    const int U = p.unit, span = p.cta_units * U, n = span + 2 * U + 2;
+    const int64_t base = (int64_t)blockIdx.x * span, k0 = base - U - 1;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) near[i] = k0 + i >= 0 && k0 + i < a.R ? p.s.key[0][k0 + i] : -1;
+    for (int i = threadIdx.x; i < span + U; i += blockDim.x) near[n + i] = base + i < a.R ? p.s.pos[0][base + i] : 0;
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int m = (int)blockIdx.x * p.cta_units + warp / p.unit_warps;
+    if (m >= p.units) return;
+    const int64_t u0 = (int64_t)m * U, u1 = min(a.R, u0 + U);
+    auto key = [&](int64_t i) { return near[i - k0]; };
+    auto pos = [&](int64_t i) { return near[n + (i - base)]; };
+    const UnitRange r = unit_range(key, u0, u1, U, p.none, lane);
+    if (r.lo >= r.hi) return;
+    if (r.part1 && warp % p.unit_warps == 0 && lane == 0) p.s.list[atomicAdd(p.s.count, 1)] = make_int2(m, key(u1 - 1));
+    for (int slab = warp % p.unit_warps; slab < p.slabs; slab += p.unit_warps) {
+        const int c = slab * 256 + 8 * lane;
+        if (c < a.d)
+            sum_unit<TG, TT, kAdd>(a, key, pos, [&](int slot, const float (&acc)[8]) {
+                store8(p.s.parts + ((int64_t)m * 2 + slot) * p.s.part_ld + c, acc, 8, true);
+            }, r, u0, c, p.wide_grad, p.wide_table);
+    }
 }
 
 constexpr int kJoinWarps = 8;
 
 // Tokens that left parts: unit m's second part, then the first parts of the units after it that begin
 // with the same token.  A CTA takes a token and 128 columns, its warps a share of the parts each.
-template <typename TT>
+template <typename TT, bool kAdd>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_parts_kernel(const SumParams p) {
     __shared__ float acc[kJoinWarps][128];
     const EmbedRows &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slabs = (int)((a.d + 127) / 128);
+    grid_dependency_wait();
     const int64_t items = (int64_t)*p.s.count * slabs;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const int2 e = p.s.list[item / slabs];
@@ -356,12 +552,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_parts_kernel(const SumPa
         }
         const int per = (n + 1 + kJoinWarps - 1) / kJoinWarps;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c < a.d)
-            for (int i = warp * per; i < min(n + 1, (warp + 1) * per); ++i) {
+        if (c < a.d) {
+            const int last = min(n + 1, (warp + 1) * per);
+#pragma unroll 4
+            for (int i = warp * per; i < last; ++i) {
                 const int64_t slot = ((int64_t)e.x + i) * 2 + (i == 0);
                 const float4 v = *reinterpret_cast<const float4 *>(p.s.parts + slot * p.s.part_ld + c);
                 s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
             }
+        }
         *reinterpret_cast<float4 *>(&acc[warp][4 * lane]) = s;
         __syncthreads();
         if (threadIdx.x < 16) {
@@ -373,10 +572,71 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_parts_kernel(const SumPa
                     v[j] = 0.0f;
                     for (int w = 0; w < kJoinWarps; ++w) v[j] += acc[w][8 * threadIdx.x + j];
                 }
-                write_row<TT>(a, e.y, c8, v, p.wide_table);
+                Raw8<TT> old;
+                if constexpr (kAdd)
+                    load8(old, static_cast<const TT *>(a.table.p) + (int64_t)e.y * a.table.ld + c8, (int)a.d - c8,
+                          p.wide_table);
+                write_row<TT, kAdd>(a, e.y, c8, v, old, p.wide_table);
             }
         }
         __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- few positions
+
+constexpr int kFewUnit = 4, kFewLanes = 4;  // positions of a unit; threads of a unit, eight columns each
+constexpr int kFewUnits = kFewRows / kFewUnit;
+constexpr int kFewCols = 8 * kFewLanes;
+
+// All of it in one kernel: a CTA orders the positions for itself, and sums kFewCols columns of all of them, four threads
+// per unit; parts stay in shared memory.
+template <typename TG, typename TT, bool kAdd>
+__global__ void __launch_bounds__(kSortThreads) few_rows_kernel(const SumParams p, const SortParams sp) {
+    __shared__ __align__(16) float parts[kFewUnits][2][kFewCols];
+    __shared__ __align__(16) int32_t unsorted[kFewRows];
+    __shared__ int32_t key_s[kFewRows], pos_s[kFewRows];
+    const EmbedRows &a = p.a;
+    order_few(sp, unsorted, key_s, pos_s);
+    grid_dependency_wait();  // (what clears the gradient)
+    const int R = (int)a.R, U = kFewUnit;
+    auto key = [&](int64_t i) { return i >= 0 && i < R ? key_s[i] : -1; };
+    auto pos = [&](int64_t i) { return pos_s[i]; };
+    const int quad = threadIdx.x / kFewLanes, sub = threadIdx.x % kFewLanes;
+    const int c = (int)blockIdx.x * kFewCols + 8 * sub;
+    const int units = (R + U - 1) / U;
+    // (a warp holds eight units: their ranges one after another, each by all lanes)
+    UnitRange r{0, 0, false, false};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int q = 0; q < 32 / kFewLanes; ++q) {
+        const int m = warp * (32 / kFewLanes) + q;
+        if (m >= units) break;
+        const int64_t u0 = (int64_t)m * U;
+        const UnitRange t = unit_range(key, u0, min((int64_t)R, u0 + U), U, p.none, lane);
+        if (q == lane / kFewLanes) r = t;
+    }
+    const bool on = quad < units && c < a.d;
+    if (on && r.lo < r.hi)
+        sum_unit<TG, TT, kAdd>(a, key, pos, [&](int slot, const float (&acc)[8]) {
+            store8(&parts[quad][slot][8 * sub], acc, 8, true);
+        }, r, (int64_t)quad * U, c, p.wide_grad, p.wide_table);
+    __syncthreads();
+    if (on && r.part1) {  // a token that left parts: this unit's second, then the first ones of those after it
+        const int32_t k = key_s[quad * U + U - 1];
+        float acc[8], v[8];
+        Raw8<TT> old;
+        if constexpr (kAdd)
+            load8(old, static_cast<const TT *>(a.table.p) + (int64_t)k * a.table.ld + c, (int)a.d - c, p.wide_table);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) acc[t] = parts[quad][1][8 * sub + t];
+        for (int m = quad + 1; m < units && key_s[m * U] == k; ++m) {
+            Raw8<float> raw;
+            load8(raw, &parts[m][0][8 * sub], 8, true);
+            unpack8(v, raw);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) acc[t] += v[t];
+        }
+        write_row<TT, kAdd>(a, k, c, acc, old, p.wide_table);
     }
 }
 
@@ -384,6 +644,7 @@ template <typename TT>
 __global__ void __launch_bounds__(256) clear_rows_kernel(const EmbedRows a, int64_t rows, bool wide) {
     const int d = (int)a.d, eights = (d + 7) / 8;
     const float zero[8] = {};
+    grid_launch_dependents();  // the order of the tokens is found meanwhile
     for (int64_t v = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); v < rows; v += (int64_t)gridDim.x * 8)
         for (int c = threadIdx.x & 31; c < eights; c += 32)
             store8(static_cast<TT *>(a.table.p) + v * a.table.ld + 8 * c, zero, d - 8 * c, wide);
@@ -391,13 +652,17 @@ __global__ void __launch_bounds__(256) clear_rows_kernel(const EmbedRows a, int6
 
 // ---------------------------------------------------------------- plan
 
-int unit_of(int64_t R) { return R >= 32768 ? 64 : R >= 8192 ? 32 : 8; }
+// Sorted positions of a unit: long ones where that still leaves every SM some warps of 256 columns.
+int unit_of(int64_t R, int64_t d) {
+    const int64_t warps = (d + 255) / 256 * R;  // of one position each
+    return warps >= 64 * 8192 ? kMaxUnit : warps >= 32 * 4096 ? 32 : 16;
+}
 
 size_t align16(size_t b) { return (b + 15) & ~size_t(15); }
 
 SortSpace lay_out(uint8_t *base, int64_t R, int64_t d, size_t *bytes) {
     SortSpace s;
-    const int64_t units = (R + unit_of(R) - 1) / unit_of(R);
+    const int64_t units = (R + unit_of(R, d) - 1) / unit_of(R, d);
     size_t at = 0;
     auto take = [&](size_t n) {
         uint8_t *q = base + at;
@@ -416,14 +681,71 @@ SortSpace lay_out(uint8_t *base, int64_t R, int64_t d, size_t *bytes) {
     return s;
 }
 
-template <typename TG, typename TT>
-cudaError_t sums(const SumParams &p, cudaStream_t stream) {
-    const int64_t warps = (int64_t)p.units * p.slabs;
-    sum_rows_kernel<TG, TT><<<(unsigned)((warps + kSumWarps - 1) / kSumWarps), 32 * kSumWarps, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.a.R <= p.unit) return e;
-    join_parts_kernel<TT><<<(unsigned)std::max(1, device_sm_count() * 4), 32 * kJoinWarps, 0, stream>>>(p);
-    return cudaGetLastError();
+// Launches that start while the kernel before them ends.
+template <typename... Args>
+cudaError_t launch_chained(void (*kernel)(Args...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream, bool chained,
+                           unsigned cluster, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = chained ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// The shared-memory limit of a kernel, raised once per kernel and device.
+template <typename... Args>
+cudaError_t allow_shared(void (*kernel)(Args...), int which, size_t bytes) {
+    constexpr int kMaxDevices = 64, kKernels = 9;
+    static std::atomic<bool> done[kKernels][kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < kMaxDevices && done[which][dev].load(std::memory_order_acquire))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < kMaxDevices) done[which][dev].store(true, std::memory_order_release);
+    return e;
+}
+
+template <int N>
+cudaError_t sort_near(const SortParams &sp, unsigned ctas, bool chained, cudaStream_t stream) {
+    const cudaError_t e = allow_shared(sort_tokens_kernel<N>, N, sort_shared_bytes(N));
+    if (e != cudaSuccess) return e;
+    return launch_chained(sort_tokens_kernel<N>, ctas, kSortThreads, sort_shared_bytes(N), stream, chained, ctas, sp);
+}
+
+cudaError_t sort_tokens(SortParams sp, bool chained, cudaStream_t stream) {
+    if (sp.R > kSortMost) return launch_chained(sort_far_kernel, kSortCtas, kSortThreads, 0, stream, chained, kSortCtas, sp);
+    const unsigned ctas = sp.R <= 8 * kSortThreads ? 1 : kSortCtas;
+    const int items = (int)((sp.R + ctas * kSortThreads - 1) / (ctas * kSortThreads));
+    return items <= 1   ? sort_near<1>(sp, ctas, chained, stream)
+           : items <= 2 ? sort_near<2>(sp, ctas, chained, stream)
+           : items <= 4 ? sort_near<4>(sp, ctas, chained, stream)
+                        : sort_near<8>(sp, ctas, chained, stream);
+}
+
+template <typename TG, typename TT, bool kAdd>
+cudaError_t sums(const SumParams &p, const SortParams &sp, cudaStream_t stream) {
+    if (p.a.R <= kFewRows) {
+        return launch_chained(few_rows_kernel<TG, TT, kAdd>, (unsigned)((p.a.d + kFewCols - 1) / kFewCols), kSortThreads, 0,
+                              stream, !kAdd, 1u, p, sp);
+    }
+    cudaError_t e = sort_tokens(sp, !kAdd, stream);
+    if (e != cudaSuccess) return e;
+    const unsigned ctas = (unsigned)((p.units + p.cta_units - 1) / p.cta_units);
+    const size_t smem = (size_t)(2 * p.cta_units * p.unit + 3 * p.unit + 2) * sizeof(int32_t);
+    e = launch_chained(sum_rows_kernel<TG, TT, kAdd>, ctas, 32u * p.unit_warps * p.cta_units, smem, stream, true, 1u, p);
+    if (e != cudaSuccess) return e;
+    return launch_chained(join_parts_kernel<TT, kAdd>, (unsigned)std::max(1, device_sm_count() * 4), 32u * kJoinWarps, 0,
+                          stream, true, 1u, p);
 }
 
 }  // namespace
@@ -475,34 +797,29 @@ cudaError_t launch_token_embed_backward(const EmbedRows &a, void *workspace, cud
     sp.none = (int32_t)rows;
     int bits = 1;
     while ((rows >> bits) != 0) ++bits;
-    sp.passes = (bits + 7) / 8;
+    const int most = a.R > kSortMost ? kFarBits : kDigitBits;
+    sp.passes = (bits + most - 1) / most;
     sp.bits = (bits + sp.passes - 1) / sp.passes;
-    cudaLaunchConfig_t cfg = {};
-    const unsigned ctas = a.R <= 2048 ? 1 : 8;
-    cfg.gridDim = dim3(ctas, 1, 1);
-    cfg.blockDim = dim3(kSortThreads, 1, 1);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, sort_tokens_kernel, sp);
-    if (e != cudaSuccess) return e;
     SumParams p{};
     p.a = a;
     p.s = sp.s;
     p.none = sp.none;
-    p.unit = unit_of(a.R);
+    p.unit = unit_of(a.R, a.d);
     p.units = (int)((a.R + p.unit - 1) / p.unit);
     p.slabs = (int)((a.d + 255) / 256);
+    p.unit_warps = std::min(p.slabs, kMaxSumWarps);
+    p.cta_units = std::max(1, 4 / p.unit_warps);
     p.wide_grad = wide_rows(a.rows);
     p.wide_table = wide_table;
-    if (a.rows.dtype == DG_F32)
-        return a.table.dtype == DG_F32 ? sums<float, float>(p, stream) : sums<float, __nv_bfloat16>(p, stream);
-    return a.table.dtype == DG_F32 ? sums<__nv_bfloat16, float>(p, stream) : sums<__nv_bfloat16, __nv_bfloat16>(p, stream);
+    auto typed = [&](auto add) {
+        constexpr bool kAdd = decltype(add)::value;
+        if (a.rows.dtype == DG_F32)
+            return a.table.dtype == DG_F32 ? sums<float, float, kAdd>(p, sp, stream)
+                                           : sums<float, __nv_bfloat16, kAdd>(p, sp, stream);
+        return a.table.dtype == DG_F32 ? sums<__nv_bfloat16, float, kAdd>(p, sp, stream)
+                                       : sums<__nv_bfloat16, __nv_bfloat16, kAdd>(p, sp, stream);
+    };
+    return a.accumulate ? typed(std::true_type()) : typed(std::false_type());
 }
 
 }  // namespace dg
