@@ -14,7 +14,6 @@
 // positions one kernel does all of it, every CTA for a few columns of all positions, the parts in shared memory.
 // The kernels of a call start while the one before them ends; the order is found while the gradient is cleared.
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
 #include "dg_internal.h"
@@ -89,14 +88,13 @@ void gather_out(const GatherParams &p, unsigned grid, cudaStream_t stream) {
 // ---------------------------------------------------------------- the order of the tokens
 
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
-constexpr int kDigitBits = 10, kMaxBins = 1 << kDigitBits;
-constexpr int kSortCtas = 8;                                    // of the cluster that sorts more than a CTA can
-constexpr int kSortMost = kSortCtas * 8 * kSortThreads;         // positions that fit its registers and shared memory
-constexpr int kFarBits = 8;                                     // digits of the sort through global memory
+constexpr int kDigitBits = 8, kMaxBins = 1 << kDigitBits;
+constexpr int kSortMost = 65536;  // positions that are sorted in runs, which are then merged
+constexpr int kSortCtas = 8;      // of the cluster that sorts more
 
 // Where everything lies in the workspace.
 struct SortSpace {
-    int32_t *key[2], *pos[2];  // sorted: [0]; [1]: of the sort through global memory alone
+    int32_t *key[2], *pos[2];  // sorted: [0]; [1]: the runs, or between passes
     int2 *list;                // (unit, key) of the tokens that leave parts
     int32_t *count;
     float *parts;              // [unit][0: begun before it, 1: begun in it][part_ld]
@@ -132,38 +130,60 @@ __device__ __forceinline__ uint32_t cluster_load(const void *local, uint32_t cta
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_to_cta(smem_u32(local), cta)) : "memory");
     return v;
 }
-__device__ __forceinline__ void cluster_store(const void *local, uint32_t cta, uint32_t v) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_cta(smem_u32(local), cta)), "r"(v) : "memory");
-}
-
-// The lanes whose digit of `bits` bits is this lane's; `in`: the lanes that have one.
-__device__ __forceinline__ uint32_t same_digit(uint32_t digit, int bits, uint32_t in) {
+// The lanes whose digit is this lane's; `in`: the lanes that have one.
+__device__ __forceinline__ uint32_t same_digit(uint32_t digit, uint32_t in) {
     uint32_t same = in;
-    for (int b = 0; b < bits; ++b) {
+#pragma unroll
+    for (int b = 0; b < kDigitBits; ++b) {
         const uint32_t set = __ballot_sync(0xffffffffu, (digit >> b) & 1);
         same &= (digit >> b) & 1 ? set : ~set;
     }
     return same;
 }
 
-// Shared memory of a CTA's sort: counts by digit and warp, and the items between passes.
+// Exclusive sums over the digits of this CTA's counts by digit and warp, in place, and each digit's total: 1024 / bins
+// threads sum a digit's 16 pairs of counts.
 constexpr int kHistPitch = kSortWarps + 2;  // (17 words: a column's rows lie in different banks)
-struct SortShared {
-    uint32_t total[kMaxBins], start[kMaxBins], warp_total[kSortWarps];
-    uint16_t hist[kMaxBins][kHistPitch];
-};
-constexpr size_t sort_shared_bytes(int items) { return sizeof(SortShared) + (size_t)items * kSortThreads * 8; }
+__device__ __forceinline__ void scan_warps(uint32_t *hist, uint32_t *total, int bits) {
+    const int per = min(16, kSortThreads >> bits), pairs = 16 / per;
+    const int b = threadIdx.x / per, q = threadIdx.x % per;
+    uint32_t *h = hist + b * (kHistPitch / 2) + q * pairs;
+    uint32_t sum = 0;
+    if (b < 1 << bits)
+        for (int i = 0; i < pairs; ++i) sum += (h[i] & 0xFFFFu) + (h[i] >> 16);
+    uint32_t upto = sum;
+    for (int off = 1; off < per; off <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, upto, off);
+        if (q >= off) upto += o;
+    }
+    if (b < 1 << bits) {
+        uint32_t run = upto - sum;
+        for (int i = 0; i < pairs; ++i) {
+            const uint32_t c = h[i], mid = run + (c & 0xFFFFu);
+            h[i] = run | mid << 16;
+            run = mid + (c >> 16);
+        }
+        if (q == per - 1) total[b] = run;
+    }
+}
 
-// Stable radix sort of up to N items per thread of each CTA of the cluster, least digit first; an item is a key and
-// its position.  Item i of CTA c is i of N * 1024; a warp takes N * 32 of them in a row.  Leaves the CTA's sorted
-// items in key_s and pos_s (N * kSortThreads each).
+// Stable radix sort of a run of N * 1024 positions by one CTA, least digit first, an item's key and position in
+// registers and, between passes, in shared memory; a warp takes N * 32 items in a row.  Run c of the positions goes to
+// place c of `key` and `pos`.  Digits of at most 8 bits: with 10, two passes in place of three, clearing and summing
+// the counts took longer than the pass that it saved.
 template <int N>
-__device__ void sort_items(const SortParams &p, SortShared &sh, int32_t *key_s, int32_t *pos_s, int ctas, int rank) {
+__global__ void __launch_bounds__(kSortThreads) sort_run_kernel(const SortParams p, int32_t *key_out, int32_t *pos_out) {
     constexpr int kItems = N * kSortThreads;
+    __shared__ int32_t key_s[kItems], pos_s[kItems];
+    __shared__ uint32_t total[kMaxBins], start[kMaxBins], warp_total[kSortWarps];
+    __shared__ uint16_t hist[kMaxBins][kHistPitch];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int bins = 1 << p.bits;
     const int local0 = warp * (N * 32) + lane;  // item j of this thread: local0 + 32 j
-    const int64_t first = (int64_t)rank * kItems;
+    const int64_t first = (int64_t)blockIdx.x * kItems;
+    const uint32_t lane_bit = 1u << lane;
+    grid_launch_dependents();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.s.count = 0;
     int32_t key[N], pos[N];
     uint32_t in[N];
 #pragma unroll
@@ -173,99 +193,96 @@ __device__ void sort_items(const SortParams &p, SortShared &sh, int32_t *key_s, 
         key[j] = i < p.R ? token_key(p, i) : 0;
         in[j] = __ballot_sync(0xffffffffu, i < p.R);
     }
-    const uint32_t lane_bit = 1u << lane;
-    uint32_t *h32 = reinterpret_cast<uint32_t *>(&sh.hist[0][0]);
-    // a digit's 16 pairs of counts are summed by `per` threads
-    const int per = min(16, kSortThreads >> p.bits), pairs = 16 / per;
+    uint32_t *h32 = reinterpret_cast<uint32_t *>(&hist[0][0]);
     for (int pass = 0; pass < p.passes; ++pass) {
         const int shift = pass * p.bits;
         for (int b = threadIdx.x; b < bins * (kHistPitch / 2); b += kSortThreads) h32[b] = 0;
+        uint32_t same[N], below[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) same[j] = same_digit((uint32_t)(key[j] >> shift) & (bins - 1), in[j]);
         __syncthreads();
-        uint32_t below[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const uint32_t dig = (uint32_t)(key[j] >> shift) & (bins - 1);
-            const uint32_t same = same_digit(dig, p.bits, in[j]);
-            const uint32_t less = __popc(same & (lane_bit - 1));
-            below[j] = sh.hist[dig][warp] + less;
+            const uint32_t less = __popc(same[j] & (lane_bit - 1));
+            below[j] = hist[dig][warp] + less;
             __syncwarp();
-            if ((in[j] & lane_bit) && less == 0) sh.hist[dig][warp] += (uint16_t)__popc(same);
+            if ((in[j] & lane_bit) && less == 0) hist[dig][warp] += (uint16_t)__popc(same[j]);
             __syncwarp();
         }
         __syncthreads();
-        // over the warps of this CTA, then over the CTAs, then over the digits
-        {
-            const int b = threadIdx.x / per, q = threadIdx.x % per;
-            uint32_t sum = 0;
-            if (b < bins)
-                for (int i = 0; i < pairs; ++i) {
-                    const uint32_t c = h32[b * (kHistPitch / 2) + q * pairs + i];
-                    sum += (c & 0xFFFFu) + (c >> 16);
-                }
-            uint32_t upto = sum;
-            for (int off = 1; off < per; off <<= 1) {
-                const uint32_t o = __shfl_up_sync(0xffffffffu, upto, off);
-                if (q >= off) upto += o;
-            }
-            uint32_t run = upto - sum;
-            if (b < bins) {
-                for (int i = 0; i < pairs; ++i) {
-                    uint32_t *h = &h32[b * (kHistPitch / 2) + q * pairs + i];
-                    const uint32_t c = *h, mid = run + (c & 0xFFFFu);
-                    *h = run | mid << 16;
-                    run = mid + (c >> 16);
-                }
-                if (q == per - 1) sh.total[b] = run;
-            }
-        }
+        scan_warps(h32, total, p.bits);
         __syncthreads();
-        uint32_t all = 0, before = 0;
-        if (ctas > 1) {
-            cluster_sync_all();
-            if ((int)threadIdx.x < bins) {
-                uint32_t t[kSortCtas];
-#pragma unroll
-                for (int c = 0; c < kSortCtas; ++c) t[c] = c < ctas ? cluster_load(&sh.total[threadIdx.x], (uint32_t)c) : 0;
-#pragma unroll
-                for (int c = 0; c < kSortCtas; ++c) {
-                    all += t[c];
-                    if (c < rank) before += t[c];
-                }
-            }
-        } else if ((int)threadIdx.x < bins) {
-            all = sh.total[threadIdx.x];
-        }
-        const uint32_t sum = warp_scan(all, lane);
-        if (lane == 31) sh.warp_total[warp] = sum;
+        const uint32_t all = (int)threadIdx.x < bins ? total[threadIdx.x] : 0, sum = warp_scan(all, lane);
+        if (lane == 31) warp_total[warp] = sum;
         __syncthreads();
-        const uint32_t w = __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_total[lane] : 0);
-        if ((int)threadIdx.x < bins) sh.start[threadIdx.x] = before + sum - all + w;
+        if (threadIdx.x < kMaxBins) {  // (whole warps)
+            const uint32_t w = __reduce_add_sync(0xffffffffu, lane < warp ? warp_total[lane] : 0);
+            start[threadIdx.x] = sum - all + w;
+        }
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < N; ++j)
             if (in[j] & lane_bit) {
                 const uint32_t dig = (uint32_t)(key[j] >> shift) & (bins - 1);
-                const uint32_t at = sh.start[dig] + sh.hist[dig][warp] + below[j];
-                if (ctas > 1) {
-                    cluster_store(&key_s[at % kItems], at / kItems, (uint32_t)key[j]);
-                    cluster_store(&pos_s[at % kItems], at / kItems, (uint32_t)pos[j]);
-                } else {
-                    key_s[at] = key[j];
-                    pos_s[at] = pos[j];
-                }
+                const uint32_t at = start[dig] + hist[dig][warp] + below[j];
+                key_s[at] = key[j];
+                pos_s[at] = pos[j];
             }
-        if (ctas > 1) cluster_sync_all();
         __syncthreads();
-        if (pass + 1 < p.passes) {
 #pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (in[j] & lane_bit) {
-                    key[j] = key_s[local0 + 32 * j];
-                    pos[j] = pos_s[local0 + 32 * j];
-                }
-            __syncthreads();
-        }
+        for (int j = 0; j < N; ++j)
+            if (in[j] & lane_bit) {
+                key[j] = key_s[local0 + 32 * j];
+                pos[j] = pos_s[local0 + 32 * j];
+            }
     }
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (in[j] & lane_bit) {
+            key_out[first + local0 + 32 * j] = key[j];
+            pos_out[first + local0 + 32 * j] = pos[j];
+        }
+    // what clears the gradient has completed before this kernel has, and so before the sums begin
+    grid_dependency_wait();
+}
+
+// Merges sorted runs of `run` positions: an item's place is its own place in its run, and in the other runs that of the
+// first larger key (runs before it) or of the first one not smaller (after it).
+__global__ void __launch_bounds__(256) merge_runs_kernel(const SortParams p, int run) {
+    constexpr int kAtOnce = 4;  // searches
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= p.R) return;
+    const int own = i / run, runs = (p.R + run - 1) / run;
+    const int32_t k = p.s.key[1][i];
+    int at = i - own * run;
+    for (int c0 = 0; c0 < runs; c0 += kAtOnce) {
+        int lo[kAtOnce], hi[kAtOnce], below[kAtOnce];
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) {
+            const int c = c0 + q;
+            lo[q] = min(c * run, p.R);
+            hi[q] = c < runs && c != own ? min((c + 1) * run, p.R) : lo[q];
+            at -= lo[q];
+            below[q] = c < own ? k + 1 : k;  // (k < 2^31 - 1)
+        }
+        for (int step = run; step > 0; step >>= 1)
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q)
+                if (lo[q] < hi[q]) {
+                    const int mid = (lo[q] + hi[q]) >> 1;
+                    if (p.s.key[1][mid] < below[q])
+                        lo[q] = mid + 1;
+                    else
+                        hi[q] = mid;
+                }
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) at += lo[q];
+    }
+    p.s.key[0][at] = k;
+    p.s.pos[0][at] = p.s.pos[1][i];
 }
 
 // The order of up to kFewRows positions by counting, for each, the items before it: T = kSortThreads / kFewRows threads
@@ -295,29 +312,10 @@ __device__ __forceinline__ void order_few(const SortParams &p, int32_t *unsorted
     __syncthreads();
 }
 
-// The sort of up to kSortMost positions, by one CTA or a cluster of them.
-template <int N>
-__global__ void __launch_bounds__(kSortThreads) sort_tokens_kernel(const SortParams p) {
-    extern __shared__ uint4 smem[];
-    SortShared &sh = *reinterpret_cast<SortShared *>(smem);
-    int32_t *key_s = reinterpret_cast<int32_t *>(&sh + 1), *pos_s = key_s + N * kSortThreads;
-    const int rank = (int)blockIdx.x;
-    grid_launch_dependents();
-    if (rank == 0 && threadIdx.x == 0) *p.s.count = 0;
-    sort_items<N>(p, sh, key_s, pos_s, (int)gridDim.x, rank);
-    const int64_t first = (int64_t)rank * (N * kSortThreads);
-    for (int i = threadIdx.x; i < N * kSortThreads && first + i < p.R; i += kSortThreads) {
-        p.s.key[0][first + i] = key_s[i];
-        p.s.pos[0][first + i] = pos_s[i];
-    }
-    // what clears the gradient has completed before this kernel has, and so before the sums begin
-    grid_dependency_wait();
-}
-
 // The sort of more positions: the same by one cluster through global memory.
 __global__ void __launch_bounds__(kSortThreads) sort_far_kernel(const SortParams p) {
-    __shared__ uint32_t hist[1 << kFarBits][kSortWarps + 1];
-    __shared__ uint32_t total[1 << kFarBits], start[1 << kFarBits], warp_total[(1 << kFarBits) / 32];
+    __shared__ uint32_t hist[kMaxBins][kSortWarps + 1];
+    __shared__ uint32_t total[kMaxBins], start[kMaxBins], warp_total[kMaxBins / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ctas = (int)gridDim.x, rank = (int)blockIdx.x;  // one cluster
     const int bins = 1 << p.bits;
@@ -356,7 +354,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_far_kernel(const SortParams
                 if (c < rank) before += t;
             }
         const uint32_t sum = warp_scan(all, lane);
-        if (warp < (1 << kFarBits) / 32 && lane == 31) warp_total[warp] = sum;
+        if (warp < kMaxBins / 32 && lane == 31) warp_total[warp] = sum;
         __syncthreads();
         if ((int)threadIdx.x < bins) {
             uint32_t base = before + sum - all;
@@ -702,34 +700,21 @@ cudaError_t launch_chained(void (*kernel)(Args...), unsigned grid, unsigned thre
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// The shared-memory limit of a kernel, raised once per kernel and device.
-template <typename... Args>
-cudaError_t allow_shared(void (*kernel)(Args...), int which, size_t bytes) {
-    constexpr int kMaxDevices = 64, kKernels = 9;
-    static std::atomic<bool> done[kKernels][kMaxDevices];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || (dev < kMaxDevices && done[which][dev].load(std::memory_order_acquire))) return e;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess && dev < kMaxDevices) done[which][dev].store(true, std::memory_order_release);
-    return e;
-}
-
 template <int N>
-cudaError_t sort_near(const SortParams &sp, unsigned ctas, bool chained, cudaStream_t stream) {
-    const cudaError_t e = allow_shared(sort_tokens_kernel<N>, N, sort_shared_bytes(N));
-    if (e != cudaSuccess) return e;
-    return launch_chained(sort_tokens_kernel<N>, ctas, kSortThreads, sort_shared_bytes(N), stream, chained, ctas, sp);
+cudaError_t sort_runs(const SortParams &sp, bool chained, cudaStream_t stream) {
+    const int run = N * kSortThreads;
+    const unsigned runs = (unsigned)((sp.R + run - 1) / run);
+    const int to = runs > 1;
+    const cudaError_t e = launch_chained(sort_run_kernel<N>, runs, kSortThreads, 0, stream, chained, 1u, sp, sp.s.key[to], sp.s.pos[to]);
+    if (e != cudaSuccess || runs == 1) return e;
+    return launch_chained(merge_runs_kernel, (unsigned)((sp.R + 255) / 256), 256u, 0, stream, true, 1u, sp, run);
 }
 
-cudaError_t sort_tokens(SortParams sp, bool chained, cudaStream_t stream) {
+cudaError_t sort_tokens(const SortParams &sp, bool chained, cudaStream_t stream) {
     if (sp.R > kSortMost) return launch_chained(sort_far_kernel, kSortCtas, kSortThreads, 0, stream, chained, kSortCtas, sp);
-    const unsigned ctas = sp.R <= 8 * kSortThreads ? 1 : kSortCtas;
-    const int items = (int)((sp.R + ctas * kSortThreads - 1) / (ctas * kSortThreads));
-    return items <= 1   ? sort_near<1>(sp, ctas, chained, stream)
-           : items <= 2 ? sort_near<2>(sp, ctas, chained, stream)
-           : items <= 4 ? sort_near<4>(sp, ctas, chained, stream)
-                        : sort_near<8>(sp, ctas, chained, stream);
+    return sp.R <= kSortThreads ? sort_runs<1>(sp, chained, stream)
+           : sp.R <= 8 * kSortThreads ? sort_runs<2>(sp, chained, stream)
+                                      : sort_runs<4>(sp, chained, stream);
 }
 
 template <typename TG, typename TT, bool kAdd>
@@ -797,8 +782,7 @@ cudaError_t launch_token_embed_backward(const EmbedRows &a, void *workspace, cud
     sp.none = (int32_t)rows;
     int bits = 1;
     while ((rows >> bits) != 0) ++bits;
-    const int most = a.R > kSortMost ? kFarBits : kDigitBits;
-    sp.passes = (bits + most - 1) / most;
+    sp.passes = (bits + kDigitBits - 1) / kDigitBits;
     sp.bits = (bits + sp.passes - 1) / sp.passes;
     SumParams p{};
     p.a = a;
