@@ -23,7 +23,7 @@ inline int entry_size(int dtype) { return dtype == DG_F32 ? 4 : dtype == DG_BF16
 // Whether every row starts where eight entries can be moved by the widest accesses (E4M3: 8 bytes, else 16).
 inline bool wide_rows(const Rows &m) {
     const uintptr_t a = m.dtype == DG_E4M3 ? 7 : 15;
-    return (reinterpret_cast<uintptr_t>(m.p) & a) == 0 && (((uintptr_t)m.ld * entry_size(m.dtype)) & a) == 0;
+    return !m.p || ((reinterpret_cast<uintptr_t>(m.p) & a) == 0 && (((uintptr_t)m.ld * entry_size(m.dtype)) & a) == 0);
 }
 
 namespace hidden {
@@ -55,41 +55,46 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// n entries at q (those past n as zeros); wide: q starts where rows may (wide_rows).
-__device__ __forceinline__ void load8(Raw8<float> &r, const float *q, int n, bool wide) {
-    if (wide && n >= 8) {
+// The first n of eight entries at q; the others hold anything (kWide) or zeros.  kWide: q starts where rows may
+// (wide_rows), and whole 16-byte groups (E4M3: 8) that hold an entry are read, without a branch: a choice between
+// kinds of loads at run time, or a branch on n, kept rows from being in flight side by side.
+template <bool kWide>
+__device__ __forceinline__ void load8(Raw8<float> &r, const float *q, int n) {
+    if constexpr (kWide) {
         r.a = *reinterpret_cast<const float4 *>(q);
-        r.b = *reinterpret_cast<const float4 *>(q + 4);
-        return;
-    }
-    float v[8];
+        r.b = n > 4 ? *reinterpret_cast<const float4 *>(q + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
+        float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < n ? q[j] : 0.0f;
-    r.a = make_float4(v[0], v[1], v[2], v[3]);
-    r.b = make_float4(v[4], v[5], v[6], v[7]);
+        for (int j = 0; j < 8; ++j) v[j] = j < n ? q[j] : 0.0f;
+        r.a = make_float4(v[0], v[1], v[2], v[3]);
+        r.b = make_float4(v[4], v[5], v[6], v[7]);
+    }
 }
-__device__ __forceinline__ void load8(Raw8<__nv_bfloat16> &r, const __nv_bfloat16 *q, int n, bool wide) {
-    if (wide && n >= 8) {
+template <bool kWide>
+__device__ __forceinline__ void load8(Raw8<__nv_bfloat16> &r, const __nv_bfloat16 *q, int n) {
+    if constexpr (kWide) {
         r.a = *reinterpret_cast<const uint4 *>(q);
-        return;
-    }
-    uint32_t w[4];
-    const uint16_t *u = reinterpret_cast<const uint16_t *>(q);
+    } else {
+        uint32_t w[4];
+        const uint16_t *u = reinterpret_cast<const uint16_t *>(q);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        w[j] = (2 * j < n ? (uint32_t)u[2 * j] : 0u) | (2 * j + 1 < n ? (uint32_t)u[2 * j + 1] << 16 : 0u);
-    r.a = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int j = 0; j < 4; ++j)
+            w[j] = (2 * j < n ? (uint32_t)u[2 * j] : 0u) | (2 * j + 1 < n ? (uint32_t)u[2 * j + 1] << 16 : 0u);
+        r.a = make_uint4(w[0], w[1], w[2], w[3]);
+    }
 }
-__device__ __forceinline__ void load8(Raw8<E4m3> &r, const E4m3 *q, int n, bool wide) {
-    if (wide && n >= 8) {
+template <bool kWide>
+__device__ __forceinline__ void load8(Raw8<E4m3> &r, const E4m3 *q, int n) {
+    if constexpr (kWide) {
         r.a = *reinterpret_cast<const uint2 *>(q);
-        return;
-    }
-    uint32_t w[2] = {0u, 0u};
+    } else {
+        uint32_t w[2] = {0u, 0u};
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (j < n) w[j >> 2] |= (uint32_t)q[j].code << (8 * (j & 3));
-    r.a = make_uint2(w[0], w[1]);
+        for (int j = 0; j < 8; ++j)
+            if (j < n) w[j >> 2] |= (uint32_t)q[j].code << (8 * (j & 3));
+        r.a = make_uint2(w[0], w[1]);
+    }
 }
 
 __device__ __forceinline__ void unpack8(float (&v)[8], const Raw8<float> &r) {
@@ -114,9 +119,17 @@ __device__ __forceinline__ void unpack8(float (&v)[8], const Raw8<E4m3> &r) {
     }
 }
 
+// Zeros in place of the values from n on.
+__device__ __forceinline__ void mask8(float (&v)[8], int n) {
+    if (n < 8)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < n ? v[j] : 0.0f;
+}
+
 // The first n of eight values, each rounded once.
-__device__ __forceinline__ void store8(float *q, const float (&v)[8], int n, bool wide) {
-    if (wide && n >= 8) {
+template <bool kWide>
+__device__ __forceinline__ void store8(float *q, const float (&v)[8], int n) {
+    if (kWide && n >= 8) {
         *reinterpret_cast<float4 *>(q) = make_float4(v[0], v[1], v[2], v[3]);
         *reinterpret_cast<float4 *>(q + 4) = make_float4(v[4], v[5], v[6], v[7]);
         return;
@@ -125,9 +138,10 @@ __device__ __forceinline__ void store8(float *q, const float (&v)[8], int n, boo
     for (int j = 0; j < 8; ++j)
         if (j < n) q[j] = v[j];
 }
-__device__ __forceinline__ void store8(__nv_bfloat16 *q, const float (&v)[8], int n, bool wide) {
+template <bool kWide>
+__device__ __forceinline__ void store8(__nv_bfloat16 *q, const float (&v)[8], int n) {
     const uint4 w = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-    if (wide && n >= 8) {
+    if (kWide && n >= 8) {
         *reinterpret_cast<uint4 *>(q) = w;
         return;
     }
@@ -136,10 +150,11 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *q, const float (&v)[8], in
     for (int j = 0; j < 8; ++j)
         if (j < n) reinterpret_cast<uint16_t *>(q)[j] = (uint16_t)(u[j >> 1] >> (16 * (j & 1)));
 }
-__device__ __forceinline__ void store8(E4m3 *q, const float (&v)[8], int n, bool wide) {
+template <bool kWide>
+__device__ __forceinline__ void store8(E4m3 *q, const float (&v)[8], int n) {
     const uint2 w = make_uint2(pack_e4m3x2(v[0], v[1]) | pack_e4m3x2(v[2], v[3]) << 16,
                                pack_e4m3x2(v[4], v[5]) | pack_e4m3x2(v[6], v[7]) << 16);
-    if (wide && n >= 8) {
+    if (kWide && n >= 8) {
         *reinterpret_cast<uint2 *>(q) = w;
         return;
     }
@@ -150,22 +165,24 @@ __device__ __forceinline__ void store8(E4m3 *q, const float (&v)[8], int n, bool
 }
 
 // Entries whose type is known at run time only (vectors read again and again, from the caches).
-__device__ __forceinline__ void load8_any(float (&v)[8], const void *p, int dtype, int64_t at, int n, bool wide) {
+template <bool kWide>
+__device__ __forceinline__ void load8_any(float (&v)[8], const void *p, int dtype, int64_t at, int n) {
     if (dtype == DG_F32) {
         Raw8<float> r;
-        load8(r, static_cast<const float *>(p) + at, n, wide);
+        load8<kWide>(r, static_cast<const float *>(p) + at, n);
         unpack8(v, r);
     } else {
         Raw8<__nv_bfloat16> r;
-        load8(r, static_cast<const __nv_bfloat16 *>(p) + at, n, wide);
+        load8<kWide>(r, static_cast<const __nv_bfloat16 *>(p) + at, n);
         unpack8(v, r);
     }
 }
-__device__ __forceinline__ void store8_any(void *p, int dtype, int64_t at, const float (&v)[8], int n, bool wide) {
+template <bool kWide>
+__device__ __forceinline__ void store8_any(void *p, int dtype, int64_t at, const float (&v)[8], int n) {
     if (dtype == DG_F32)
-        store8(static_cast<float *>(p) + at, v, n, wide);
+        store8<kWide>(static_cast<float *>(p) + at, v, n);
     else
-        store8(static_cast<__nv_bfloat16 *>(p) + at, v, n, wide);
+        store8<kWide>(static_cast<__nv_bfloat16 *>(p) + at, v, n);
 }
 
 }  // namespace hidden

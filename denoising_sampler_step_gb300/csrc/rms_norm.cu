@@ -21,7 +21,8 @@ namespace {
 
 using namespace hidden;
 
-constexpr int kMaxThreads = 1024;
+// Threads of a row's CTA, by the eights of columns that each takes (row_shape).
+constexpr int max_threads(int n) { return n == 1 ? 256 : n == 2 ? 512 : 1024; }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -54,11 +55,10 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t *parts) {
 
 struct NormParams {
     NormRows a;
-    bool wide_x, wide_res, wide_hidden, wide_out, wide_w;
 };
 
-template <typename TX, typename TR, typename TO, int N>
-__global__ void __launch_bounds__(kMaxThreads) rms_norm_kernel(const NormParams p) {
+template <typename TX, typename TR, typename TO, int N, bool kWide>
+__global__ void __launch_bounds__(max_threads(N)) rms_norm_kernel(const NormParams p) {
     constexpr bool kCodes = sizeof(TO) == 1;
     __shared__ float sums[32];
     __shared__ uint32_t maxima[32];
@@ -74,13 +74,13 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_kernel(const NormParams 
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int c = 8 * (threadIdx.x + i * blockDim.x);
-            if (c < d) load8(rx[i], x + c, d - c, p.wide_x);
+            if (c < d) load8<kWide>(rx[i], x + c, d - c);
         }
         if (a.residual.p)
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int c = 8 * (threadIdx.x + i * blockDim.x);
-                if (c < d) load8(rr[i], res + c, d - c, p.wide_res);
+                if (c < d) load8<kWide>(rr[i], res + c, d - c);
             }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_kernel(const NormParams 
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[i][j] += t[j];
                 }
+                mask8(v[i], d - c);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_kernel(const NormParams 
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int c = 8 * (threadIdx.x + i * blockDim.x);
-            if (c < d) store8_any(a.hidden.p, a.hidden.dtype, r * a.hidden.ld + c, v[i], d - c, p.wide_hidden);
+            if (c < d) store8_any<kWide>(a.hidden.p, a.hidden.dtype, r * a.hidden.ld + c, v[i], d - c);
         }
     const float mean = cta_sum(s, sums) / (float)d;
     const float rstd = 1.0f / sqrtf(mean + a.eps);
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_kernel(const NormParams 
         if (c < d) {
             float w[8];
             if (a.weight) {
-                load8_any(w, a.weight, a.weight_dtype, c, d - c, p.wide_w);
+                load8_any<kWide>(w, a.weight, a.weight_dtype, c, d - c);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * (a.weight_offset + w[j]);
             } else {
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_kernel(const NormParams 
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] = scale != 0.0f ? __fdiv_rn(v[i][j], scale) : 0.0f;
             }
-            store8(out + c, v[i], d - c, p.wide_out);
+            store8<kWide>(out + c, v[i], d - c);
         }
     }
 }
@@ -160,11 +161,10 @@ struct NormBackParams {
     NormBackRows a;
     float *parts;  // [gridDim.x, part_ld]
     int64_t part_ld;
-    bool wide_g, wide_h, wide_gh, wide_gx, wide_w;
 };
 
-template <typename TG, typename TH, typename TD, int N>
-__global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_kernel(const NormBackParams p) {
+template <typename TG, typename TH, typename TD, int N, bool kWide>
+__global__ void __launch_bounds__(max_threads(N)) rms_norm_backward_kernel(const NormBackParams p) {
     __shared__ float sums[2][32];
     const NormBackRows &a = p.a;
     const int d = (int)a.d;
@@ -184,8 +184,8 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_kernel(const No
         for (int i = 0; i < N; ++i) {
             const int c = 8 * (threadIdx.x + i * blockDim.x);
             if (c < d) {
-                load8(rg[i], gp + c, d - c, p.wide_g);
-                load8(rh[i], hp + c, d - c, p.wide_h);
+                load8<kWide>(rg[i], gp + c, d - c);
+                load8<kWide>(rh[i], hp + c, d - c);
             }
         }
         if (a.grad_hidden.p) {
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_kernel(const No
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int c = 8 * (threadIdx.x + i * blockDim.x);
-                if (c < d) load8(rd[i], dp + c, d - c, p.wide_gh);
+                if (c < d) load8<kWide>(rd[i], dp + c, d - c);
             }
         }
         const float rstd = a.rstd[r];
@@ -206,7 +206,9 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_kernel(const No
                 float w[8], q = 0.0f;
                 unpack8(g[i], rg[i]);
                 unpack8(xh[i], rh[i]);
-                if (a.weight) load8_any(w, a.weight, a.weight_dtype, c, d - c, p.wide_w);
+                mask8(g[i], d - c);
+                mask8(xh[i], d - c);
+                if (a.weight) load8_any<kWide>(w, a.weight, a.weight_dtype, c, d - c);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     xh[i][j] *= rstd;
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_kernel(const No
                 if (a.grad_hidden.p) unpack8(t, rd[i]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) g[i][j] = fmaf(rstd, fmaf(-mean, xh[i][j], g[i][j]), t[j]);
-                store8(static_cast<TH *>(a.grad_x.p) + r * a.grad_x.ld + c, g[i], d - c, p.wide_gx);
+                store8<kWide>(static_cast<TH *>(a.grad_x.p) + r * a.grad_x.ld + c, g[i], d - c);
             }
         }
     }
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_kernel(const No
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int c = 8 * (threadIdx.x + i * blockDim.x);
-            if (c < d) store8(p.parts + blockIdx.x * p.part_ld + c, dw[i], 8, true);
+            if (c < d) store8<true>(p.parts + blockIdx.x * p.part_ld + c, dw[i], 8);
         }
 }
 
@@ -264,25 +266,28 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float *__restri
 
 bool wide_vector(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Threads of a row's CTA and eights of columns per thread.
+// Threads of a row's CTA and eights of columns per thread; wide: all rows start where the widest accesses may.
 struct Shape {
     int threads, n;
+    bool wide;
 };
-Shape row_shape(int64_t d) {
+Shape row_shape(int64_t d, bool wide) {
     const int64_t eights = (d + 7) / 8;
-    const int n = eights <= 256 ? 1 : eights <= 1024 ? 2 : 4;
-    return {(int)(((eights + n - 1) / n + 31) / 32 * 32), n};
+    const int n = !wide ? 4 : eights <= 256 ? 1 : eights <= 1024 ? 2 : 4;
+    return {(int)(((eights + n - 1) / n + 31) / 32 * 32), n, wide};
 }
 
 template <typename TX, typename TR, typename TO>
 void norm_width(const NormParams &p, const Shape &s, cudaStream_t stream) {
     const unsigned grid = (unsigned)p.a.R;
-    if (s.n == 1)
-        rms_norm_kernel<TX, TR, TO, 1><<<grid, s.threads, 0, stream>>>(p);
+    if (!s.wide)
+        rms_norm_kernel<TX, TR, TO, 4, false><<<grid, s.threads, 0, stream>>>(p);
+    else if (s.n == 1)
+        rms_norm_kernel<TX, TR, TO, 1, true><<<grid, s.threads, 0, stream>>>(p);
     else if (s.n == 2)
-        rms_norm_kernel<TX, TR, TO, 2><<<grid, s.threads, 0, stream>>>(p);
+        rms_norm_kernel<TX, TR, TO, 2, true><<<grid, s.threads, 0, stream>>>(p);
     else
-        rms_norm_kernel<TX, TR, TO, 4><<<grid, s.threads, 0, stream>>>(p);
+        rms_norm_kernel<TX, TR, TO, 4, true><<<grid, s.threads, 0, stream>>>(p);
 }
 template <typename TX, typename TR>
 void norm_out(const NormParams &p, const Shape &s, cudaStream_t stream) {
@@ -303,12 +308,14 @@ void norm_residual(const NormParams &p, const Shape &s, cudaStream_t stream) {
 
 template <typename TG, typename TH, typename TD>
 void back_width(const NormBackParams &p, const Shape &s, unsigned grid, cudaStream_t stream) {
-    if (s.n == 1)
-        rms_norm_backward_kernel<TG, TH, TD, 1><<<grid, s.threads, 0, stream>>>(p);
+    if (!s.wide)
+        rms_norm_backward_kernel<TG, TH, TD, 4, false><<<grid, s.threads, 0, stream>>>(p);
+    else if (s.n == 1)
+        rms_norm_backward_kernel<TG, TH, TD, 1, true><<<grid, s.threads, 0, stream>>>(p);
     else if (s.n == 2)
-        rms_norm_backward_kernel<TG, TH, TD, 2><<<grid, s.threads, 0, stream>>>(p);
+        rms_norm_backward_kernel<TG, TH, TD, 2, true><<<grid, s.threads, 0, stream>>>(p);
     else
-        rms_norm_backward_kernel<TG, TH, TD, 4><<<grid, s.threads, 0, stream>>>(p);
+        rms_norm_backward_kernel<TG, TH, TD, 4, true><<<grid, s.threads, 0, stream>>>(p);
 }
 template <typename TG, typename TH>
 void back_residual(const NormBackParams &p, const Shape &s, unsigned grid, cudaStream_t stream) {
@@ -321,16 +328,16 @@ void back_residual(const NormBackParams &p, const Shape &s, unsigned grid, cudaS
 int64_t part_stride(int64_t d) { return (d + 7) / 8 * 8; }
 
 // CTAs of the backward pass: as many rows in work as the SMs' threads allow.
-int64_t back_grid(int64_t R, int64_t d) {
-    const Shape s = row_shape(d);
+int64_t back_grid(int64_t R, const Shape &s) {
     return std::min<int64_t>(R, (int64_t)std::max(1, device_sm_count()) * std::max(1, std::min(16, 1024 / s.threads)));
 }
 
 }  // namespace
 
 cudaError_t launch_rms_norm(const NormRows &a, cudaStream_t stream) {
-    NormParams p{a, wide_rows(a.x), wide_rows(a.residual), wide_rows(a.hidden), wide_rows(a.out), wide_vector(a.weight)};
-    const Shape s = row_shape(a.d);
+    const NormParams p{a};
+    const Shape s = row_shape(a.d, wide_rows(a.x) && wide_rows(a.residual) && wide_rows(a.hidden) && wide_rows(a.out) &&
+                                       wide_vector(a.weight));
     if (a.x.dtype == DG_F32)
         norm_residual<float>(p, s, stream);
     else
@@ -339,20 +346,15 @@ cudaError_t launch_rms_norm(const NormRows &a, cudaStream_t stream) {
 }
 
 size_t rms_norm_backward_bytes(int64_t R, int64_t d) {
-    return (size_t)back_grid(R, d) * (size_t)part_stride(d) * sizeof(float);
+    const int64_t most = std::max(back_grid(R, row_shape(d, true)), back_grid(R, row_shape(d, false)));
+    return (size_t)most * (size_t)part_stride(d) * sizeof(float);
 }
 
 cudaError_t launch_rms_norm_backward(const NormBackRows &a, void *workspace, cudaStream_t stream) {
-    NormBackParams p{a,
-                     static_cast<float *>(workspace),
-                     part_stride(a.d),
-                     wide_rows(a.grad),
-                     wide_rows(a.hidden),
-                     wide_rows(a.grad_hidden),
-                     wide_rows(a.grad_x),
-                     wide_vector(a.weight)};
-    const Shape s = row_shape(a.d);
-    const unsigned grid = (unsigned)back_grid(a.R, a.d);
+    const NormBackParams p{a, static_cast<float *>(workspace), part_stride(a.d)};
+    const Shape s = row_shape(a.d, wide_rows(a.grad) && wide_rows(a.hidden) && wide_rows(a.grad_hidden) &&
+                                       wide_rows(a.grad_x) && wide_vector(a.weight));
+    const unsigned grid = (unsigned)back_grid(a.R, s);
     const bool g32 = a.grad.dtype == DG_F32, h32 = a.hidden.dtype == DG_F32;
     if (a.R > 0) {
         if (g32 && h32)

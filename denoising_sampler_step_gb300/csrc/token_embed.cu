@@ -34,10 +34,9 @@ constexpr int kGatherThreads = 256;
 struct GatherParams {
     EmbedRows a;
     int lanes;  // threads of a row
-    bool wide_table, wide_out;
 };
 
-template <typename TT, typename TO>
+template <typename TT, typename TO, bool kWide>
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherParams p) {
     const EmbedRows &a = p.a;
     const int per_cta = kGatherThreads / p.lanes;
@@ -56,7 +55,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int c = c0 + i * 8 * p.lanes;
-                    if (c < d) load8(raw[i], src + c, d - c, p.wide_table);
+                    if (c < d) load8<kWide>(raw[i], src + c, d - c);
                 }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -71,18 +70,25 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = 0.0f;
                 }
-                store8(dst + c, v, d - c, p.wide_out);
+                store8<kWide>(dst + c, v, d - c);
             }
         }
     }
 }
 
+template <typename TT, typename TO>
+void gather_wide(const GatherParams &p, unsigned grid, cudaStream_t stream) {
+    if (wide_rows(p.a.table) && wide_rows(p.a.rows))
+        gather_kernel<TT, TO, true><<<grid, kGatherThreads, 0, stream>>>(p);
+    else
+        gather_kernel<TT, TO, false><<<grid, kGatherThreads, 0, stream>>>(p);
+}
 template <typename TT>
 void gather_out(const GatherParams &p, unsigned grid, cudaStream_t stream) {
     if (p.a.rows.dtype == DG_F32)
-        gather_kernel<TT, float><<<grid, kGatherThreads, 0, stream>>>(p);
+        gather_wide<TT, float>(p, grid, stream);
     else
-        gather_kernel<TT, __nv_bfloat16><<<grid, kGatherThreads, 0, stream>>>(p);
+        gather_wide<TT, __nv_bfloat16>(p, grid, stream);
 }
 
 // ---------------------------------------------------------------- the order of the tokens
@@ -109,10 +115,29 @@ struct SortParams {
     SortSpace s;
 };
 
-__device__ __forceinline__ int32_t token_key(const SortParams &p, int64_t i) {
-    const int64_t t = p.token[i];
+__device__ __forceinline__ int32_t key_of(const SortParams &p, int64_t t) {
     if (t >= p.V) atomicOr(&g_device_error, kIndexRange);
     return t >= p.vocab_start && t < p.vocab_end ? (int32_t)(t - p.vocab_start) : p.none;
+}
+
+__device__ __forceinline__ int32_t token_key(const SortParams &p, int64_t i) { return key_of(p, p.token[i]); }
+
+// All keys, with the largest number up to the next multiple of four.
+__device__ __forceinline__ void gather_keys(const SortParams &p, int32_t *keys) {
+    constexpr int kAhead = 8;  // loads in flight
+    for (int i0 = threadIdx.x; i0 < (p.R + 3) / 4 * 4; i0 += kAhead * blockDim.x) {
+        int32_t t[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j * blockDim.x;
+            t[j] = i < p.R ? p.token[i] : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j * blockDim.x;
+            if (i < (p.R + 3) / 4 * 4) keys[i] = i < p.R ? key_of(p, t[j]) : INT32_MAX;
+        }
+    }
 }
 
 // Inclusive sum over the lanes.
@@ -168,11 +193,10 @@ __device__ __forceinline__ void scan_warps(uint32_t *hist, uint32_t *total, int 
 }
 
 // Stable radix sort of a run of N * 1024 positions by one CTA, least digit first, an item's key and position in
-// registers and, between passes, in shared memory; a warp takes N * 32 items in a row.  Run c of the positions goes to
-// place c of `key` and `pos`.  Digits of at most 8 bits: with 10, two passes in place of three, clearing and summing
+// registers and, between passes, in shared memory; a warp takes N * 32 items in a row.  Digits of at most 8 bits: with 10, two passes in place of three, clearing and summing
 // the counts took longer than the pass that it saved.
 template <int N>
-__global__ void __launch_bounds__(kSortThreads) sort_run_kernel(const SortParams p, int32_t *key_out, int32_t *pos_out) {
+__global__ void __launch_bounds__(kSortThreads) sort_run_kernel(const SortParams p) {
     constexpr int kItems = N * kSortThreads;
     __shared__ int32_t key_s[kItems], pos_s[kItems];
     __shared__ uint32_t total[kMaxBins], start[kMaxBins], warp_total[kSortWarps];
@@ -240,8 +264,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_run_kernel(const SortParams
 #pragma unroll
     for (int j = 0; j < N; ++j)
         if (in[j] & lane_bit) {
-            key_out[first + local0 + 32 * j] = key[j];
-            pos_out[first + local0 + 32 * j] = pos[j];
+            p.s.key[1][first + local0 + 32 * j] = key[j];
+            p.s.pos[1][first + local0 + 32 * j] = pos[j];
         }
     // what clears the gradient has completed before this kernel has, and so before the sums begin
     grid_dependency_wait();
@@ -285,31 +309,68 @@ __global__ void __launch_bounds__(256) merge_runs_kernel(const SortParams p, int
     p.s.pos[0][at] = p.s.pos[1][i];
 }
 
-// The order of up to kFewRows positions by counting, for each, the items before it: T = kSortThreads / kFewRows threads
-// per position compare it with every T-th four of the others.
+// The order of positions by counting: a position's place is the number of positions before it, those with a smaller
+// key and those before it with the same one.  q of T threads per position i compare it with every T-th four of the
+// keys (`keys`, up to the next multiple of four past R filled with the largest number); all T get the sum.
+template <int T>
+__device__ __forceinline__ int count_before(const int32_t *keys, int R, int i, int q) {
+    const int32_t k = keys[i];
+    const int4 *fours = reinterpret_cast<const int4 *>(keys);
+    const int own = i / 4, all = (R + 3) / 4;
+    int n = 0, g = q;
+    // equal keys count where they come earlier (k < 2^31 - 1)
+#pragma unroll 4
+    for (; g < own; g += T) {
+        const int4 o = fours[g];
+        n += (o.x <= k) + (o.y <= k) + (o.z <= k) + (o.w <= k);
+    }
+    if (g == own) {
+        const int4 o = fours[g];
+        n += (o.x < k || (o.x == k && i % 4 > 0)) + (o.y < k || (o.y == k && i % 4 > 1)) +
+             (o.z < k || (o.z == k && i % 4 > 2)) + (o.w < k);
+        g += T;
+    }
+#pragma unroll 4
+    for (; g < all; g += T) {
+        const int4 o = fours[g];
+        n += (o.x < k) + (o.y < k) + (o.z < k) + (o.w < k);
+    }
+#pragma unroll
+    for (int off = 1; off < T; off <<= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
+    return n;
+}
+
+// By one CTA, up to kFewRows.
 constexpr int kFewRows = 512;
 __device__ __forceinline__ void order_few(const SortParams &p, int32_t *unsorted, int32_t *key_s, int32_t *pos_s) {
     constexpr int T = kSortThreads / kFewRows;
-    for (int i = threadIdx.x; i < kFewRows; i += kSortThreads) unsorted[i] = i < p.R ? token_key(p, i) : INT32_MAX;
+    gather_keys(p, unsorted);
     __syncthreads();
-    const int i = threadIdx.x / T, q = threadIdx.x % T;
-    if (i < p.R) {  // (whole warps or the lanes of whole positions)
-        const int32_t k = unsorted[i];
-        int n = 0;
-        for (int g = q; 4 * g < p.R; g += T) {
-            const int4 o = reinterpret_cast<const int4 *>(unsorted)[g];
-            const int32_t t = 4 * g + 3 < i ? k + 1 : k;  // equal keys count where they come earlier (k < 2^31 - 1)
-            n += (o.x < t) + (o.y < t) + (o.z < t) + (o.w < t);
-            if (g == i / 4) n += (i % 4 > 0 && o.x == k) + (i % 4 > 1 && o.y == k) + (i % 4 > 2 && o.z == k);
-        }
-#pragma unroll
-        for (int off = 1; off < T; off <<= 1) n += __shfl_xor_sync(__activemask(), n, off);
-        if (q == 0) {
-            key_s[n] = k;
-            pos_s[n] = i;
-        }
+    const int i = threadIdx.x / T;
+    const int n = count_before<T>(unsorted, p.R, min(i, p.R - 1), threadIdx.x % T);
+    if (i < p.R && threadIdx.x % T == 0) {
+        key_s[n] = unsorted[i];
+        pos_s[n] = i;
     }
     __syncthreads();
+}
+
+// By the whole chip, up to kCountRows.
+constexpr int kCountRows = 4096, kCountThreads = 512, kCountShare = 8;
+__global__ void __launch_bounds__(kCountThreads) count_tokens_kernel(const SortParams p) {
+    __shared__ __align__(16) int32_t keys[kCountRows];
+    grid_launch_dependents();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.s.count = 0;
+    gather_keys(p, keys);
+    __syncthreads();
+    const int i = (int)blockIdx.x * (kCountThreads / kCountShare) + threadIdx.x / kCountShare;
+    const int n = count_before<kCountShare>(keys, p.R, min(i, p.R - 1), threadIdx.x % kCountShare);
+    if (i < p.R && threadIdx.x % kCountShare == 0) {
+        p.s.key[0][n] = keys[i];
+        p.s.pos[0][n] = i;
+    }
+    // what clears the gradient has completed before this kernel has, and so before the sums begin
+    grid_dependency_wait();
 }
 
 // The sort of more positions: the same by one cluster through global memory.
@@ -387,32 +448,31 @@ __global__ void __launch_bounds__(kSortThreads) sort_far_kernel(const SortParams
 
 // ---------------------------------------------------------------- the sums
 
-constexpr int kMaxUnit = 64, kMaxSumWarps = 16;
+constexpr int kSumWarps = 4, kSumAhead = 4;
 
 struct SumParams {
     EmbedRows a;
     SortSpace s;
     int32_t none;
     int unit, units, slabs;  // sorted positions of a unit; slabs of 256 columns
-    int unit_warps, cta_units;  // warps of a unit, units of a CTA
-    bool wide_grad, wide_table;
+    int unit_warps, cta_units, slab_ctas;  // warps of a unit in a CTA, units of a CTA, CTAs that share a unit's slabs
 };
 
 // What a unit [u0, u1) of sorted positions sums: [lo, hi), of which the first token's part, begun before it, goes to
 // slot 0, and the last one's, going on after it, to slot 1.
 struct UnitRange {
-    int64_t lo, hi;
+    int lo, hi;
     bool part0, part1;
 };
 
-// `key(i)` for i in [u0 - U - 1, u1 + U] gives the sorted key, or -1 outside [0, R).  A token that covers a whole
-// unit and both its neighbouring positions leaves parts: as its positions are consecutive, a unit sees that from
+// `key(i)` for i in [u0 - U - 1, u1 + U] gives the sorted key, or -1 where there is no position.  A token that covers a
+// whole unit and both its neighbouring positions leaves parts: as its positions are consecutive, a unit sees that from
 // itself, the unit before and the unit after.  A shorter one is summed by the unit it begins in.  All lanes take
 // part and get the same answer.
 template <typename Key>
-__device__ __forceinline__ UnitRange unit_range(const Key &key, int64_t u0, int64_t u1, int U, int32_t none, int lane) {
+__device__ __forceinline__ UnitRange unit_range(const Key &key, int u0, int u1, int U, int32_t none, int lane) {
     UnitRange r{u0, u1, false, false};
-    auto until = [&](int64_t i, int64_t end, auto same) {  // the first position from i on that is not `same`, or end
+    auto until = [&](int i, int end, auto same) {  // the first position from i on that is not `same`, or end
         while (true) {
             const uint32_t other = __ballot_sync(0xffffffffu, i + lane >= end || !same(key(i + lane)));
             if (other) return i + __ffs(other) - 1;
@@ -434,9 +494,8 @@ __device__ __forceinline__ UnitRange unit_range(const Key &key, int64_t u0, int6
 }
 
 // gW[key][c ..] (+)= gamma sum; old: what is there, with accumulate
-template <typename TT, bool kAdd>
-__device__ __forceinline__ void write_row(const EmbedRows &a, int32_t key, int c, const float (&sum)[8], const Raw8<TT> &old,
-                                          bool wide) {
+template <typename TT, bool kAdd, bool kWide>
+__device__ __forceinline__ void write_row(const EmbedRows &a, int32_t key, int c, const float (&sum)[8], const Raw8<TT> &old) {
     float v[8];
     if constexpr (kAdd) {
         unpack8(v, old);
@@ -446,15 +505,15 @@ __device__ __forceinline__ void write_row(const EmbedRows &a, int32_t key, int c
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = sum[j] * a.gamma;
     }
-    store8(static_cast<TT *>(a.table.p) + (int64_t)key * a.table.ld + c, v, (int)a.d - c, wide);
+    store8<kWide>(static_cast<TT *>(a.table.p) + (int64_t)key * a.table.ld + c, v, (int)a.d - c);
 }
 
 // Sums the positions [r.lo, r.hi) of a unit in eight columns from c on: each token's to its row, parts to part(slot).
-// The rows of kAhead positions are in flight at once, and with them the rows that the finished sums are added to.
-template <typename TG, typename TT, bool kAdd, typename Key, typename Pos, typename Part>
+// The rows of kAhead positions are in flight at once, and with them the rows that their sums may be added to (those of
+// one token's positions come from L1 but once), without a branch between the loads.
+template <int kAhead, typename TG, typename TT, bool kAdd, bool kWide, typename Key, typename Pos, typename Part>
 __device__ __forceinline__ void sum_unit(const EmbedRows &a, const Key &key, const Pos &pos, const Part &part, const UnitRange &r,
-                                         int64_t u0, int c, bool wide_grad, bool wide_table) {
-    constexpr int kAhead = 4;
+                                         int u0, int c) {
     const int n = (int)a.d - c;
     const TG *g = static_cast<const TG *>(a.rows.p) + c;
     const TT *table = static_cast<const TT *>(a.table.p) + c;
@@ -462,75 +521,70 @@ __device__ __forceinline__ void sum_unit(const EmbedRows &a, const Key &key, con
     float acc[8];
 #pragma unroll
     for (int t = 0; t < 8; ++t) acc[t] = 0.0f;
-    for (int64_t i = r.lo; i < r.hi; i += kAhead) {
+    for (int i = r.lo; i < r.hi; i += kAhead) {
         Raw8<TG> raw[kAhead];
         Raw8<TT> old[kAhead];
-        int32_t k[kAhead];
-        bool end[kAhead];
+        int32_t k[kAhead + 1];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (i + j < r.hi) {
-                load8(raw[j], g + (int64_t)pos(i + j) * a.rows.ld, n, wide_grad);
-                k[j] = key(i + j);
-                end[j] = i + j + 1 == r.hi || key(i + j + 1) != k[j];
-                if constexpr (kAdd)
-                    if (end[j]) load8(old[j], table + (int64_t)k[j] * a.table.ld, n, wide_table);
+        for (int j = 0; j <= kAhead; ++j) k[j] = i + j < r.hi ? key(i + j) : -1;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            load8<kWide>(raw[j], g + (int64_t)pos(min(i + j, r.hi - 1)) * a.rows.ld, n);
+            if constexpr (kAdd) load8<kWide>(old[j], table + (int64_t)max(k[j], 0) * a.table.ld, n);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            float v[8];
+            unpack8(v, raw[j]);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) acc[t] += v[t];
+            if (k[j] != k[j + 1]) {  // (at the end -1 follows the last key, and itself)
+                if (r.part0 && k[j] == first)
+                    part(0, acc);
+                else if (r.part1 && i + j + 1 == r.hi)
+                    part(1, acc);
+                else
+                    write_row<TT, kAdd, kWide>(a, k[j], c, acc, old[j]);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) acc[t] = 0.0f;
             }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (i + j < r.hi) {
-                float v[8];
-                unpack8(v, raw[j]);
-#pragma unroll
-                for (int t = 0; t < 8; ++t) acc[t] += v[t];
-                if (end[j]) {
-                    if (r.part0 && k[j] == first)
-                        part(0, acc);
-                    else if (r.part1 && i + j + 1 == r.hi)
-                        part(1, acc);
-                    else
-                        write_row<TT, kAdd>(a, k[j], c, acc, old[j], wide_table);
-#pragma unroll
-                    for (int t = 0; t < 8; ++t) acc[t] = 0.0f;
-                }
-            }
+        }
     }
 }
 
-template <typename TG, typename TT, bool kAdd>
-__global__ void __launch_bounds__(32 * kMaxSumWarps) sum_rows_kernel(const SumParams p) {
+template <typename TG, typename TT, bool kAdd, bool kWide>
+__global__ void __launch_bounds__(32 * kSumWarps) sum_rows_kernel(const SumParams p) {
     extern __shared__ int32_t near[];  // this CTA's keys, with a unit and one before and after, and positions
     const EmbedRows &a = p.a;
     const int U = p.unit, span = p.cta_units * U, n = span + 2 * U + 2;
-    const int64_t base = (int64_t)blockIdx.x * span, k0 = base - U - 1;
+    const int group = (int)blockIdx.x / p.slab_ctas, base = group * span, k0 = base - U - 1, R = (int)a.R;
     grid_dependency_wait();
     grid_launch_dependents();
-    for (int i = threadIdx.x; i < n; i += blockDim.x) near[i] = k0 + i >= 0 && k0 + i < a.R ? p.s.key[0][k0 + i] : -1;
-    for (int i = threadIdx.x; i < span + U; i += blockDim.x) near[n + i] = base + i < a.R ? p.s.pos[0][base + i] : 0;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) near[i] = k0 + i >= 0 && k0 + i < R ? p.s.key[0][k0 + i] : -1;
+    for (int i = threadIdx.x; i < span + U; i += blockDim.x) near[n + i] = base + i < R ? p.s.pos[0][base + i] : 0;
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int m = (int)blockIdx.x * p.cta_units + warp / p.unit_warps;
+    const int m = group * p.cta_units + warp / p.unit_warps;
     if (m >= p.units) return;
-    const int64_t u0 = (int64_t)m * U, u1 = min(a.R, u0 + U);
-    auto key = [&](int64_t i) { return near[i - k0]; };
-    auto pos = [&](int64_t i) { return near[n + (i - base)]; };
+    const int slab0 = (int)blockIdx.x % p.slab_ctas * p.unit_warps + warp % p.unit_warps;
+    const int u0 = m * U, u1 = min(R, u0 + U);
+    auto key = [&](int i) { return near[i - k0]; };
+    auto pos = [&](int i) { return near[n + (i - base)]; };
     const UnitRange r = unit_range(key, u0, u1, U, p.none, lane);
     if (r.lo >= r.hi) return;
-    if (r.part1 && warp % p.unit_warps == 0 && lane == 0) p.s.list[atomicAdd(p.s.count, 1)] = make_int2(m, key(u1 - 1));
-    for (int slab = warp % p.unit_warps; slab < p.slabs; slab += p.unit_warps) {
-        const int c = slab * 256 + 8 * lane;
-        if (c < a.d)
-            sum_unit<TG, TT, kAdd>(a, key, pos, [&](int slot, const float (&acc)[8]) {
-                store8(p.s.parts + ((int64_t)m * 2 + slot) * p.s.part_ld + c, acc, 8, true);
-            }, r, u0, c, p.wide_grad, p.wide_table);
-    }
+    if (r.part1 && slab0 == 0 && lane == 0) p.s.list[atomicAdd(p.s.count, 1)] = make_int2(m, key(u1 - 1));
+    const int c = slab0 * 256 + 8 * lane;
+    if (c < a.d)
+        sum_unit<kSumAhead, TG, TT, kAdd, kWide>(a, key, pos, [&](int slot, const float (&acc)[8]) {
+            store8<true>(p.s.parts + ((int64_t)m * 2 + slot) * p.s.part_ld + c, acc, 8);
+        }, r, u0, c);
 }
 
 constexpr int kJoinWarps = 8;
 
 // Tokens that left parts: unit m's second part, then the first parts of the units after it that begin
 // with the same token.  A CTA takes a token and 128 columns, its warps a share of the parts each.
-template <typename TT, bool kAdd>
+template <typename TT, bool kAdd, bool kWide>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_parts_kernel(const SumParams p) {
     __shared__ float acc[kJoinWarps][128];
     const EmbedRows &a = p.a;
@@ -572,9 +626,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_parts_kernel(const SumPa
                 }
                 Raw8<TT> old;
                 if constexpr (kAdd)
-                    load8(old, static_cast<const TT *>(a.table.p) + (int64_t)e.y * a.table.ld + c8, (int)a.d - c8,
-                          p.wide_table);
-                write_row<TT, kAdd>(a, e.y, c8, v, old, p.wide_table);
+                    load8<kWide>(old, static_cast<const TT *>(a.table.p) + (int64_t)e.y * a.table.ld + c8, (int)a.d - c8);
+                write_row<TT, kAdd, kWide>(a, e.y, c8, v, old);
             }
         }
         __syncthreads();
@@ -589,7 +642,7 @@ constexpr int kFewCols = 8 * kFewLanes;
 
 // All of it in one kernel: a CTA orders the positions for itself, and sums kFewCols columns of all of them, four threads
 // per unit; parts stay in shared memory.
-template <typename TG, typename TT, bool kAdd>
+template <typename TG, typename TT, bool kAdd, bool kWide>
 __global__ void __launch_bounds__(kSortThreads) few_rows_kernel(const SumParams p, const SortParams sp) {
     __shared__ __align__(16) float parts[kFewUnits][2][kFewCols];
     __shared__ __align__(16) int32_t unsorted[kFewRows];
@@ -598,8 +651,8 @@ __global__ void __launch_bounds__(kSortThreads) few_rows_kernel(const SumParams 
     order_few(sp, unsorted, key_s, pos_s);
     grid_dependency_wait();  // (what clears the gradient)
     const int R = (int)a.R, U = kFewUnit;
-    auto key = [&](int64_t i) { return i >= 0 && i < R ? key_s[i] : -1; };
-    auto pos = [&](int64_t i) { return pos_s[i]; };
+    auto key = [&](int i) { return i >= 0 && i < R ? key_s[i] : -1; };
+    auto pos = [&](int i) { return pos_s[i]; };
     const int quad = threadIdx.x / kFewLanes, sub = threadIdx.x % kFewLanes;
     const int c = (int)blockIdx.x * kFewCols + 8 * sub;
     const int units = (R + U - 1) / U;
@@ -609,43 +662,53 @@ __global__ void __launch_bounds__(kSortThreads) few_rows_kernel(const SumParams 
     for (int q = 0; q < 32 / kFewLanes; ++q) {
         const int m = warp * (32 / kFewLanes) + q;
         if (m >= units) break;
-        const int64_t u0 = (int64_t)m * U;
-        const UnitRange t = unit_range(key, u0, min((int64_t)R, u0 + U), U, p.none, lane);
+        const UnitRange t = unit_range(key, m * U, min(R, m * U + U), U, p.none, lane);
         if (q == lane / kFewLanes) r = t;
     }
     const bool on = quad < units && c < a.d;
     if (on && r.lo < r.hi)
-        sum_unit<TG, TT, kAdd>(a, key, pos, [&](int slot, const float (&acc)[8]) {
-            store8(&parts[quad][slot][8 * sub], acc, 8, true);
-        }, r, (int64_t)quad * U, c, p.wide_grad, p.wide_table);
+        sum_unit<4, TG, TT, kAdd, kWide>(a, key, pos, [&](int slot, const float (&acc)[8]) {
+            store8<true>(&parts[quad][slot][8 * sub], acc, 8);
+        }, r, quad * U, c);
     __syncthreads();
-    if (on && r.part1) {  // a token that left parts: this unit's second, then the first ones of those after it
-        const int32_t k = key_s[quad * U + U - 1];
-        float acc[8], v[8];
-        Raw8<TT> old;
-        if constexpr (kAdd)
-            load8(old, static_cast<const TT *>(a.table.p) + (int64_t)k * a.table.ld + c, (int)a.d - c, p.wide_table);
+    // tokens that left parts: their unit's second, then the first ones of those after it, by all of the warp
+    uint32_t longs = __ballot_sync(0xffffffffu, quad < units && r.part1 && sub == 0);
+    while (longs) {
+        const int owner = (warp * 32 + __ffs(longs) - 1) / kFewLanes;
+        longs &= longs - 1;
+        const int32_t k = key_s[owner * U + U - 1];
+        float acc[8];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) acc[t] = parts[quad][1][8 * sub + t];
-        for (int m = quad + 1; m < units && key_s[m * U] == k; ++m) {
+        for (int t = 0; t < 8; ++t) acc[t] = lane < kFewLanes ? parts[owner][1][8 * sub + t] : 0.0f;
+        for (int m = owner + 1 + lane / kFewLanes; m < units && key_s[m * U] == k; m += 32 / kFewLanes) {
             Raw8<float> raw;
-            load8(raw, &parts[m][0][8 * sub], 8, true);
+            float v[8];
+            load8<true>(raw, &parts[m][0][8 * sub], 8);
             unpack8(v, raw);
 #pragma unroll
             for (int t = 0; t < 8; ++t) acc[t] += v[t];
         }
-        write_row<TT, kAdd>(a, k, c, acc, old, p.wide_table);
+#pragma unroll
+        for (int off = kFewLanes; off < 32; off <<= 1)
+#pragma unroll
+            for (int t = 0; t < 8; ++t) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], off);
+        if (lane < kFewLanes && c < a.d) {
+            Raw8<TT> old;
+            if constexpr (kAdd)
+                load8<kWide>(old, static_cast<const TT *>(a.table.p) + (int64_t)k * a.table.ld + c, (int)a.d - c);
+            write_row<TT, kAdd, kWide>(a, k, c, acc, old);
+        }
     }
 }
 
-template <typename TT>
-__global__ void __launch_bounds__(256) clear_rows_kernel(const EmbedRows a, int64_t rows, bool wide) {
+template <typename TT, bool kWide>
+__global__ void __launch_bounds__(256) clear_rows_kernel(const EmbedRows a, int64_t rows) {
     const int d = (int)a.d, eights = (d + 7) / 8;
     const float zero[8] = {};
     grid_launch_dependents();  // the order of the tokens is found meanwhile
     for (int64_t v = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); v < rows; v += (int64_t)gridDim.x * 8)
         for (int c = threadIdx.x & 31; c < eights; c += 32)
-            store8(static_cast<TT *>(a.table.p) + v * a.table.ld + 8 * c, zero, d - 8 * c, wide);
+            store8<kWide>(static_cast<TT *>(a.table.p) + v * a.table.ld + 8 * c, zero, d - 8 * c);
 }
 
 // ---------------------------------------------------------------- plan
@@ -653,7 +716,7 @@ __global__ void __launch_bounds__(256) clear_rows_kernel(const EmbedRows a, int6
 // Sorted positions of a unit: long ones where that still leaves every SM some warps of 256 columns.
 int unit_of(int64_t R, int64_t d) {
     const int64_t warps = (d + 255) / 256 * R;  // of one position each
-    return warps >= 64 * 8192 ? kMaxUnit : warps >= 32 * 4096 ? 32 : 16;
+    return warps >= 32 * 2048 ? 32 : 16;
 }
 
 size_t align16(size_t b) { return (b + 15) & ~size_t(15); }
@@ -700,43 +763,44 @@ cudaError_t launch_chained(void (*kernel)(Args...), unsigned grid, unsigned thre
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+constexpr int kRunItems = 4;  // positions per thread of a run
+
 template <int N>
 cudaError_t sort_runs(const SortParams &sp, bool chained, cudaStream_t stream) {
     const int run = N * kSortThreads;
     const unsigned runs = (unsigned)((sp.R + run - 1) / run);
-    const int to = runs > 1;
-    const cudaError_t e = launch_chained(sort_run_kernel<N>, runs, kSortThreads, 0, stream, chained, 1u, sp, sp.s.key[to], sp.s.pos[to]);
-    if (e != cudaSuccess || runs == 1) return e;
+    const cudaError_t e = launch_chained(sort_run_kernel<N>, runs, kSortThreads, 0, stream, chained, 1u, sp);
+    if (e != cudaSuccess) return e;
     return launch_chained(merge_runs_kernel, (unsigned)((sp.R + 255) / 256), 256u, 0, stream, true, 1u, sp, run);
 }
 
 cudaError_t sort_tokens(const SortParams &sp, bool chained, cudaStream_t stream) {
     if (sp.R > kSortMost) return launch_chained(sort_far_kernel, kSortCtas, kSortThreads, 0, stream, chained, kSortCtas, sp);
-    return sp.R <= kSortThreads ? sort_runs<1>(sp, chained, stream)
-           : sp.R <= 8 * kSortThreads ? sort_runs<2>(sp, chained, stream)
-                                      : sort_runs<4>(sp, chained, stream);
+    if (sp.R > kCountRows) return sort_runs<kRunItems>(sp, chained, stream);
+    constexpr int per = kCountThreads / kCountShare;
+    return launch_chained(count_tokens_kernel, (unsigned)((sp.R + per - 1) / per), kCountThreads, 0, stream, chained, 1u, sp);
 }
 
-template <typename TG, typename TT, bool kAdd>
+template <typename TG, typename TT, bool kAdd, bool kWide>
 cudaError_t sums(const SumParams &p, const SortParams &sp, cudaStream_t stream) {
     if (p.a.R <= kFewRows) {
-        return launch_chained(few_rows_kernel<TG, TT, kAdd>, (unsigned)((p.a.d + kFewCols - 1) / kFewCols), kSortThreads, 0,
+        return launch_chained(few_rows_kernel<TG, TT, kAdd, kWide>, (unsigned)((p.a.d + kFewCols - 1) / kFewCols), kSortThreads, 0,
                               stream, !kAdd, 1u, p, sp);
     }
     cudaError_t e = sort_tokens(sp, !kAdd, stream);
     if (e != cudaSuccess) return e;
-    const unsigned ctas = (unsigned)((p.units + p.cta_units - 1) / p.cta_units);
+    const unsigned ctas = (unsigned)((p.units + p.cta_units - 1) / p.cta_units * p.slab_ctas);
     const size_t smem = (size_t)(2 * p.cta_units * p.unit + 3 * p.unit + 2) * sizeof(int32_t);
-    e = launch_chained(sum_rows_kernel<TG, TT, kAdd>, ctas, 32u * p.unit_warps * p.cta_units, smem, stream, true, 1u, p);
+    e = launch_chained(sum_rows_kernel<TG, TT, kAdd, kWide>, ctas, 32u * p.unit_warps * p.cta_units, smem, stream, true, 1u, p);
     if (e != cudaSuccess) return e;
-    return launch_chained(join_parts_kernel<TT, kAdd>, (unsigned)std::max(1, device_sm_count() * 4), 32u * kJoinWarps, 0,
+    return launch_chained(join_parts_kernel<TT, kAdd, kWide>, (unsigned)std::max(1, device_sm_count() * 4), 32u * kJoinWarps, 0,
                           stream, true, 1u, p);
 }
 
 }  // namespace
 
 cudaError_t launch_token_embed(const EmbedRows &a, cudaStream_t stream) {
-    GatherParams p{a, 32, wide_rows(a.table), wide_rows(a.rows)};
+    GatherParams p{a, 32};
     const int64_t sms = std::max(1, device_sm_count()), eights = (a.d + 7) / 8;
     // a warp per row where the rows alone fill the chip, more threads per row where they do not
     while (p.lanes < kGatherThreads && a.R * p.lanes < sms * 2048 && p.lanes < eights) p.lanes *= 2;
@@ -760,13 +824,12 @@ size_t token_embed_backward_bytes(int64_t R, int64_t rows, int64_t d) {
 
 cudaError_t launch_token_embed_backward(const EmbedRows &a, void *workspace, cudaStream_t stream) {
     const int64_t rows = a.vocab_end - a.vocab_start;
-    const bool wide_table = wide_rows(a.table);
     if (!a.accumulate && rows > 0) {
         const unsigned grid = (unsigned)std::min<int64_t>((rows + 7) / 8, (int64_t)std::max(1, device_sm_count()) * 32);
-        if (a.table.dtype == DG_F32)
-            clear_rows_kernel<float><<<grid, 256, 0, stream>>>(a, rows, wide_table);
-        else
-            clear_rows_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, rows, wide_table);
+        const bool f32 = a.table.dtype == DG_F32, wide = wide_rows(a.table);
+        (f32 ? wide ? clear_rows_kernel<float, true> : clear_rows_kernel<float, false>
+         : wide ? clear_rows_kernel<__nv_bfloat16, true>
+                : clear_rows_kernel<__nv_bfloat16, false>)<<<grid, 256, 0, stream>>>(a, rows);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
@@ -791,19 +854,21 @@ cudaError_t launch_token_embed_backward(const EmbedRows &a, void *workspace, cud
     p.unit = unit_of(a.R, a.d);
     p.units = (int)((a.R + p.unit - 1) / p.unit);
     p.slabs = (int)((a.d + 255) / 256);
-    p.unit_warps = std::min(p.slabs, kMaxSumWarps);
-    p.cta_units = std::max(1, 4 / p.unit_warps);
-    p.wide_grad = wide_rows(a.rows);
-    p.wide_table = wide_table;
-    auto typed = [&](auto add) {
-        constexpr bool kAdd = decltype(add)::value;
+    p.unit_warps = std::min(p.slabs, kSumWarps);
+    p.cta_units = kSumWarps / p.unit_warps;
+    p.slab_ctas = (p.slabs + p.unit_warps - 1) / p.unit_warps;
+    auto typed = [&](auto add, auto wide) {
+        constexpr bool kAdd = decltype(add)::value, kWide = decltype(wide)::value;
         if (a.rows.dtype == DG_F32)
-            return a.table.dtype == DG_F32 ? sums<float, float, kAdd>(p, sp, stream)
-                                           : sums<float, __nv_bfloat16, kAdd>(p, sp, stream);
-        return a.table.dtype == DG_F32 ? sums<__nv_bfloat16, float, kAdd>(p, sp, stream)
-                                       : sums<__nv_bfloat16, __nv_bfloat16, kAdd>(p, sp, stream);
+            return a.table.dtype == DG_F32 ? sums<float, float, kAdd, kWide>(p, sp, stream)
+                                           : sums<float, __nv_bfloat16, kAdd, kWide>(p, sp, stream);
+        return a.table.dtype == DG_F32 ? sums<__nv_bfloat16, float, kAdd, kWide>(p, sp, stream)
+                                       : sums<__nv_bfloat16, __nv_bfloat16, kAdd, kWide>(p, sp, stream);
     };
-    return a.accumulate ? typed(std::true_type()) : typed(std::false_type());
+    const std::true_type yes;
+    const std::false_type no;
+    return wide_rows(a.rows) && wide_rows(a.table) ? (a.accumulate ? typed(yes, yes) : typed(no, yes))
+                                                   : (a.accumulate ? typed(yes, no) : typed(no, no));
 }
 
 }  // namespace dg
