@@ -21,8 +21,9 @@ namespace {
 
 using namespace hidden;
 
-// Threads of a row's CTA, by the eights of columns that each takes (row_shape).
+// Threads of a row's CTA at most, by the eights of columns that each takes: forward and backward.
 constexpr int max_threads(int n) { return n == 1 ? 256 : n == 2 ? 512 : 1024; }
+constexpr int max_back_threads(int n) { return n == 4 ? 1024 : 512; }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -163,75 +164,90 @@ struct NormBackParams {
     int64_t part_ld;
 };
 
-template <typename TG, typename TH, typename TD, int N, bool kWide>
-__global__ void __launch_bounds__(max_threads(N)) rms_norm_backward_kernel(const NormBackParams p) {
+// A row as it lies in memory, this thread's columns of it.
+template <typename TG, typename TH, typename TD, int N>
+struct BackRow {
+    Raw8<TG> g[N];
+    Raw8<TH> h[N];
+    Raw8<TD> up[N];
+    float rstd;
+};
+
+// Loads in flight side by side: a thread past the row's end reads its last eight columns again, in place of a branch.
+template <bool kUp, bool kWide, typename TG, typename TH, typename TD, int N>
+__device__ __forceinline__ void load_row(BackRow<TG, TH, TD, N> &row, const NormBackRows &a, int64_t r, const int (&col)[N]) {
+    const TG *g = static_cast<const TG *>(a.grad.p) + r * a.grad.ld;
+    const TH *h = static_cast<const TH *>(a.hidden.p) + r * a.hidden.ld;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        load8<kWide>(row.g[i], g + col[i], (int)a.d - col[i]);
+        load8<kWide>(row.h[i], h + col[i], (int)a.d - col[i]);
+    }
+    if constexpr (kUp) {
+        const TD *up = static_cast<const TD *>(a.grad_hidden.p) + r * a.grad_hidden.ld;
+#pragma unroll
+        for (int i = 0; i < N; ++i) load8<kWide>(row.up[i], up + col[i], (int)a.d - col[i]);
+    }
+    row.rstd = a.rstd[r];
+}
+
+// kUp: with grad_hidden.  The next row is loaded while this one is reduced and stored.
+template <typename TG, typename TH, typename TD, int N, bool kUp, bool kWide>
+__global__ void __launch_bounds__(max_back_threads(N)) rms_norm_backward_kernel(const NormBackParams p) {
     __shared__ float sums[2][32];
     const NormBackRows &a = p.a;
-    const int d = (int)a.d;
-    float dw[N][8];
+    const int d = (int)a.d, last = (d - 1) / 8 * 8;
+    int col[N];
+    float w[N][8], dw[N][8];
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int i = 0; i < N; ++i) {
+        const int c = 8 * (threadIdx.x + i * blockDim.x);
+        col[i] = min(c, last);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+        for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f, w[i][j] = 1.0f;
+        if (a.weight) {
+            load8_any<kWide>(w[i], a.weight, a.weight_dtype, col[i], d - col[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[i][j] += a.weight_offset;
+        }
+        mask8(w[i], d - c);  // (all zeros past the row's end)
+    }
+    const float inv_d = 1.0f / (float)d;
+    BackRow<TG, TH, TD, N> row;
+    if (blockIdx.x < a.R) load_row<kUp, kWide>(row, a, blockIdx.x, col);
     int turn = 0;
     for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x, turn ^= 1) {
-        Raw8<TG> rg[N];
-        Raw8<TH> rh[N];
-        Raw8<TD> rd[N];
-        const TG *gp = static_cast<const TG *>(a.grad.p) + r * a.grad.ld;
-        const TH *hp = static_cast<const TH *>(a.hidden.p) + r * a.hidden.ld;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int c = 8 * (threadIdx.x + i * blockDim.x);
-            if (c < d) {
-                load8<kWide>(rg[i], gp + c, d - c);
-                load8<kWide>(rh[i], hp + c, d - c);
-            }
-        }
-        if (a.grad_hidden.p) {
-            const TD *dp = static_cast<const TD *>(a.grad_hidden.p) + r * a.grad_hidden.ld;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int c = 8 * (threadIdx.x + i * blockDim.x);
-                if (c < d) load8<kWide>(rd[i], dp + c, d - c);
-            }
-        }
-        const float rstd = a.rstd[r];
-        float g[N][8], xh[N][8];
+        float g[N][8], xh[N][8], up[kUp ? N : 1][8];
+        const float rstd = row.rstd;
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int c = 8 * (threadIdx.x + i * blockDim.x);
-            if (c < d) {
-                float w[8], q = 0.0f;
-                unpack8(g[i], rg[i]);
-                unpack8(xh[i], rh[i]);
-                mask8(g[i], d - c);
-                mask8(xh[i], d - c);
-                if (a.weight) load8_any<kWide>(w, a.weight, a.weight_dtype, c, d - c);
+            float q = 0.0f;
+            unpack8(g[i], row.g[i]);
+            unpack8(xh[i], row.h[i]);
+            if constexpr (kUp) unpack8(up[i], row.up[i]);
+            mask8(g[i], d - 8 * (int)(threadIdx.x + i * blockDim.x));  // (nothing past the row's end counts)
+            mask8(xh[i], d - 8 * (int)(threadIdx.x + i * blockDim.x));
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    xh[i][j] *= rstd;
-                    dw[i][j] = fmaf(g[i][j], xh[i][j], dw[i][j]);
-                    if (a.weight) g[i][j] *= a.weight_offset + w[j];
-                    q = fmaf(g[i][j], xh[i][j], q);
-                }
-                s += q;
+            for (int j = 0; j < 8; ++j) {
+                xh[i][j] *= rstd;
+                dw[i][j] = fmaf(g[i][j], xh[i][j], dw[i][j]);
+                g[i][j] *= w[i][j];
+                q = fmaf(g[i][j], xh[i][j], q);
             }
+            s += q;
         }
-        const float mean = cta_sum(s, sums[turn]) / (float)d;
+        if (r + gridDim.x < a.R) load_row<kUp, kWide>(row, a, r + gridDim.x, col);
+        const float mean = cta_sum(s, sums[turn]) * inv_d;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int c = 8 * (threadIdx.x + i * blockDim.x);
-            if (c < d) {
-                float t[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) t[j] = 0.0f;
-                if (a.grad_hidden.p) unpack8(t, rd[i]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) g[i][j] = fmaf(rstd, fmaf(-mean, xh[i][j], g[i][j]), t[j]);
-                store8<kWide>(static_cast<TH *>(a.grad_x.p) + r * a.grad_x.ld + c, g[i], d - c);
+            for (int j = 0; j < 8; ++j) {
+                g[i][j] = rstd * fmaf(-mean, xh[i][j], g[i][j]);
+                if constexpr (kUp) g[i][j] += up[i][j];
             }
+            if (c < d) store8<kWide>(static_cast<TH *>(a.grad_x.p) + r * a.grad_x.ld + c, g[i], d - c);
         }
     }
     if (a.grad_weight)
@@ -266,111 +282,113 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float *__restri
 
 bool wide_vector(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Threads of a row's CTA and eights of columns per thread; wide: all rows start where the widest accesses may.
-struct Shape {
-    int threads, n;
-    bool wide;
-};
-Shape row_shape(int64_t d, bool wide) {
+// Eights of columns per thread, the fewest with which a row fits a CTA; off the boundaries (not wide) one kernel is
+// enough for all rows but the widest.
+template <typename Max>
+int eights_per_thread(int64_t d, bool wide, int narrow, Max most) {
     const int64_t eights = (d + 7) / 8;
-    const int n = !wide ? 4 : eights <= 256 ? 1 : eights <= 1024 ? 2 : 4;
-    return {(int)(((eights + n - 1) / n + 31) / 32 * 32), n, wide};
+    for (const int n : {1, 2})
+        if (eights <= n * most(n) && (wide || n == narrow)) return n;
+    return 4;
 }
+int row_threads(int64_t d, int n) { return (int)((((d + 7) / 8 + n - 1) / n + 31) / 32 * 32); }
 
 template <typename TX, typename TR, typename TO>
-void norm_width(const NormParams &p, const Shape &s, cudaStream_t stream) {
+void norm_width(const NormParams &p, bool wide, cudaStream_t stream) {
     const unsigned grid = (unsigned)p.a.R;
-    if (!s.wide)
-        rms_norm_kernel<TX, TR, TO, 4, false><<<grid, s.threads, 0, stream>>>(p);
-    else if (s.n == 1)
-        rms_norm_kernel<TX, TR, TO, 1, true><<<grid, s.threads, 0, stream>>>(p);
-    else if (s.n == 2)
-        rms_norm_kernel<TX, TR, TO, 2, true><<<grid, s.threads, 0, stream>>>(p);
-    else
-        rms_norm_kernel<TX, TR, TO, 4, true><<<grid, s.threads, 0, stream>>>(p);
+    const int n = eights_per_thread(p.a.d, wide, 2, max_threads), threads = row_threads(p.a.d, n);
+    (wide ? n == 1   ? rms_norm_kernel<TX, TR, TO, 1, true>
+            : n == 2 ? rms_norm_kernel<TX, TR, TO, 2, true>
+                     : rms_norm_kernel<TX, TR, TO, 4, true>
+     : n == 2 ? rms_norm_kernel<TX, TR, TO, 2, false>
+              : rms_norm_kernel<TX, TR, TO, 4, false>)<<<grid, threads, 0, stream>>>(p);
 }
 template <typename TX, typename TR>
-void norm_out(const NormParams &p, const Shape &s, cudaStream_t stream) {
+void norm_out(const NormParams &p, bool wide, cudaStream_t stream) {
     if (p.a.out.dtype == DG_F32)
-        norm_width<TX, TR, float>(p, s, stream);
+        norm_width<TX, TR, float>(p, wide, stream);
     else if (p.a.out.dtype == DG_BF16)
-        norm_width<TX, TR, __nv_bfloat16>(p, s, stream);
+        norm_width<TX, TR, __nv_bfloat16>(p, wide, stream);
     else
-        norm_width<TX, TR, E4m3>(p, s, stream);
+        norm_width<TX, TR, E4m3>(p, wide, stream);
 }
 template <typename TX>
-void norm_residual(const NormParams &p, const Shape &s, cudaStream_t stream) {
+void norm_residual(const NormParams &p, bool wide, cudaStream_t stream) {
     if (p.a.residual.p && p.a.residual.dtype == DG_F32)
-        norm_out<TX, float>(p, s, stream);
+        norm_out<TX, float>(p, wide, stream);
     else
-        norm_out<TX, __nv_bfloat16>(p, s, stream);
-}
-
-template <typename TG, typename TH, typename TD>
-void back_width(const NormBackParams &p, const Shape &s, unsigned grid, cudaStream_t stream) {
-    if (!s.wide)
-        rms_norm_backward_kernel<TG, TH, TD, 4, false><<<grid, s.threads, 0, stream>>>(p);
-    else if (s.n == 1)
-        rms_norm_backward_kernel<TG, TH, TD, 1, true><<<grid, s.threads, 0, stream>>>(p);
-    else if (s.n == 2)
-        rms_norm_backward_kernel<TG, TH, TD, 2, true><<<grid, s.threads, 0, stream>>>(p);
-    else
-        rms_norm_backward_kernel<TG, TH, TD, 4, true><<<grid, s.threads, 0, stream>>>(p);
-}
-template <typename TG, typename TH>
-void back_residual(const NormBackParams &p, const Shape &s, unsigned grid, cudaStream_t stream) {
-    if (p.a.grad_hidden.p && p.a.grad_hidden.dtype == DG_F32)
-        back_width<TG, TH, float>(p, s, grid, stream);
-    else
-        back_width<TG, TH, __nv_bfloat16>(p, s, grid, stream);
+        norm_out<TX, __nv_bfloat16>(p, wide, stream);
 }
 
 int64_t part_stride(int64_t d) { return (d + 7) / 8 * 8; }
 
-// CTAs of the backward pass: as many rows in work as the SMs' threads allow.
-int64_t back_grid(int64_t R, const Shape &s) {
-    return std::min<int64_t>(R, (int64_t)std::max(1, device_sm_count()) * std::max(1, std::min(16, 1024 / s.threads)));
+// CTAs of the backward pass at most: as many as the SMs could hold.
+int64_t back_grid_most(int64_t R, int64_t d) {
+    return std::min<int64_t>(R, (int64_t)std::max(1, device_sm_count()) * std::min(32, 2048 / row_threads(d, 4)));
+}
+
+// One wave of CTAs, each of which keeps its columns' sums over all its rows; *grid: how many.
+template <typename TG, typename TH, typename TD, int N, bool kUp, bool kWide>
+cudaError_t launch_back(const NormBackParams &p, unsigned *grid, cudaStream_t stream) {
+    const auto kernel = rms_norm_backward_kernel<TG, TH, TD, N, kUp, kWide>;
+    const int threads = row_threads(p.a.d, N);
+    int per_sm = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
+    if (e != cudaSuccess) return e;
+    *grid = (unsigned)std::min(back_grid_most(p.a.R, p.a.d), (int64_t)std::max(1, device_sm_count()) * std::max(1, per_sm));
+    kernel<<<*grid, threads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+template <typename TG, typename TH, typename TD, bool kUp>
+cudaError_t back_width(const NormBackParams &p, bool wide, unsigned *grid, cudaStream_t stream) {
+    const int n = eights_per_thread(p.a.d, wide, 1, max_back_threads);
+    if (wide)
+        return n == 1   ? launch_back<TG, TH, TD, 1, kUp, true>(p, grid, stream)
+               : n == 2 ? launch_back<TG, TH, TD, 2, kUp, true>(p, grid, stream)
+                        : launch_back<TG, TH, TD, 4, kUp, true>(p, grid, stream);
+    return n == 1 ? launch_back<TG, TH, TD, 1, kUp, false>(p, grid, stream)
+                  : launch_back<TG, TH, TD, 4, kUp, false>(p, grid, stream);
+}
+template <typename TG, typename TH>
+cudaError_t back_residual(const NormBackParams &p, bool wide, unsigned *grid, cudaStream_t stream) {
+    if (!p.a.grad_hidden.p) return back_width<TG, TH, float, false>(p, wide, grid, stream);
+    return p.a.grad_hidden.dtype == DG_F32 ? back_width<TG, TH, float, true>(p, wide, grid, stream)
+                                           : back_width<TG, TH, __nv_bfloat16, true>(p, wide, grid, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rms_norm(const NormRows &a, cudaStream_t stream) {
     const NormParams p{a};
-    const Shape s = row_shape(a.d, wide_rows(a.x) && wide_rows(a.residual) && wide_rows(a.hidden) && wide_rows(a.out) &&
-                                       wide_vector(a.weight));
+    const bool wide = wide_rows(a.x) && wide_rows(a.residual) && wide_rows(a.hidden) && wide_rows(a.out) &&
+                      wide_vector(a.weight);
     if (a.x.dtype == DG_F32)
-        norm_residual<float>(p, s, stream);
+        norm_residual<float>(p, wide, stream);
     else
-        norm_residual<__nv_bfloat16>(p, s, stream);
+        norm_residual<__nv_bfloat16>(p, wide, stream);
     return cudaGetLastError();
 }
 
 size_t rms_norm_backward_bytes(int64_t R, int64_t d) {
-    const int64_t most = std::max(back_grid(R, row_shape(d, true)), back_grid(R, row_shape(d, false)));
-    return (size_t)most * (size_t)part_stride(d) * sizeof(float);
+    return (size_t)back_grid_most(R, d) * (size_t)part_stride(d) * sizeof(float);
 }
 
 cudaError_t launch_rms_norm_backward(const NormBackRows &a, void *workspace, cudaStream_t stream) {
     const NormBackParams p{a, static_cast<float *>(workspace), part_stride(a.d)};
-    const Shape s = row_shape(a.d, wide_rows(a.grad) && wide_rows(a.hidden) && wide_rows(a.grad_hidden) &&
-                                       wide_rows(a.grad_x) && wide_vector(a.weight));
-    const unsigned grid = (unsigned)back_grid(a.R, s);
-    const bool g32 = a.grad.dtype == DG_F32, h32 = a.hidden.dtype == DG_F32;
+    const bool wide = wide_rows(a.grad) && wide_rows(a.hidden) && wide_rows(a.grad_hidden) && wide_rows(a.grad_x) &&
+                      wide_vector(a.weight);
+    unsigned grid = 0;
     if (a.R > 0) {
-        if (g32 && h32)
-            back_residual<float, float>(p, s, grid, stream);
-        else if (g32)
-            back_residual<float, __nv_bfloat16>(p, s, grid, stream);
-        else if (h32)
-            back_residual<__nv_bfloat16, float>(p, s, grid, stream);
-        else
-            back_residual<__nv_bfloat16, __nv_bfloat16>(p, s, grid, stream);
-        const cudaError_t e = cudaGetLastError();
+        const bool g32 = a.grad.dtype == DG_F32, h32 = a.hidden.dtype == DG_F32;
+        const cudaError_t e = g32 ? h32 ? back_residual<float, float>(p, wide, &grid, stream)
+                                        : back_residual<float, __nv_bfloat16>(p, wide, &grid, stream)
+                              : h32 ? back_residual<__nv_bfloat16, float>(p, wide, &grid, stream)
+                                    : back_residual<__nv_bfloat16, __nv_bfloat16>(p, wide, &grid, stream);
         if (e != cudaSuccess) return e;
     }
     if (a.grad_weight)
-        norm_weight_kernel<<<(unsigned)((a.d + 31) / 32), 1024, 0, stream>>>(p.parts, p.part_ld, a.R > 0 ? (int)grid : 0,
-                                                                            a.d, a.grad_weight, a.weight_dtype);
+        norm_weight_kernel<<<(unsigned)((a.d + 31) / 32), 1024, 0, stream>>>(p.parts, p.part_ld, (int)grid, a.d,
+                                                                            a.grad_weight, a.weight_dtype);
     return cudaGetLastError();
 }
 
