@@ -164,22 +164,48 @@ __device__ __forceinline__ void store8(E4m3 *q, const float (&v)[8], int n) {
         if (j < n) q[j].code = (uint8_t)(u[j >> 2] >> (8 * (j & 3)));
 }
 
-// Entries whose type is known at run time only (vectors read again and again, from the caches).
-template <bool kWide>
-__device__ __forceinline__ void load8_any(float (&v)[8], const void *p, int dtype, int64_t at, int n) {
-    if (dtype == DG_F32) {
-        Raw8<float> r;
-        load8<kWide>(r, static_cast<const float *>(p) + at, n);
-        unpack8(v, r);
+// Eight entries of a type known at run time only, fp32 or not (bf16).
+struct Any8 {
+    uint4 a, b;
+};
+__device__ __forceinline__ void load8(Any8 &r, const void *p, bool f32, int64_t at, int n) {
+    if (f32) {
+        Raw8<float> t;
+        load8<false>(t, static_cast<const float *>(p) + at, n);
+        r.a = *reinterpret_cast<const uint4 *>(&t.a);
+        r.b = *reinterpret_cast<const uint4 *>(&t.b);
     } else {
-        Raw8<__nv_bfloat16> r;
-        load8<kWide>(r, static_cast<const __nv_bfloat16 *>(p) + at, n);
-        unpack8(v, r);
+        Raw8<__nv_bfloat16> t;
+        load8<false>(t, static_cast<const __nv_bfloat16 *>(p) + at, n);
+        r.a = t.a;
+    }
+}
+// The same from shared memory, 16-byte aligned.
+__device__ __forceinline__ void read8(float (&v)[8], const uint8_t *row, bool f32, int at) {
+    if (f32) {
+        const float4 a = *reinterpret_cast<const float4 *>(row + 4 * at), b = *reinterpret_cast<const float4 *>(row + 4 * at + 16);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+        const uint4 a = *reinterpret_cast<const uint4 *>(row + 2 * at);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[2 * j] = bf16_low(w[j]), v[2 * j + 1] = bf16_high(w[j]);
+    }
+}
+__device__ __forceinline__ void unpack8(float (&v)[8], const Any8 &r, bool f32) {
+    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+    if (f32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[2 * j] = bf16_low(w[j]), v[2 * j + 1] = bf16_high(w[j]);
     }
 }
 template <bool kWide>
-__device__ __forceinline__ void store8_any(void *p, int dtype, int64_t at, const float (&v)[8], int n) {
-    if (dtype == DG_F32)
+__device__ __forceinline__ void store8(void *p, bool f32, int64_t at, const float (&v)[8], int n) {
+    if (f32)
         store8<kWide>(static_cast<float *>(p) + at, v, n);
     else
         store8<kWide>(static_cast<__nv_bfloat16 *>(p) + at, v, n);

@@ -4,26 +4,42 @@
 //   dh = grad_hidden + rstd (g - xh mean(g xh)),  g = dy (offset + weight),  xh = h rstd
 //   dweight = sum over the rows of dy xh
 //
-// Both are bound by HBM: a CTA keeps a row in registers from its load to its last store, so that every
-// matrix is moved once.  Forward, the norm is taken of the fp32 sum h, not of the h that is stored (which
-// is rounded once).  An 8-bit output takes the row's largest |y| before the first code is written:
-// scale = amax / 448 and codes = e4m3(y / scale), as the table's rows are quantised.  Backward, a thread
-// keeps its columns' part of dweight in fp32 registers over all rows of its CTA; a second kernel adds the
-// CTAs' parts in a fixed order.
+// Both are bound by HBM.  A CTA takes every gridDim.x-th row and keeps it in registers from its arrival to its last
+// store, so that every matrix is moved once; the rows to come arrive meanwhile in a ring of shared memory by bulk
+// copies that a warp of their own sends for (with the next row in registers an SM held too few rows to keep the memory
+// busy; sent for by a warp that also computes, the copies held every row up).  What is left per row and thread is some
+// 150 instructions: types are known at compile time, and arithmetic is in pairs.  Forward, the norm is taken of the
+// fp32 sum h, not of the h that is stored (which is rounded once).  An 8-bit output takes the row's largest |y| before
+// the first code is written: scale = amax / 448 and codes = e4m3(y / scale), as the table's rows are quantised.
+// Backward, a thread keeps its columns' part of dweight in fp32 registers over all rows of its CTA; a second kernel adds
+// the CTAs' parts in a fixed order.  Rows that start off 16-byte boundaries, and rows that do not fit, are read where
+// they lie.
 #include <algorithm>
+#include <atomic>
 
 #include "dg_internal.h"
 #include "hidden.cuh"
+#include "vocab_row.cuh"
 
 namespace dg {
 
 namespace {
 
 using namespace hidden;
+using vocab::add2;
+using vocab::f32x2;
+using vocab::fma2;
+using vocab::mul2;
+using vocab::pair;
+using vocab::unpair;
 
-// Threads of a row's CTA at most, by the eights of columns that each takes: forward and backward.
-constexpr int max_threads(int n) { return n == 1 ? 256 : n == 2 ? 512 : 1024; }
-constexpr int max_back_threads(int n) { return n == 4 ? 1024 : 512; }
+constexpr int kMaxStages = 16;
+constexpr int kRingHeader = 16 * kMaxStages;  // the ring's barriers, and room past its end: a thread reads eight
+constexpr int kRingTail = 32;                 // columns where fewer are left
+constexpr int kSmemPerSm = 224 * 1024, kSmemLimit = 232448 - 1024;  // of an SM's CTAs, and of one
+
+// Threads that work on a row at most, by the eights of columns that each takes.
+__host__ __device__ constexpr int max_threads(int n) { return n == 8 ? 512 : 256; }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -31,231 +47,496 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Sum over the CTA, the same in every thread; `parts` is free again after the next barrier but one.
-__device__ __forceinline__ float cta_sum(float v, float *parts) {
+// A barrier of the row's threads.
+__device__ __forceinline__ void row_sync(int threads) { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); }
+
+// Sum over the row's threads, the same in all; `parts` is free again after the next barrier but one.
+__device__ __forceinline__ float row_sum(float v, float *parts, int threads) {
     v = warp_sum(v);
-    const int warps = blockDim.x >> 5;
-    if (warps == 1) return v;
-    if ((threadIdx.x & 31) == 0) parts[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.0f;
-    for (int w = 0; w < warps; ++w) v += parts[w];
-    return v;
+    if (threads == 32) return v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) parts[threadIdx.x >> 5] = v;
+    row_sync(threads);
+    return warp_sum(lane < threads >> 5 ? parts[lane] : 0.0f);
 }
 
-// The largest magnitude's bits over the CTA: as whole numbers NaN is above infinity.
-__device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t *parts) {
+// The largest magnitude's bits: as whole numbers NaN is above infinity.
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t *parts, int threads) {
     v = __reduce_max_sync(0xffffffffu, v);
-    const int warps = blockDim.x >> 5;
-    if (warps == 1) return v;
-    if ((threadIdx.x & 31) == 0) parts[threadIdx.x >> 5] = v;
-    __syncthreads();
-    for (int w = 0; w < warps; ++w) v = max(v, parts[w]);
-    return v;
+    if (threads == 32) return v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) parts[threadIdx.x >> 5] = v;
+    row_sync(threads);
+    return __reduce_max_sync(0xffffffffu, lane < threads >> 5 ? parts[lane] : 0u);
 }
+
+// 1 / sqrt(x) within some 2^-23: the hardware's, and a Newton step where x is positive and finite.  (The exact root
+// and quotient were a tenth of the forward kernel's instructions.)
+__device__ __forceinline__ float inv_sqrt(float x) {
+    const float r = rsqrtf(x);
+    return x > 0.0f && x < INFINITY ? fmaf(0.5f * r, fmaf(-x * r, r, 1.0f), r) : r;
+}
+
+// Rows of up to three matrices on their way through shared memory.
+struct Source {
+    Rows m[3];
+    int bytes[3];  // of a row, in whole 16-byte groups; 0: no such matrix
+    int stages, stage_bytes;
+};
+
+// The CTA's k-th row, blockIdx.x + k gridDim.x, is in slot k % stages: `full` once it has arrived, `empty` once every
+// warp of the row's threads has read it.
+struct Ring {
+    uint8_t *slots;
+    uint64_t *full, *empty;
+    volatile int *gave_up;
+    int stages, stage_bytes;
+    int slot = 0;
+    uint32_t phase = 0;
+
+    __device__ __forceinline__ Ring(const Source &src, uint4 *smem, volatile int *flag, int threads)
+        : slots(reinterpret_cast<uint8_t *>(smem) + kRingHeader), full(reinterpret_cast<uint64_t *>(smem)),
+          empty(full + kMaxStages), gave_up(flag), stages(src.stages), stage_bytes(src.stage_bytes) {
+        if (threadIdx.x == 0) {
+            *gave_up = 0;
+            for (int s = 0; s < stages; ++s) {
+                mbar_init(smem_u32(&full[s]), 1);
+                mbar_init(smem_u32(&empty[s]), threads >> 5);
+            }
+            fence_mbar_init();
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ void next() {
+        if (++slot == stages) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+    // One thread sends for all of the CTA's rows.
+    __device__ __forceinline__ void send(const Source &src, int64_t R) {
+        bool again = false;  // the slot has been used before
+        for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
+            if (again && !mbar_wait(smem_u32(&empty[slot]), phase ^ 1, gave_up)) return;
+            const uint32_t bar = smem_u32(&full[slot]);
+            uint32_t at = smem_u32(slots) + (uint32_t)slot * stage_bytes;
+            mbar_arrive_expect_tx(bar, (uint32_t)stage_bytes);
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+                if (src.bytes[q] == 0) continue;
+                const char *row = static_cast<const char *>(src.m[q].p) + r * src.m[q].ld * (src.m[q].dtype == DG_F32 ? 4 : 2);
+                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(at),
+                             "l"(row), "r"(src.bytes[q]), "r"(bar)
+                             : "memory");
+                at += src.bytes[q];
+            }
+            next();
+            if (slot == 0) again = true;
+        }
+    }
+    // The row's slot, once it has arrived.  (A wait that gave up has recorded it, and the row is computed of what is there.)
+    __device__ __forceinline__ const uint8_t *wait() {
+        mbar_wait(smem_u32(&full[slot]), phase, gave_up);
+        return slots + slot * stage_bytes;
+    }
+    // This warp has read the slot for the last time.
+    __device__ __forceinline__ void release() {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&empty[slot]));
+    }
+    // Copies in flight after a wait gave up land before the CTA leaves.
+    __device__ __forceinline__ void leave() {
+        __syncthreads();
+        if (*gave_up) {
+            const unsigned long long t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+        }
+    }
+};
+
+// This thread's columns: from 8 (threadIdx.x + i threads) on.  Past the row's end it reads the row's last ones, counts
+// zeros and writes nothing.
+template <int N>
+struct Columns {
+    int at[N], read[N], n[N];
+    __device__ __forceinline__ Columns(int width, int threads) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            at[i] = 8 * (threadIdx.x + i * threads);
+            read[i] = min(at[i], (width - 1) / 8 * 8);
+            n[i] = width - at[i];
+        }
+    }
+};
+
+// Eight columns as pairs, those from n on as zeros.
+__device__ __forceinline__ void mask4(f32x2 (&v)[4], int n) {
+    if (n < 8)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float a, b;
+            unpair(v[j], a, b);
+            v[j] = pair(2 * j < n ? a : 0.0f, 2 * j + 1 < n ? b : 0.0f);
+        }
+}
+template <bool kF32>
+__device__ __forceinline__ void read4(f32x2 (&v)[4], const uint8_t *row, int at, int n) {
+    if constexpr (kF32) {
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(row + 4 * at);
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(row + 4 * at + 16);
+        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+    } else {
+        const uint4 a = *reinterpret_cast<const uint4 *>(row + 2 * at);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = pair(bf16_low(w[j]), bf16_high(w[j]));
+    }
+    mask4(v, n);
+}
+__device__ __forceinline__ void singles(float (&v)[8], const f32x2 (&p)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) unpair(p[j], v[2 * j], v[2 * j + 1]);
+}
+
+// offset + weight in these columns (ones without a weight), zeros past the row's end.
+__device__ __forceinline__ void load_weight(float (&w)[8], const void *weight, int dtype, float offset, int at, int n, int width) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = 1.0f;
+    if (weight) {
+        Any8 raw;
+        load8(raw, weight, dtype == DG_F32, at, width - at);
+        unpack8(w, raw, dtype == DG_F32);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] += offset;
+    }
+    mask8(w, n);
+}
+template <int N>
+__device__ __forceinline__ void load_weight(f32x2 (&w)[N][4], const void *weight, int dtype, float offset,
+                                            const Columns<N> &col, int width) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float v[8];
+        load_weight(v, weight, dtype, offset, col.read[i], col.n[i], width);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[i][j] = pair(v[2 * j], v[2 * j + 1]);
+    }
+}
+
+// A matrix of a row: none, bf16, or fp32.
+enum { kNone = 0, kBf16 = 1, kF32 = 2 };
+int kind_of(const Rows &m) { return !m.p ? kNone : m.dtype == DG_F32 ? kF32 : kBf16; }
+
+// ---------------------------------------------------------------- forward
 
 struct NormParams {
     NormRows a;
+    Source src;  // x, residual
 };
 
-template <typename TX, typename TR, typename TO, int N, bool kWide>
-__global__ void __launch_bounds__(max_threads(N)) rms_norm_kernel(const NormParams p) {
-    constexpr bool kCodes = sizeof(TO) == 1;
-    __shared__ float sums[32];
-    __shared__ uint32_t maxima[32];
+// y in place of h rstd w, as codes: y times the scale's reciprocal, within a rounding of the quotient; a scale whose
+// reciprocal may overflow divides.
+__device__ __forceinline__ void to_codes(float (&v)[8], float scale) {
+    if (scale < 1e-37f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = scale != 0.0f ? __fdiv_rn(v[j], scale) : 0.0f;
+    } else {
+        const float inv = 1.0f / scale;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= inv;
+    }
+}
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// kX, kRes: what x and the residual are; hidden has the residual's type (none: no hidden).
+template <int N, int kX, int kRes, bool kCodes>
+__global__ void __launch_bounds__(max_threads(N) + 32) rms_norm_kernel(const NormParams p) {
+    extern __shared__ uint4 smem[];
+    __shared__ float sums[2][32];
+    __shared__ uint32_t maxima[2][32];
+    __shared__ int gave_up;
     const NormRows &a = p.a;
-    const int64_t r = blockIdx.x;
-    const int d = (int)a.d;
-    const TX *x = static_cast<const TX *>(a.x.p) + r * a.x.ld;
-    const TR *res = static_cast<const TR *>(a.residual.p) + (a.residual.p ? r * a.residual.ld : 0);
-    float v[N][8];
-    {
-        Raw8<TX> rx[N];
-        Raw8<TR> rr[N];
+    const int d = (int)a.d, threads = blockDim.x - 32;
+    Ring ring(p.src, smem, &gave_up, threads);
+    if ((int)threadIdx.x >= threads) {
+        if ((int)threadIdx.x == threads) ring.send(p.src, a.R);
+        ring.leave();
+        return;
+    }
+    const Columns<N> col(d, threads);
+    const float inv_d = 1.0f / (float)d;
+    const bool out32 = a.out.dtype == DG_F32;
+    f32x2 w[N][4];
+    load_weight(w, a.weight, a.weight_dtype, a.weight_offset, col, d);
+    int turn = 0;
+    for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x, turn ^= 1) {
+        f32x2 v[N][4], sq = 0;
+        const uint8_t *row = ring.wait();
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int c = 8 * (threadIdx.x + i * blockDim.x);
-            if (c < d) load8<kWide>(rx[i], x + c, d - c);
-        }
-        if (a.residual.p)
+            read4<kX == kF32>(v[i], row, col.read[i], col.n[i]);
+            if constexpr (kRes != kNone) {
+                f32x2 t[4];
+                read4<kRes == kF32>(t, row + p.src.bytes[0], col.read[i], col.n[i]);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int c = 8 * (threadIdx.x + i * blockDim.x);
-                if (c < d) load8<kWide>(rr[i], res + c, d - c);
+                for (int j = 0; j < 4; ++j) v[i][j] = add2(v[i][j], t[j]);
             }
+            f32x2 q = mul2(v[i][0], v[i][0]);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int c = 8 * (threadIdx.x + i * blockDim.x);
-            if (c < d) {
-                unpack8(v[i], rx[i]);
-                if (a.residual.p) {
-                    float t[8];
-                    unpack8(t, rr[i]);
+            for (int j = 1; j < 4; ++j) q = fma2(v[i][j], v[i][j], q);
+            sq = add2(sq, q);
+        }
+        ring.release();
+        ring.next();
+        float s0, s1;
+        unpair(sq, s0, s1);
+        const float rstd = inv_sqrt(fmaf(row_sum(s0 + s1, sums[turn], threads), inv_d, a.eps));
+        if constexpr (kRes != kNone)
+            if (a.hidden.p)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[i][j] += t[j];
+                for (int i = 0; i < N; ++i) {
+                    float h[8];
+                    singles(h, v[i]);
+                    if (col.n[i] > 0) store8<true>(a.hidden.p, kRes == kF32, r * a.hidden.ld + col.at[i], h, col.n[i]);
                 }
-                mask8(v[i], d - c);
-            } else {
+        if (a.rstd && threadIdx.x == 0) a.rstd[r] = rstd;
+        uint32_t top = 0;
+        const f32x2 rr = pair(rstd, rstd);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[i][j] = mul2(mul2(v[i][j], rr), w[i][j]);
+                if constexpr (kCodes) {
+                    // (past the row's end 0, or NaN where the whole row has one)
+                    float y0, y1;
+                    unpair(v[i][j], y0, y1);
+                    top = max(top, max(magnitude(y0), magnitude(y1)));
+                }
             }
+        float scale = 0.0f;
+        if constexpr (kCodes) {
+            scale = __fdiv_rn(__uint_as_float(row_max(top, maxima[turn], threads)), 448.0f);
+            if (threadIdx.x == 0) a.scale[r] = scale;
         }
-    }
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        float q = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q = fmaf(v[i][j], v[i][j], q);
-        s += q;
-    }
-    if (a.hidden.p)
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int c = 8 * (threadIdx.x + i * blockDim.x);
-            if (c < d) store8_any<kWide>(a.hidden.p, a.hidden.dtype, r * a.hidden.ld + c, v[i], d - c);
+            float y[8];
+            singles(y, v[i]);
+            if constexpr (kCodes) to_codes(y, scale);
+            if (col.n[i] > 0) {
+                if constexpr (kCodes)
+                    store8<true>(static_cast<E4m3 *>(a.out.p) + r * a.out.ld + col.at[i], y, col.n[i]);
+                else
+                    store8<true>(a.out.p, out32, r * a.out.ld + col.at[i], y, col.n[i]);
+            }
         }
-    const float mean = cta_sum(s, sums) / (float)d;
-    const float rstd = 1.0f / sqrtf(mean + a.eps);
-    if (a.rstd && threadIdx.x == 0) a.rstd[r] = rstd;
-    uint32_t top = 0;
+    }
+    ring.leave();
+}
+
+// Rows read where they lie, element by element; any types.
+template <int N>
+__global__ void __launch_bounds__(max_threads(N)) rms_norm_plain_kernel(const NormParams p) {
+    __shared__ float sums[2][32];
+    __shared__ uint32_t maxima[2][32];
+    const NormRows &a = p.a;
+    const int d = (int)a.d, threads = blockDim.x;
+    const Columns<N> col(d, threads);
+    const bool codes = a.out.dtype == DG_E4M3;
+    int turn = 0;
+    for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x, turn ^= 1) {
+        float v[N][8], s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int c = 8 * (threadIdx.x + i * blockDim.x);
-        if (c < d) {
+        for (int i = 0; i < N; ++i) {
+            Any8 raw;
+            load8(raw, a.x.p, a.x.dtype == DG_F32, r * a.x.ld + col.read[i], d - col.read[i]);
+            unpack8(v[i], raw, a.x.dtype == DG_F32);
+            if (a.residual.p) {
+                float t[8];
+                load8(raw, a.residual.p, a.residual.dtype == DG_F32, r * a.residual.ld + col.read[i], d - col.read[i]);
+                unpack8(t, raw, a.residual.dtype == DG_F32);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] += t[j];
+            }
+            mask8(v[i], col.n[i]);
+            float q = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q = fmaf(v[i][j], v[i][j], q);
+            s += q;
+        }
+        const float rstd = inv_sqrt(fmaf(row_sum(s, sums[turn], threads), 1.0f / (float)d, a.eps));
+        if (a.rstd && threadIdx.x == 0) a.rstd[r] = rstd;
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (a.hidden.p && col.n[i] > 0)
+                store8<false>(a.hidden.p, a.hidden.dtype == DG_F32, r * a.hidden.ld + col.at[i], v[i], col.n[i]);
             float w[8];
-            if (a.weight) {
-                load8_any<kWide>(w, a.weight, a.weight_dtype, c, d - c);
+            load_weight(w, a.weight, a.weight_dtype, a.weight_offset, col.read[i], col.n[i], d);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * (a.weight_offset + w[j]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] *= rstd;
-            }
-            if constexpr (kCodes) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (c + j < d) top = max(top, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
+            for (int j = 0; j < 8; ++j) {
+                v[i][j] = v[i][j] * rstd * w[j];
+                top = max(top, magnitude(v[i][j]));
             }
         }
-    }
-    TO *out = static_cast<TO *>(a.out.p) + r * a.out.ld;
-    float scale = 0.0f;
-    if constexpr (kCodes) {
-        scale = __fdiv_rn(__uint_as_float(cta_max(top, maxima)), 448.0f);
-        if (threadIdx.x == 0) a.scale[r] = scale;
-    }
+        float scale = 0.0f;
+        if (codes) {
+            scale = __fdiv_rn(__uint_as_float(row_max(top, maxima[turn], threads)), 448.0f);
+            if (threadIdx.x == 0) a.scale[r] = scale;
+        }
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int c = 8 * (threadIdx.x + i * blockDim.x);
-        if (c < d) {
-            if constexpr (kCodes) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = scale != 0.0f ? __fdiv_rn(v[i][j], scale) : 0.0f;
+        for (int i = 0; i < N; ++i) {
+            if (col.n[i] <= 0) continue;
+            if (codes) {
+                to_codes(v[i], scale);
+                store8<false>(static_cast<E4m3 *>(a.out.p) + r * a.out.ld + col.at[i], v[i], col.n[i]);
+            } else {
+                store8<false>(a.out.p, a.out.dtype == DG_F32, r * a.out.ld + col.at[i], v[i], col.n[i]);
             }
-            store8<kWide>(out + c, v[i], d - c);
         }
     }
 }
 
+// ---------------------------------------------------------------- backward
+
 struct NormBackParams {
     NormBackRows a;
+    Source src;    // grad, hidden, grad_hidden
     float *parts;  // [gridDim.x, part_ld]
     int64_t part_ld;
 };
 
-// A row as it lies in memory, this thread's columns of it.
-template <typename TG, typename TH, typename TD, int N>
-struct BackRow {
-    Raw8<TG> g[N];
-    Raw8<TH> h[N];
-    Raw8<TD> up[N];
-    float rstd;
-};
-
-// Loads in flight side by side: a thread past the row's end reads its last eight columns again, in place of a branch.
-template <bool kUp, bool kWide, typename TG, typename TH, typename TD, int N>
-__device__ __forceinline__ void load_row(BackRow<TG, TH, TD, N> &row, const NormBackRows &a, int64_t r, const int (&col)[N]) {
-    const TG *g = static_cast<const TG *>(a.grad.p) + r * a.grad.ld;
-    const TH *h = static_cast<const TH *>(a.hidden.p) + r * a.hidden.ld;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        load8<kWide>(row.g[i], g + col[i], (int)a.d - col[i]);
-        load8<kWide>(row.h[i], h + col[i], (int)a.d - col[i]);
-    }
-    if constexpr (kUp) {
-        const TD *up = static_cast<const TD *>(a.grad_hidden.p) + r * a.grad_hidden.ld;
-#pragma unroll
-        for (int i = 0; i < N; ++i) load8<kWide>(row.up[i], up + col[i], (int)a.d - col[i]);
-    }
-    row.rstd = a.rstd[r];
-}
-
-// kUp: with grad_hidden.  The next row is loaded while this one is reduced and stored.
-template <typename TG, typename TH, typename TD, int N, bool kUp, bool kWide>
-__global__ void __launch_bounds__(max_back_threads(N)) rms_norm_backward_kernel(const NormBackParams p) {
+template <int N, bool kG32, bool kH32, int kUp>
+__global__ void __launch_bounds__(max_threads(N) + 32) rms_norm_backward_kernel(const NormBackParams p) {
+    extern __shared__ uint4 smem[];
     __shared__ float sums[2][32];
+    __shared__ int gave_up;
     const NormBackRows &a = p.a;
-    const int d = (int)a.d, last = (d - 1) / 8 * 8;
-    int col[N];
-    float w[N][8], dw[N][8];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int c = 8 * (threadIdx.x + i * blockDim.x);
-        col[i] = min(c, last);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f, w[i][j] = 1.0f;
-        if (a.weight) {
-            load8_any<kWide>(w[i], a.weight, a.weight_dtype, col[i], d - col[i]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[i][j] += a.weight_offset;
-        }
-        mask8(w[i], d - c);  // (all zeros past the row's end)
+    const int d = (int)a.d, threads = blockDim.x - 32;
+    Ring ring(p.src, smem, &gave_up, threads);
+    if ((int)threadIdx.x >= threads) {
+        if ((int)threadIdx.x == threads) ring.send(p.src, a.R);
+        ring.leave();
+        return;
     }
+    const Columns<N> col(d, threads);
     const float inv_d = 1.0f / (float)d;
-    BackRow<TG, TH, TD, N> row;
-    if (blockIdx.x < a.R) load_row<kUp, kWide>(row, a, blockIdx.x, col);
+    f32x2 w[N][4], dw[N][4];
+    load_weight(w, a.weight, a.weight_dtype, a.weight_offset, col, d);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dw[i][j] = 0;
+    float next_rstd = blockIdx.x < a.R ? a.rstd[blockIdx.x] : 0.0f;
     int turn = 0;
     for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x, turn ^= 1) {
-        float g[N][8], xh[N][8], up[kUp ? N : 1][8];
-        const float rstd = row.rstd;
-        float s = 0.0f;
+        f32x2 g[N][4], xh[N][4], sq = 0;
+        const float rstd = next_rstd;
+        const f32x2 rr = pair(rstd, rstd);
+        if (r + gridDim.x < a.R) next_rstd = a.rstd[r + gridDim.x];
+        const uint8_t *row = ring.wait();
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            float q = 0.0f;
-            unpack8(g[i], row.g[i]);
-            unpack8(xh[i], row.h[i]);
-            if constexpr (kUp) unpack8(up[i], row.up[i]);
-            mask8(g[i], d - 8 * (int)(threadIdx.x + i * blockDim.x));  // (nothing past the row's end counts)
-            mask8(xh[i], d - 8 * (int)(threadIdx.x + i * blockDim.x));
+            read4<kG32>(g[i], row, col.read[i], col.n[i]);
+            read4<kH32>(xh[i], row + p.src.bytes[0], col.read[i], col.n[i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                xh[i][j] = mul2(xh[i][j], rr);
+                dw[i][j] = fma2(g[i][j], xh[i][j], dw[i][j]);
+                g[i][j] = mul2(g[i][j], w[i][j]);
+                sq = fma2(g[i][j], xh[i][j], sq);
+            }
+        }
+        float s0, s1;
+        unpair(sq, s0, s1);
+        const float mean = row_sum(s0 + s1, sums[turn], threads) * inv_d;
+        const f32x2 mm = pair(-mean, -mean);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            f32x2 up[4];
+            if constexpr (kUp != kNone) read4<kUp == kF32>(up, row + p.src.bytes[0] + p.src.bytes[1], col.read[i], col.n[i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                g[i][j] = mul2(rr, fma2(mm, xh[i][j], g[i][j]));
+                if constexpr (kUp != kNone) g[i][j] = add2(g[i][j], up[j]);
+            }
+            float y[8];
+            singles(y, g[i]);
+            if (col.n[i] > 0) store8<true>(a.grad_x.p, kH32, r * a.grad_x.ld + col.at[i], y, col.n[i]);
+        }
+        ring.release();
+        ring.next();
+    }
+    grid_launch_dependents();
+    if (a.grad_weight)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (col.n[i] > 0) {
+                float y[8];
+                singles(y, dw[i]);
+                store8<true>(p.parts + blockIdx.x * p.part_ld + col.at[i], y, 8);
+            }
+    ring.leave();
+}
+
+// Rows read where they lie, element by element; any types.
+template <int N>
+__global__ void __launch_bounds__(max_threads(N)) rms_norm_backward_plain_kernel(const NormBackParams p) {
+    __shared__ float sums[2][32];
+    const NormBackRows &a = p.a;
+    const int d = (int)a.d, threads = blockDim.x;
+    const Columns<N> col(d, threads);
+    float dw[N][8];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+    int turn = 0;
+    for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x, turn ^= 1) {
+        const float rstd = a.rstd[r];
+        float g[N][8], xh[N][8], s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float w[8], q = 0.0f;
+            Any8 raw;
+            load_weight(w, a.weight, a.weight_dtype, a.weight_offset, col.read[i], col.n[i], d);
+            load8(raw, a.grad.p, a.grad.dtype == DG_F32, r * a.grad.ld + col.read[i], d - col.read[i]);
+            unpack8(g[i], raw, a.grad.dtype == DG_F32);
+            load8(raw, a.hidden.p, a.hidden.dtype == DG_F32, r * a.hidden.ld + col.read[i], d - col.read[i]);
+            unpack8(xh[i], raw, a.hidden.dtype == DG_F32);
+            mask8(g[i], col.n[i]);
+            mask8(xh[i], col.n[i]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 xh[i][j] *= rstd;
                 dw[i][j] = fmaf(g[i][j], xh[i][j], dw[i][j]);
-                g[i][j] *= w[i][j];
+                g[i][j] *= w[j];
                 q = fmaf(g[i][j], xh[i][j], q);
             }
             s += q;
         }
-        if (r + gridDim.x < a.R) load_row<kUp, kWide>(row, a, r + gridDim.x, col);
-        const float mean = cta_sum(s, sums[turn]) * inv_d;
+        const float mean = row_sum(s, sums[turn], threads) * (1.0f / (float)d);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int c = 8 * (threadIdx.x + i * blockDim.x);
+            if (col.n[i] <= 0) continue;
+            float up[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                g[i][j] = rstd * fmaf(-mean, xh[i][j], g[i][j]);
-                if constexpr (kUp) g[i][j] += up[i][j];
+            for (int j = 0; j < 8; ++j) up[j] = 0.0f;
+            if (a.grad_hidden.p) {
+                Any8 raw;
+                load8(raw, a.grad_hidden.p, a.grad_hidden.dtype == DG_F32, r * a.grad_hidden.ld + col.at[i], col.n[i]);
+                unpack8(up, raw, a.grad_hidden.dtype == DG_F32);
             }
-            if (c < d) store8<kWide>(static_cast<TH *>(a.grad_x.p) + r * a.grad_x.ld + c, g[i], d - c);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[i][j] = rstd * fmaf(-mean, xh[i][j], g[i][j]) + up[j];
+            store8<false>(a.grad_x.p, a.grad_x.dtype == DG_F32, r * a.grad_x.ld + col.at[i], g[i], col.n[i]);
         }
     }
     if (a.grad_weight)
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int c = 8 * (threadIdx.x + i * blockDim.x);
-            if (c < d) store8<true>(p.parts + blockIdx.x * p.part_ld + c, dw[i], 8);
-        }
+        for (int i = 0; i < N; ++i)
+            if (col.n[i] > 0) store8<true>(p.parts + blockIdx.x * p.part_ld + col.at[i], dw[i], 8);
 }
 
 // dweight from the CTAs' parts: a warp row of 32 columns, the CTA's warps a share of the parts each.
@@ -264,10 +545,12 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float *__restri
     __shared__ float acc[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-    const int per = (n + 31) / 32;
+    const int per = (n + 31) / 32, end = min(n, (warp + 1) * per);
     float s = 0.0f;
+    grid_dependency_wait();
     if (c < d)
-        for (int i = warp * per; i < min(n, (warp + 1) * per); ++i) s += parts[i * part_ld + c];
+#pragma unroll 8
+        for (int i = warp * per; i < end; ++i) s += parts[i * part_ld + c];
     acc[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && c < d) {
@@ -280,116 +563,180 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float *__restri
     }
 }
 
-bool wide_vector(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+// ---------------------------------------------------------------- plan
 
-// Eights of columns per thread, the fewest with which a row fits a CTA; off the boundaries (not wide) one kernel is
-// enough for all rows but the widest.
-template <typename Max>
-int eights_per_thread(int64_t d, bool wide, int narrow, Max most) {
-    const int64_t eights = (d + 7) / 8;
-    for (const int n : {1, 2})
-        if (eights <= n * most(n) && (wide || n == narrow)) return n;
-    return 4;
-}
 int row_threads(int64_t d, int n) { return (int)((((d + 7) / 8 + n - 1) / n + 31) / 32 * 32); }
 
-template <typename TX, typename TR, typename TO>
-void norm_width(const NormParams &p, bool wide, cudaStream_t stream) {
-    const unsigned grid = (unsigned)p.a.R;
-    const int n = eights_per_thread(p.a.d, wide, 2, max_threads), threads = row_threads(p.a.d, n);
-    (wide ? n == 1   ? rms_norm_kernel<TX, TR, TO, 1, true>
-            : n == 2 ? rms_norm_kernel<TX, TR, TO, 2, true>
-                     : rms_norm_kernel<TX, TR, TO, 4, true>
-     : n == 2 ? rms_norm_kernel<TX, TR, TO, 2, false>
-              : rms_norm_kernel<TX, TR, TO, 4, false>)<<<grid, threads, 0, stream>>>(p);
+// Eights of columns per thread: two where that leaves four warps, whose instructions per row are then fewer.
+int eights_per_thread(int64_t d) {
+    const int64_t eights = (d + 7) / 8;
+    return eights <= 128 ? 1 : eights <= 2 * max_threads(2) ? 2 : eights <= 4 * max_threads(4) ? 4 : 8;
 }
-template <typename TX, typename TR>
-void norm_out(const NormParams &p, bool wide, cudaStream_t stream) {
-    if (p.a.out.dtype == DG_F32)
-        norm_width<TX, TR, float>(p, wide, stream);
-    else if (p.a.out.dtype == DG_BF16)
-        norm_width<TX, TR, __nv_bfloat16>(p, wide, stream);
-    else
-        norm_width<TX, TR, E4m3>(p, wide, stream);
+
+// A launch: CTAs of a row each, as many as the SMs hold, the shared memory left to each as its ring.
+struct Plan {
+    bool ring;
+    int n, threads, smem;  // threads: of a row
+    unsigned grid;
+};
+constexpr int kRingFixed = kRingHeader + kRingTail, kMaxCtas = 16;  // bytes; CTAs of an SM
+
+// `wide`: the matrices that are written may be reached by the widest accesses.
+Plan make_plan(Source *src, int64_t R, int64_t d, bool wide) {
+    Plan plan{};
+    src->stage_bytes = 0;
+    bool ring = wide;
+    for (int q = 0; q < 3; ++q) {
+        src->bytes[q] = src->m[q].p ? (int)((d * entry_size(src->m[q].dtype) + 15) / 16 * 16) : 0;
+        src->stage_bytes += src->bytes[q];
+        ring = ring && wide_rows(src->m[q]);
+    }
+    plan.ring = ring && src->stage_bytes <= kSmemLimit - kRingFixed;
+    plan.n = plan.ring ? eights_per_thread(d) : (d + 7) / 8 <= max_threads(1) ? 1 : 8;
+    plan.threads = row_threads(d, plan.n);
+    const int64_t sms = std::max(1, device_sm_count());
+    plan.grid = (unsigned)std::min<int64_t>(R, sms * std::min(kMaxCtas, 2048 / plan.threads));
+    return plan;
 }
-template <typename TX>
-void norm_residual(const NormParams &p, bool wide, cudaStream_t stream) {
-    if (p.a.residual.p && p.a.residual.dtype == DG_F32)
-        norm_out<TX, float>(p, wide, stream);
-    else
-        norm_out<TX, __nv_bfloat16>(p, wide, stream);
+
+// The rest of a ring's plan, for a kernel of so many registers a thread.
+void plan_ring(Plan *plan, Source *src, int64_t R, int regs) {
+    const int64_t sms = std::max(1, device_sm_count()), rows_per_sm = (R + sms - 1) / sms;
+    const int held = 65536 / ((regs + 7) / 8 * 8 * (plan->threads + 32));
+    int ctas = (int)std::max<int64_t>(1, std::min<int64_t>(rows_per_sm, std::min(held, kMaxCtas)));
+    while (ctas > 1 && kSmemPerSm / ctas - 1024 - kRingFixed < 2 * src->stage_bytes) --ctas;  // two rows at least for each
+    const int room = std::min(kSmemLimit, kSmemPerSm / ctas - 1024) - kRingFixed;
+    const int64_t rows_per_cta = (rows_per_sm + ctas - 1) / ctas;
+    src->stages = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(kMaxStages, room / src->stage_bytes), rows_per_cta));
+    plan->smem = kRingFixed + src->stages * src->stage_bytes;
+    plan->grid = (unsigned)std::min<int64_t>(R, sms * ctas);
+}
+
+// What is asked of the device once per kernel.
+struct Asked {
+    std::atomic<int> regs[64];  // 0: not yet
+};
+template <typename Params>
+cudaError_t launch_ring(void (*kernel)(Params), Asked &asked, Params p, Plan plan, unsigned *grid, cudaStream_t stream) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    int regs = e == cudaSuccess && dev < 64 ? asked.regs[dev].load(std::memory_order_acquire) : 0;
+    if (e == cudaSuccess && regs == 0) {
+        cudaFuncAttributes attr;
+        e = cudaFuncGetAttributes(&attr, kernel);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+        if (e == cudaSuccess) regs = attr.numRegs;
+        if (e == cudaSuccess && dev < 64) asked.regs[dev].store(regs, std::memory_order_release);
+    }
+    if (e != cudaSuccess) return e;
+    plan_ring(&plan, &p.src, p.a.R, regs);
+    *grid = plan.grid;
+    kernel<<<plan.grid, plan.threads + 32, plan.smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <int N, int kX, int kRes, bool kCodes>
+cudaError_t forward(const NormParams &p, const Plan &plan, cudaStream_t stream) {
+    static Asked asked;
+    unsigned grid;
+    return launch_ring(rms_norm_kernel<N, kX, kRes, kCodes>, asked, p, plan, &grid, stream);
+}
+template <int N, int kX, int kRes>
+cudaError_t forward_out(const NormParams &p, const Plan &plan, cudaStream_t stream) {
+    return p.a.out.dtype == DG_E4M3 ? forward<N, kX, kRes, true>(p, plan, stream) : forward<N, kX, kRes, false>(p, plan, stream);
+}
+template <int N, int kX>
+cudaError_t forward_residual(const NormParams &p, const Plan &plan, cudaStream_t stream) {
+    const int kind = kind_of(p.a.residual);
+    return kind == kNone   ? forward_out<N, kX, kNone>(p, plan, stream)
+           : kind == kBf16 ? forward_out<N, kX, kBf16>(p, plan, stream)
+                           : forward_out<N, kX, kF32>(p, plan, stream);
+}
+template <int N>
+cudaError_t forward_types(const NormParams &p, const Plan &plan, cudaStream_t stream) {
+    return p.a.x.dtype == DG_F32 ? forward_residual<N, kF32>(p, plan, stream) : forward_residual<N, kBf16>(p, plan, stream);
+}
+
+template <int N, bool kG32, bool kH32, int kUp>
+cudaError_t backward(const NormBackParams &p, const Plan &plan, unsigned *grid, cudaStream_t stream) {
+    static Asked asked;
+    return launch_ring(rms_norm_backward_kernel<N, kG32, kH32, kUp>, asked, p, plan, grid, stream);
+}
+template <int N, bool kG32, bool kH32>
+cudaError_t backward_up(const NormBackParams &p, const Plan &plan, unsigned *grid, cudaStream_t stream) {
+    const int kind = kind_of(p.a.grad_hidden);
+    return kind == kNone   ? backward<N, kG32, kH32, kNone>(p, plan, grid, stream)
+           : kind == kBf16 ? backward<N, kG32, kH32, kBf16>(p, plan, grid, stream)
+                           : backward<N, kG32, kH32, kF32>(p, plan, grid, stream);
+}
+template <int N>
+cudaError_t backward_types(const NormBackParams &p, const Plan &plan, unsigned *grid, cudaStream_t stream) {
+    const bool h32 = p.a.hidden.dtype == DG_F32;
+    if (p.a.grad.dtype == DG_F32)
+        return h32 ? backward_up<N, true, true>(p, plan, grid, stream) : backward_up<N, true, false>(p, plan, grid, stream);
+    return h32 ? backward_up<N, false, true>(p, plan, grid, stream) : backward_up<N, false, false>(p, plan, grid, stream);
 }
 
 int64_t part_stride(int64_t d) { return (d + 7) / 8 * 8; }
 
-// CTAs of the backward pass at most: as many as the SMs could hold.
-int64_t back_grid_most(int64_t R, int64_t d) {
-    return std::min<int64_t>(R, (int64_t)std::max(1, device_sm_count()) * std::min(32, 2048 / row_threads(d, 4)));
-}
-
-// One wave of CTAs, each of which keeps its columns' sums over all its rows; *grid: how many.
-template <typename TG, typename TH, typename TD, int N, bool kUp, bool kWide>
-cudaError_t launch_back(const NormBackParams &p, unsigned *grid, cudaStream_t stream) {
-    const auto kernel = rms_norm_backward_kernel<TG, TH, TD, N, kUp, kWide>;
-    const int threads = row_threads(p.a.d, N);
-    int per_sm = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
-    if (e != cudaSuccess) return e;
-    *grid = (unsigned)std::min(back_grid_most(p.a.R, p.a.d), (int64_t)std::max(1, device_sm_count()) * std::max(1, per_sm));
-    kernel<<<*grid, threads, 0, stream>>>(p);
-    return cudaGetLastError();
-}
-template <typename TG, typename TH, typename TD, bool kUp>
-cudaError_t back_width(const NormBackParams &p, bool wide, unsigned *grid, cudaStream_t stream) {
-    const int n = eights_per_thread(p.a.d, wide, 1, max_back_threads);
-    if (wide)
-        return n == 1   ? launch_back<TG, TH, TD, 1, kUp, true>(p, grid, stream)
-               : n == 2 ? launch_back<TG, TH, TD, 2, kUp, true>(p, grid, stream)
-                        : launch_back<TG, TH, TD, 4, kUp, true>(p, grid, stream);
-    return n == 1 ? launch_back<TG, TH, TD, 1, kUp, false>(p, grid, stream)
-                  : launch_back<TG, TH, TD, 4, kUp, false>(p, grid, stream);
-}
-template <typename TG, typename TH>
-cudaError_t back_residual(const NormBackParams &p, bool wide, unsigned *grid, cudaStream_t stream) {
-    if (!p.a.grad_hidden.p) return back_width<TG, TH, float, false>(p, wide, grid, stream);
-    return p.a.grad_hidden.dtype == DG_F32 ? back_width<TG, TH, float, true>(p, wide, grid, stream)
-                                           : back_width<TG, TH, __nv_bfloat16, true>(p, wide, grid, stream);
-}
-
 }  // namespace
 
 cudaError_t launch_rms_norm(const NormRows &a, cudaStream_t stream) {
-    const NormParams p{a};
-    const bool wide = wide_rows(a.x) && wide_rows(a.residual) && wide_rows(a.hidden) && wide_rows(a.out) &&
-                      wide_vector(a.weight);
-    if (a.x.dtype == DG_F32)
-        norm_residual<float>(p, wide, stream);
-    else
-        norm_residual<__nv_bfloat16>(p, wide, stream);
+    NormParams p{a, {}};
+    p.src.m[0] = a.x;
+    p.src.m[1] = a.residual;
+    // (hidden of another type than the residual, or without one, is rare: rows read where they lie)
+    const bool plain = a.hidden.p && (!a.residual.p || a.hidden.dtype != a.residual.dtype);
+    const Plan plan = make_plan(&p.src, a.R, a.d, !plain && wide_rows(a.hidden) && wide_rows(a.out));
+    if (plan.ring)
+        return plan.n == 1   ? forward_types<1>(p, plan, stream)
+               : plan.n == 2 ? forward_types<2>(p, plan, stream)
+               : plan.n == 4 ? forward_types<4>(p, plan, stream)
+                             : forward_types<8>(p, plan, stream);
+    (plan.n == 1 ? rms_norm_plain_kernel<1> : rms_norm_plain_kernel<8>)<<<plan.grid, plan.threads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
 size_t rms_norm_backward_bytes(int64_t R, int64_t d) {
-    return (size_t)back_grid_most(R, d) * (size_t)part_stride(d) * sizeof(float);
+    const int64_t most = std::min<int64_t>(R, kMaxCtas * (int64_t)std::max(1, device_sm_count()));
+    return (size_t)most * (size_t)part_stride(d) * sizeof(float);
 }
 
 cudaError_t launch_rms_norm_backward(const NormBackRows &a, void *workspace, cudaStream_t stream) {
-    const NormBackParams p{a, static_cast<float *>(workspace), part_stride(a.d)};
-    const bool wide = wide_rows(a.grad) && wide_rows(a.hidden) && wide_rows(a.grad_hidden) && wide_rows(a.grad_x) &&
-                      wide_vector(a.weight);
+    NormBackParams p{a, {}, static_cast<float *>(workspace), part_stride(a.d)};
     unsigned grid = 0;
     if (a.R > 0) {
-        const bool g32 = a.grad.dtype == DG_F32, h32 = a.hidden.dtype == DG_F32;
-        const cudaError_t e = g32 ? h32 ? back_residual<float, float>(p, wide, &grid, stream)
-                                        : back_residual<float, __nv_bfloat16>(p, wide, &grid, stream)
-                              : h32 ? back_residual<__nv_bfloat16, float>(p, wide, &grid, stream)
-                                    : back_residual<__nv_bfloat16, __nv_bfloat16>(p, wide, &grid, stream);
+        p.src.m[0] = a.grad;
+        p.src.m[1] = a.hidden;
+        p.src.m[2] = a.grad_hidden;
+        const Plan plan = make_plan(&p.src, a.R, a.d, wide_rows(a.grad_x));
+        grid = plan.grid;
+        cudaError_t e;
+        if (plan.ring) {
+            e = plan.n == 1   ? backward_types<1>(p, plan, &grid, stream)
+                : plan.n == 2 ? backward_types<2>(p, plan, &grid, stream)
+                : plan.n == 4 ? backward_types<4>(p, plan, &grid, stream)
+                              : backward_types<8>(p, plan, &grid, stream);
+        } else {
+            (plan.n == 1 ? rms_norm_backward_plain_kernel<1>
+                         : rms_norm_backward_plain_kernel<8>)<<<plan.grid, plan.threads, 0, stream>>>(p);
+            e = cudaGetLastError();
+        }
         if (e != cudaSuccess) return e;
     }
-    if (a.grad_weight)
-        norm_weight_kernel<<<(unsigned)((a.d + 31) / 32), 1024, 0, stream>>>(p.parts, p.part_ld, (int)grid, a.d,
-                                                                            a.grad_weight, a.weight_dtype);
-    return cudaGetLastError();
+    if (!a.grad_weight) return cudaSuccess;
+    // (starts while the rows' kernel ends)
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.d + 31) / 32), 1, 1);
+    cfg.blockDim = dim3(1024, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = a.R > 0 ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, norm_weight_kernel, (const float *)p.parts, p.part_ld, (int)grid, a.d, a.grad_weight,
+                              a.weight_dtype);
 }
 
 }  // namespace dg
