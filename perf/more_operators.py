@@ -219,11 +219,13 @@ def _run_own(s, c):
             s["ws"] = B.norm_workspace(c["R"], c["d"], s["x"].device)
         return B.dg_rms_norm_backward(s["grad"], s["x"], s["rstd"], s["weight"], weight_offset=c["offset"],
                                       grad_hidden=s.get("grad_hidden"), ws=s["ws"], out=s["out"])
+    if "gamma" not in s:  # a number that the program has
+        s["gamma"] = _gamma(c["d"])
     if c["pass"] == "forward":
-        return B.dg_token_embed(s["table"], s["token"], _gamma(c["d"]), scale=s.get("scale"), out=s["out"])
+        return B.dg_token_embed(s["table"], s["token"], s["gamma"], scale=s.get("scale"), out=s["out"])
     if "ws" not in s:
         s["ws"] = B.embed_workspace(c["R"], c["V"], c["d"], s["token"].device)
-    return B.dg_token_embed_backward(s["grad"], s["token"], c["V"], _gamma(c["d"]), accumulate=c["accumulate"],
+    return B.dg_token_embed_backward(s["grad"], s["token"], c["V"], s["gamma"], accumulate=c["accumulate"],
                                      ws=s["ws"], out=s["table_grad"])
 
 
