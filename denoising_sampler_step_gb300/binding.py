@@ -895,10 +895,11 @@ def _matrix(t: torch.Tensor, R: int, d: int, name: str, device, types=_DTYPE) ->
     code = types.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} has type {t.dtype}: need one of {', '.join(map(str, types))}")
-    if t.shape != (R, d) or (d > 1 and t.stride(1) != 1) or t.device != device:
+    strides = t.stride()        # (one call: each costs a small call a hundredth of its time)
+    if t.shape != (R, d) or (strides[1] != 1 and d > 1) or t.device != device:
         raise ValueError(f"{name} must be [{R}, {d}] with unit column stride on {device}, "
-                         f"got {list(t.shape)} with strides {list(t.stride())} on {t.device}")
-    return t.data_ptr(), code, t.stride(0) if R > 1 else (d + 15) // 16 * 16
+                         f"got {list(t.shape)} with strides {list(strides)} on {t.device}")
+    return t.data_ptr(), code, strides[0] if R > 1 else (d + 15) // 16 * 16
 
 
 def _here(t: torch.Tensor, name: str):
