@@ -41,7 +41,8 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
     const EmbedRows &a = p.a;
     const int per_cta = kGatherThreads / p.lanes;
     const int lane = threadIdx.x % p.lanes;
-    const int d = (int)a.d;
+    const int d = (int)a.d, last = (d - 1) / 8 * 8;
+    constexpr int kAhead = kWide ? 32 / (2 * sizeof(TT)) < 12 ? 32 / (2 * sizeof(TT)) : 12 : 2;  // loads in flight
     for (int64_t r = (int64_t)blockIdx.x * per_cta + threadIdx.x / p.lanes; r < a.R; r += (int64_t)gridDim.x * per_cta) {
         const int64_t t = a.token[r];
         const bool on = t >= a.vocab_start && t < a.vocab_end;
@@ -49,16 +50,16 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
         const TT *src = static_cast<const TT *>(a.table.p) + (on ? (t - a.vocab_start) * a.table.ld : 0);
         const float f = on && a.scale ? a.scale[t - a.vocab_start] : 1.0f;
         TO *dst = static_cast<TO *>(a.rows.p) + r * a.rows.ld;
-        for (int c0 = 8 * lane; c0 < d; c0 += 4 * 8 * p.lanes) {
-            Raw8<TT> raw[4];
+        for (int c0 = 8 * lane; c0 < d; c0 += kAhead * 8 * p.lanes) {
+            Raw8<TT> raw[kAhead];
             if (on)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = c0 + i * 8 * p.lanes;
-                    if (c < d) load8<kWide>(raw[i], src + c, d - c);
+                for (int i = 0; i < kAhead; ++i) {  // (past the row's end its last columns again)
+                    const int c = min(c0 + i * 8 * p.lanes, last);
+                    load8<kWide>(raw[i], src + c, d - c);
                 }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kAhead; ++i) {
                 const int c = c0 + i * 8 * p.lanes;
                 if (c >= d) break;
                 float v[8];
@@ -803,7 +804,7 @@ cudaError_t launch_token_embed(const EmbedRows &a, cudaStream_t stream) {
     GatherParams p{a, 32};
     const int64_t sms = std::max(1, device_sm_count()), eights = (a.d + 7) / 8;
     // a warp per row where the rows alone fill the chip, more threads per row where they do not
-    while (p.lanes < kGatherThreads && a.R * p.lanes < sms * 2048 && p.lanes < eights) p.lanes *= 2;
+    while (p.lanes < kGatherThreads && a.R * p.lanes < sms * 1024 && p.lanes < eights) p.lanes *= 2;
     const int64_t per = kGatherThreads / p.lanes;
     const unsigned grid = (unsigned)std::min<int64_t>((a.R + per - 1) / per, sms * 64);
     if (a.table.dtype == DG_F32)
