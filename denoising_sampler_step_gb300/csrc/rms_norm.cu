@@ -414,6 +414,7 @@ __global__ void __launch_bounds__(max_threads(N) + 32) rms_norm_backward_kernel(
     __shared__ int gave_up;
     const NormBackRows &a = p.a;
     const int d = (int)a.d, threads = blockDim.x - 32;
+    grid_launch_dependents();  // (the sum of the parts waits for this kernel's end on the SMs)
     Ring ring(p.src, smem, &gave_up, threads);
     if ((int)threadIdx.x >= threads) {
         if ((int)threadIdx.x == threads) ring.send(p.src, a.R);
@@ -468,7 +469,6 @@ __global__ void __launch_bounds__(max_threads(N) + 32) rms_norm_backward_kernel(
         ring.release();
         ring.next();
     }
-    grid_launch_dependents();
     if (a.grad_weight)
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -539,27 +539,32 @@ __global__ void __launch_bounds__(max_threads(N)) rms_norm_backward_plain_kernel
             if (col.n[i] > 0) store8<true>(p.parts + blockIdx.x * p.part_ld + col.at[i], dw[i], 8);
 }
 
-// dweight from the CTAs' parts: a warp row of 32 columns, the CTA's warps a share of the parts each.
-__global__ void __launch_bounds__(1024) norm_weight_kernel(const float *__restrict__ parts, int64_t part_ld, int n,
-                                                           int64_t d, void *__restrict__ out, int dtype) {
-    __shared__ float acc[32][33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-    const int per = (n + 31) / 32, end = min(n, (warp + 1) * per);
-    float s = 0.0f;
+// dweight from the CTAs' parts, 32 columns a CTA: a warp reads four parts at a time, eight lanes each.
+constexpr int kWeightThreads = 256;
+__global__ void __launch_bounds__(kWeightThreads) norm_weight_kernel(const float *__restrict__ parts, int64_t part_ld, int n,
+                                                                     int64_t d, void *__restrict__ out, int dtype) {
+    __shared__ float4 acc[kWeightThreads / 8][8];
+    const int at = threadIdx.x / 8;
+    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x % 8 * 4;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     grid_dependency_wait();
-    if (c < d)
+    if (c < part_ld)
 #pragma unroll 8
-        for (int i = warp * per; i < end; ++i) s += parts[i * part_ld + c];
-    acc[warp][lane] = s;
+        for (int i = at; i < n; i += kWeightThreads / 8) {
+            const float4 v = *reinterpret_cast<const float4 *>(parts + i * part_ld + c);
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+    acc[at][threadIdx.x % 8] = s;
     __syncthreads();
-    if (warp == 0 && c < d) {
-        s = 0.0f;
-        for (int w = 0; w < 32; ++w) s += acc[w][lane];
+    const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.x;
+    if (threadIdx.x < 32 && col < d) {
+        float sum = 0.0f;
+#pragma unroll 8
+        for (int i = 0; i < kWeightThreads / 8; ++i) sum += reinterpret_cast<const float *>(acc[i])[threadIdx.x];
         if (dtype == DG_F32)
-            static_cast<float *>(out)[c] = s;
+            static_cast<float *>(out)[col] = sum;
         else
-            static_cast<__nv_bfloat16 *>(out)[c] = __float2bfloat16_rn(s);
+            static_cast<__nv_bfloat16 *>(out)[col] = __float2bfloat16_rn(sum);
     }
 }
 
@@ -728,7 +733,7 @@ cudaError_t launch_rms_norm_backward(const NormBackRows &a, void *workspace, cud
     // (starts while the rows' kernel ends)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((a.d + 31) / 32), 1, 1);
-    cfg.blockDim = dim3(1024, 1, 1);
+    cfg.blockDim = dim3(kWeightThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
