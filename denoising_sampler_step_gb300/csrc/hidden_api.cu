@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "dg_internal.h"
 #include "hidden.cuh"
@@ -81,6 +82,14 @@ dg_status check_norm(const char *what, int64_t R, int64_t d, const void *weight,
     return DG_OK;
 }
 
+// Vectors of four-byte entries.
+dg_status check_vectors(const char *what, std::initializer_list<const void *> vectors) {
+    for (const void *v : vectors)
+        if (reinterpret_cast<uintptr_t>(v) & 3)
+            return fail(DG_ERR_UNSUPPORTED, "%s: a vector of tokens, scales or statistics is not 4-byte aligned", what);
+    return DG_OK;
+}
+
 dg_status check_workspace(const char *what, const void *workspace, size_t bytes, size_t need) {
     if (!workspace || bytes < need)
         return fail(DG_ERR_INVALID_ARG, "%s: workspace of %zu bytes is below the %zu needed", what,
@@ -116,6 +125,7 @@ dg_status dg_token_embed(const void *table, int32_t dtype, const float *scale, i
     if (R == 0) return DG_OK;
     if ((dtype == DG_E4M3) != (scale != nullptr) && rows > 0)
         return fail(DG_ERR_INVALID_ARG, "%s: scale goes with E4M3 codes, and with them alone", what);
+    DG_TRY(check_vectors(what, {token, scale}));
     if (meet(span(a.rows, R, d), span(a.table, rows, d))) return overlap(what, "out", "table");
     if (meet(span(a.rows, R, d), span(token, 4 * R))) return overlap(what, "out", "token");
     if (meet(span(a.rows, R, d), span(scale, 4 * rows))) return overlap(what, "out", "scale");
@@ -141,6 +151,7 @@ dg_status dg_token_embed_backward(const void *grad, int32_t dtype, int64_t R, in
     DG_TRY(check_rows(what, "grad_table", a.table, rows, d));
     DG_TRY(check_rows(what, "grad", a.rows, R, d));
     if (rows == 0 || (R == 0 && a.accumulate)) return DG_OK;
+    DG_TRY(check_vectors(what, {token}));
     if (R > 0) {
         DG_TRY(check_workspace(what, workspace, workspace_bytes, token_embed_backward_bytes(R, rows, d)));
         const Span t = span(a.table, rows, d), w = span(workspace, (int64_t)workspace_bytes);
@@ -172,6 +183,7 @@ dg_status dg_rms_norm(const void *x, int32_t dtype, int64_t R, int64_t d, int64_
     if (R == 0) return DG_OK;
     if ((out_dtype == DG_E4M3) != (out_scale != nullptr))
         return fail(DG_ERR_INVALID_ARG, "%s: out_scale goes with E4M3 codes, and with them alone", what);
+    DG_TRY(check_vectors(what, {out_scale, rstd}));
     if (!apart_or_same(a.out, a.x, R, d)) return overlap(what, "out", "x without replacing it");
     if (residual && !apart_or_same(a.out, a.residual, R, d)) return overlap(what, "out", "residual without replacing it");
     const Span so = span(a.out, R, d), sh = span(a.hidden, R, d);
@@ -218,6 +230,7 @@ dg_status dg_rms_norm_backward(const void *grad, int32_t dtype, int64_t R, int64
     if (grad_weight && reinterpret_cast<uintptr_t>(grad_weight) % entry_size(weight_dtype) != 0)
         return fail(DG_ERR_UNSUPPORTED, "%s: grad_weight is not aligned to its entries", what);
     if (R == 0 && !grad_weight) return DG_OK;
+    DG_TRY(check_vectors(what, {rstd}));
     const Span sx = span(a.grad_x, R, d), sw = span(grad_weight, grad_weight ? d * entry_size(weight_dtype) : 0);
     const Span in[] = {span(a.grad, R, d), span(a.hidden, R, d), span(a.grad_hidden, R, d), span(rstd, 4 * R),
                        span(weight, weight ? d * entry_size(weight_dtype) : 0)};
@@ -261,6 +274,7 @@ dg_status dg_head_e4m3(const uint8_t *X, int64_t ldx, const float *x_scale, int6
     if (!aligned16(logits) || (ldl * entry_size(dtype)) % 16 != 0)
         return fail(DG_ERR_UNSUPPORTED, "%s: logits rows must start on 16-byte boundaries: pad the row stride to a "
                     "multiple of %d elements", what, 16 / entry_size(dtype));
+    DG_TRY(check_vectors(what, {x_scale, scale}));
     if (ldx >= (1LL << 40) || ldq >= (1LL << 40)) return fail(DG_ERR_UNSUPPORTED, "%s: a row stride is too large", what);
     const Span sl = span(l, R, V);
     if (meet(sl, span(x, R, d)) || meet(sl, span(q, V, d)) || meet(sl, span(x_scale, 4 * R)) || meet(sl, span(scale, 4 * V)))

@@ -299,6 +299,54 @@ def test_norm_without_weight_and_many_rows(B):
     assert sorted(got) == ["out", "rstd"] and got["out"].dtype == torch.bfloat16
 
 
+def test_norm_of_many_rows(B):
+    """Several turns of every CTA, of rows that begin on 16-byte boundaries and of others."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    R, d = 20011, 264
+    x, res, up = (torch.randn(R, d + 8, generator=g, device="cuda") for _ in range(3))
+    w = torch.randn(d, generator=g, device="cuda")
+    for c in (0, 1):
+        v = [t[:, c:c + d] for t in (x, res, up)]
+        o = B.dg_rms_norm(v[0], w, residual=v[1], dtype=torch.uint8)
+        h = v[0].double() + v[1].double()
+        rstd = (h.square().mean(1) + 1e-6) ** -0.5
+        y = h * rstd[:, None] * w.double()
+        assert ((o["hidden"] - h).abs() <= U * h.abs()).all() and ((o["rstd"] - rstd).abs() <= 52 * U * rstd).all()
+        s, top = o["scale"].double()[:, None], y.abs().amax(1, keepdim=True)
+        assert ((s - top / 448).abs() <= 57 * U * top / 448).all()
+        q = o["out"].view(torch.float8_e4m3fn).double() * s
+        assert ((q - y).abs() <= torch.maximum(2.0 ** -4 * y.abs(), 2.0 ** -10 * s) * (1 + 4 * U) + 60 * U * y.abs()).all()
+        b = B.dg_rms_norm_backward(v[2], o["hidden"], o["rstd"], w, grad_hidden=v[0])
+        h, rs, gw = o["hidden"].double(), o["rstd"].double()[:, None], v[2].double() * w.double()
+        xh = h * rs
+        inner, size = (gw * xh).mean(1, keepdim=True), (gw * xh).abs().mean(1, keepdim=True)
+        ref = v[0].double() + rs * (gw - xh * inner)
+        tol = rs * (6 * U * gw.abs() + 102 * U * xh.abs() * size) + 4 * U * ref.abs() + U * v[0].abs()
+        assert ((b["grad"] - ref).abs() <= tol).all()
+        terms = v[2].double() * xh
+        assert ((b["grad_weight"] - terms.sum(0)).abs() <= (R + 3) * U * terms.abs().sum(0)).all()
+
+
+def test_norm_hidden_of_its_own_type(B):
+    rng = np.random.default_rng(6)
+    xd, xv = place(size(rng, 30, 520), "f32")
+    rd, rv = place(size(rng, 30, 520), "bf16")
+    ref = B.dg_rms_norm(xd, residual=rd)
+    for kind in ("f32", "bf16"):
+        for res, h in ((rd, xv + rv), (None, xv)):
+            o = B.dg_rms_norm(xd, residual=res, out={"hidden": empty(30, 520, kind)})
+            close(o["hidden"], h, (HALF[kind] + U) * np.abs(h))
+            untouched(o["hidden"], kind)
+        close(B.dg_rms_norm(xd, residual=rd, out={"hidden": empty(30, 520, kind)})["out"], np64(ref["out"]),
+              56 * U * np.abs(np64(ref["out"])))
+    o = B.dg_rms_norm(xd, residual=rd, out={"hidden": None})
+    assert o["hidden"] is None and torch.equal(o["out"], ref["out"])
+
+
+def np64(t):
+    return t.double().cpu().numpy()
+
+
 @pytest.mark.parametrize("out", ["f32", "e4m3"])
 def test_rows_of_zeros_and_of_what_is_no_number(B, out):
     x = torch.ones(6, 300, device="cuda")

@@ -33,7 +33,8 @@ def test_token_embed(L):
                dict(odt=2), dict(dtype=2), dict(scale=D), dict(out=off(A, 32)), dict(out=off(Bq, 8))):
         assert embed(L, **kw) == INV, kw
     for kw in (dict(V=2 ** 31, rows=2 ** 31), dict(R=2 ** 28 + 1), dict(d=2 ** 30, ldw=2 ** 30, ldo=2 ** 30),
-               dict(table=off(A, 1)), dict(out=off(C, 1)), dict(odt=0, out=off(C, 2)), dict(ldo=1 << 60)):
+               dict(table=off(A, 1)), dict(out=off(C, 1)), dict(odt=0, out=off(C, 2)), dict(token=off(Bq, 2)),
+               dict(dtype=2, scale=off(D, 1)), dict(ldo=1 << 60)):
         assert embed(L, **kw) == UNS, kw
     assert b"out" in L.dg_last_error()
     assert embed(L, R=0, token=None, out=None, table=None) == 0
@@ -51,7 +52,7 @@ def test_token_embed_backward(L):
                dict(tdt=2), dict(token=None), dict(grad=None), dict(table=None), dict(ws=None), dict(n=need - 1),
                dict(table=off(A, 64)), dict(table=Bq), dict(ws=C), dict(ws=A), dict(ws=Bq)):
         assert backward(L, **kw) == INV, kw
-    for kw in (dict(ws=off(D, 8)), dict(grad=off(A, 1)), dict(table=off(C, 2)), dict(V=2 ** 31, e=2 ** 31, rows=2 ** 31)):
+    for kw in (dict(ws=off(D, 8)), dict(token=off(Bq, 1)), dict(grad=off(A, 1)), dict(table=off(C, 2)), dict(V=2 ** 31, e=2 ** 31, rows=2 ** 31)):
         assert backward(L, **kw) == UNS, kw
     # nothing to do
     assert backward(L, R=0, acc=1, token=None, grad=None, ws=None, n=0) == 0
@@ -76,7 +77,7 @@ def test_rms_norm(L):
                dict(w=C, wdt=1), dict(rstd=A), dict(rstd=C), dict(odt=2, scale=D), dict(rstd=off(D, 4), odt=2, scale=D)):
         assert norm(L, **kw) == INV, kw
     for kw in (dict(R=2 ** 28 + 1), dict(d=32769, ldx=32769, ldo=32769), dict(x=off(A, 1)), dict(out=off(C, 1)),
-               dict(w=off(E, 2)), dict(res=off(Bq, 2), rdt=0)):
+               dict(w=off(E, 2)), dict(res=off(Bq, 2), rdt=0), dict(rstd=off(D, 2)), dict(odt=2, scale=off(E, 1))):
         assert norm(L, **kw) == UNS, kw
     assert norm(L, R=0, x=None, out=None, rstd=None) == 0
 
@@ -95,7 +96,7 @@ def test_rms_norm_backward(L):
                dict(up=E, gx=off(E, 2)), dict(gx=D), dict(w=W, gw=W), dict(w=W, gw=A), dict(w=C), dict(w=W, gw=D)):
         assert norm_back(L, **kw) == INV, kw
     for kw in (dict(d=32769, ldg=32769, ldh=32769, ldx=32769), dict(grad=off(A, 1)), dict(w=W, gw=off(G, 2)),
-               dict(w=off(W, 1), wdt=1)):
+               dict(w=off(W, 1), wdt=1), dict(rstd=off(D, 3))):
         assert norm_back(L, **kw) == UNS, kw
     assert norm_back(L, R=0, grad=None, hid=None, rstd=None, gx=None) == 0
     assert L.dg_rms_norm_backward_workspace_size(4, 32769) == 0 == L.dg_rms_norm_backward_workspace_size(0, 16)
@@ -111,7 +112,7 @@ def test_head(L):
                dict(out=off(C, 16)), dict(out=D)):
         assert head(L, **kw) == INV, kw
     for kw in (dict(R=2 ** 28 + 1), dict(V=2 ** 31, ldl=2 ** 31), dict(d=2 ** 24, ldx=2 ** 24, ldq=2 ** 24), dict(ldx=24),
-               dict(ldq=40), dict(X=off(A, 8)), dict(Q=off(C, 8)), dict(out=off(E, 8)), dict(V=99, ldl=99),
+               dict(ldq=40), dict(X=off(A, 8)), dict(Q=off(C, 8)), dict(out=off(E, 8)), dict(xs=off(Bq, 2)), dict(s=off(D, 1)), dict(V=99, ldl=99),
                dict(dtype=1, ldl=100)):
         assert head(L, **kw) == UNS, kw
     assert b"multiple of 8 elements" in L.dg_last_error()
