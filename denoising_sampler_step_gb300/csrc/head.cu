@@ -40,6 +40,8 @@ constexpr int kTmemCols = 512;
 constexpr int kSmemLimit = 232448;          // shared memory of a CTA
 constexpr int kResidentBytes = 96 * 1024;   // a CTA's half of the positions, at most, to stay in it
 constexpr int kBarrierBytes = 512;
+constexpr int kStageBytes = 8192;           // of logits on their way out: two buffers for each half of the epilogue
+constexpr int kFewPositions = 64;           // up to these the logits are stored from registers
 
 struct HeadParams {
     const float *x_scale, *w_scale;
@@ -52,6 +54,7 @@ struct HeadParams {
     uint32_t idesc;
     int stream_table;   // each table byte is read once: leave L2 first
     int stream_logits;  // the logits do not stay in L2 either way
+    int staged;         // logits go through shared memory
 };
 
 // Instruction descriptor of kind::f8f6f4 with E4M3 A and B, fp32 accumulator, both K-major.
@@ -123,10 +126,65 @@ __device__ __forceinline__ void store_chunk(const HeadParams &p, __nv_bfloat16 *
     }
 }
 
+// 32 lanes x 16 consecutive fp32 columns, as tmem_ld_32x32b_x32.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+
+// Logits through shared memory: a half of the epilogue (four warps, a lane quarter each) gathers kTokens positions of
+// all the tile's table rows, [position][table row], which one thread sends out as one tile; rows and columns past the
+// matrix are cut off there.  So a position's logits leave as one piece of 256 or 512 bytes, where a warp's own stores
+// were pieces of 64 or 128 that took twice the time of the bytes.
+template <typename T>
+constexpr int kTokens = kStageBytes / (kRowsCta * (int)sizeof(T));
+
+// Whether all threads of the half say yes: they go on, or stop, together.
+__device__ __forceinline__ bool half_vote(int half, bool yes) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.and.pred p, %2, 128, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(all)
+        : "r"((uint32_t)yes), "r"(half + 1)
+        : "memory");
+    return all != 0;
+}
+__device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(half + 1) : "memory"); }
+
+__device__ __forceinline__ void put_logits(uint32_t at, int pitch, const uint32_t (&acc)[16], int entry, float sw, float sx, int c0,
+                                           float) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+        const float y = __uint_as_float(acc[c]) * sw * __shfl_sync(0xffffffffu, sx, c0 + c);
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + (uint32_t)(c * pitch + 4 * entry)), "f"(y) : "memory");
+    }
+}
+// bf16: neighbouring lanes swap a value so that each puts two table rows' logits of one position.
+__device__ __forceinline__ void put_logits(uint32_t at, int pitch, const uint32_t (&acc)[16], int entry, float sw, float sx, int c0,
+                                           __nv_bfloat16) {
+    const int odd = entry & 1;
+#pragma unroll
+    for (int c = 0; c < 16; c += 2) {
+        const float a = __uint_as_float(acc[c]) * sw * __shfl_sync(0xffffffffu, sx, c0 + c);
+        const float b = __uint_as_float(acc[c + 1]) * sw * __shfl_sync(0xffffffffu, sx, c0 + c + 1);
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+        const uint32_t y = hidden::pack_bf16(odd ? got : a, odd ? b : got);
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + (uint32_t)((c + odd) * pitch + 2 * (entry - odd))), "r"(y) : "memory");
+    }
+}
+
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     head_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                const __grid_constant__ CUtensorMap tm_x2, const __grid_constant__ CUtensorMap tm_w2, const HeadParams p) {
+                const __grid_constant__ CUtensorMap tm_x2, const __grid_constant__ CUtensorMap tm_w2,
+                const __grid_constant__ CUtensorMap tm_out, const HeadParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem_raw);  // the even CTA's: both CTAs' tiles have landed
     uint64_t *empty = full + kMaxStages;                      // the slot's products are done
@@ -135,7 +193,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t *drained = acc_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    const uint32_t resident = (smem_u32(smem_raw) + kBarrierBytes + 1023u) & ~1023u;
+    const uint32_t staging = (smem_u32(smem_raw) + kBarrierBytes + 1023u) & ~1023u;
+    const uint32_t resident = staging + (p.staged ? 4 * kStageBytes : 0);
     const uint32_t ring = resident + p.resident_bytes;
     // a CTA's half of the positions and its table rows, per block
     const uint32_t x_bytes = (uint32_t)(p.tile_r / 2) * kBlockK, w_bytes = (uint32_t)p.rows_cta * kBlockK;
@@ -276,7 +335,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 4; ++i) sx_next[i] = t < p.tiles && r + 64 * i < p.R ? __ldg(p.x_scale + r + 64 * i) : 0.0f;
         };
         load_scales(pair);
-        int n = 0;
+        const bool sender = quarter == 0 && lane == 0;
+        int n = 0, buffer = 0;
         for (int64_t t = pair; t < p.tiles; t += pairs, ++n) {
             const int b = n & 1;
             const int v = (int)(t / p.r_tiles) * 2 * p.rows_cta + (int)rank * p.rows_cta + quarter * 32 + lane;
@@ -287,9 +347,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 4; ++i) sx[i] = sx_next[i];
             load_scales(t + pairs);
             ok = mbar_wait(smem_u32(&acc_full[b]), (uint32_t)(n >> 1) & 1, abort_flag);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            if (!half_vote(half, ok)) break;
             tc_fence_after();
             const uint32_t at = tmem_base + (uint32_t)b * 256u + ((uint32_t)(quarter * 32) << 16);
+            const int pitch = p.rows_cta * (int)sizeof(T), entry = quarter * 32 + lane, v0 = v - entry;
+            // (a tile that ends inside a 16-byte group is stored from registers: sent out, it wrote the whole group)
+            if (p.staged && (v0 + p.rows_cta <= p.V || (p.V * (int64_t)sizeof(T)) % 16 == 0)) {
+                if (v0 < p.V) {
+#pragma unroll 1
+                    for (int c = half * 32; c < p.tile_r && r0 + c < p.R; c += 64) {
+                        const float sc = c < 64 ? sx[0] : c < 128 ? sx[1] : c < 192 ? sx[2] : sx[3];
+#pragma unroll 1
+                        for (int k = 0; k < 32; k += kTokens<T>, buffer ^= 1) {
+                            const uint32_t to = staging + (uint32_t)(2 * half + buffer) * kStageBytes;
+                            // the tile sent from this buffer before has left it
+                            if (sender) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                            half_sync(half);
+#pragma unroll
+                            for (int q = 0; q < kTokens<T>; q += 16) {
+                                uint32_t acc[16];
+                                tmem_ld_32x32b_x16(at + c + k + q, acc);
+                                tmem_ld_wait();
+                                const int c0 = k + q;
+                                const float s16 = c0 ? __shfl_down_sync(0xffffffffu, sc, 16) : sc;
+                                if (quarter * 32 < p.rows_cta)  // (whole quarters: rows_cta is a multiple of 32)
+                                    put_logits(to + (uint32_t)(q * pitch), pitch, acc, entry, sw, s16, 0, T());
+                            }
+                            fence_proxy_async_smem();
+                            half_sync(half);
+                            if (sender && r0 + c + k < p.R) {
+                                asm volatile(
+                                    "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group.L2::cache_hint"
+                                    " [%0, {%2, %3}], [%1], %4;" ::"l"(&tm_out),
+                                    "r"(to), "r"(v0), "r"(r0 + c + k), "l"(policy)
+                                    : "memory");
+                            }
+                            if (sender) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                        }
+                    }
+                }
+            } else
 #pragma unroll 1
             for (int c = half * 32; live > 0 && c < p.tile_r && r0 + c < p.R; c += 64) {
                 uint32_t acc[32];
@@ -302,6 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(lead_empty + 8u * (uint32_t)b);
         }
+        if (sender) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
     __syncthreads();
@@ -398,7 +496,8 @@ cudaError_t launch_head_e4m3(const uint8_t *X, int64_t ldx, const float *x_scale
     const int x_slot = kSlotBlocks * (p.tile_r / 2) * kBlockK, slack = (kRowsCta - p.rows_cta) * kBlockK;
     p.resident_bytes = p.r_tiles == 1 && slots <= kResidentBytes / x_slot ? slots * x_slot : 0;
     p.stage_bytes = kSlotBlocks * p.rows_cta * kBlockK + (p.resident_bytes ? 0 : x_slot);
-    const int fixed = kBarrierBytes + 1024 + p.resident_bytes + slack;
+    p.staged = R > kFewPositions;
+    const int fixed = kBarrierBytes + 1024 + (p.staged ? 4 * kStageBytes : 0) + p.resident_bytes + slack;
     p.stages = std::min(kMaxStages, (kSmemLimit - fixed) / p.stage_bytes);
     p.idesc = idesc_e4m3_f32(kTileV, p.tile_r);
     p.stream_table = p.r_tiles == 1;
@@ -413,14 +512,27 @@ cudaError_t launch_head_e4m3(const uint8_t *X, int64_t ldx, const float *x_scale
         *msg = "a tensor map of the head's codes could not be encoded";
         return cudaErrorInvalidValue;
     }
+    CUtensorMap tm_out = tm_x;  // (not used without staging)
+    if (p.staged) {
+        const cuuint64_t dims[2] = {(cuuint64_t)V, (cuuint64_t)R}, strides[1] = {(cuuint64_t)ldl * entry_size(dtype)};
+        const cuuint32_t boxes[2] = {(cuuint32_t)p.rows_cta,
+                                     (cuuint32_t)(dtype == DG_BF16 ? kTokens<__nv_bfloat16> : kTokens<float>)};
+        const cuuint32_t estr[2] = {1, 1};
+        if (encode(&tm_out, dtype == DG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, logits,
+                   dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                   CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+            *msg = "a tensor map of the head's logits could not be encoded";
+            return cudaErrorInvalidValue;
+        }
+    }
     const cudaError_t e = ensure_head_attributes();
     if (e != cudaSuccess) return e;
     const unsigned grid = 2 * (unsigned)std::min(p.tiles, pairs);
     const int smem = fixed + p.stages * p.stage_bytes;
     if (dtype == DG_BF16)
-        head_kernel<__nv_bfloat16><<<grid, kThreads, smem, stream>>>(tm_x, tm_w, tm_x2, tm_w2, p);
+        head_kernel<__nv_bfloat16><<<grid, kThreads, smem, stream>>>(tm_x, tm_w, tm_x2, tm_w2, tm_out, p);
     else
-        head_kernel<float><<<grid, kThreads, smem, stream>>>(tm_x, tm_w, tm_x2, tm_w2, p);
+        head_kernel<float><<<grid, kThreads, smem, stream>>>(tm_x, tm_w, tm_x2, tm_w2, tm_out, p);
     return cudaGetLastError();
 }
 
