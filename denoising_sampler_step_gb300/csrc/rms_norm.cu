@@ -39,7 +39,7 @@ constexpr int kRingTail = 32;                 // columns where fewer are left
 constexpr int kSmemPerSm = 224 * 1024, kSmemLimit = 232448 - 1024;  // of an SM's CTAs, and of one
 
 // Threads that work on a row at most, by the eights of columns that each takes.
-__host__ __device__ constexpr int max_threads(int n) { return n == 8 ? 512 : 256; }
+__host__ __device__ constexpr int max_threads(int n) { return n == 1 || n == 8 ? 512 : 256; }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -572,10 +572,14 @@ __global__ void __launch_bounds__(kWeightThreads) norm_weight_kernel(const float
 
 int row_threads(int64_t d, int n) { return (int)((((d + 7) / 8 + n - 1) / n + 31) / 32 * 32); }
 
-// Eights of columns per thread: two where that leaves four warps, whose instructions per row are then fewer.
-int eights_per_thread(int64_t d) {
+// Eights of columns per thread.  Many rows: two where that leaves four warps, whose instructions per row are then fewer
+// (8,192 x 2,816, gradient: 34 us against 42).  Few rows to an SM: one, for a row's time (one row of 2,816: 2.5 us
+// against 3.0).
+constexpr int kFewRowsPerSm = 32;
+int eights_per_thread(int64_t d, int64_t R) {
     const int64_t eights = (d + 7) / 8;
-    return eights <= 128 ? 1 : eights <= 2 * max_threads(2) ? 2 : eights <= 4 * max_threads(4) ? 4 : 8;
+    const bool few = R <= kFewRowsPerSm * (int64_t)std::max(1, device_sm_count());
+    return eights <= (few ? max_threads(1) : 128) ? 1 : eights <= 2 * max_threads(2) ? 2 : eights <= 4 * max_threads(4) ? 4 : 8;
 }
 
 // A launch: CTAs of a row each, as many as the SMs hold, the shared memory left to each as its ring.
@@ -597,7 +601,7 @@ Plan make_plan(Source *src, int64_t R, int64_t d, bool wide) {
         ring = ring && wide_rows(src->m[q]);
     }
     plan.ring = ring && src->stage_bytes <= kSmemLimit - kRingFixed;
-    plan.n = plan.ring ? eights_per_thread(d) : (d + 7) / 8 <= max_threads(1) ? 1 : 8;
+    plan.n = plan.ring ? eights_per_thread(d, R) : (d + 7) / 8 <= max_threads(1) ? 1 : 8;
     plan.threads = row_threads(d, plan.n);
     const int64_t sms = std::max(1, device_sm_count());
     plan.grid = (unsigned)std::min<int64_t>(R, sms * std::min(kMaxCtas, 2048 / plan.threads));
