@@ -180,19 +180,6 @@ __device__ __forceinline__ void load8(Any8 &r, const void *p, bool f32, int64_t 
         r.a = t.a;
     }
 }
-// The same from shared memory, 16-byte aligned.
-__device__ __forceinline__ void read8(float (&v)[8], const uint8_t *row, bool f32, int at) {
-    if (f32) {
-        const float4 a = *reinterpret_cast<const float4 *>(row + 4 * at), b = *reinterpret_cast<const float4 *>(row + 4 * at + 16);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-        const uint4 a = *reinterpret_cast<const uint4 *>(row + 2 * at);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[2 * j] = bf16_low(w[j]), v[2 * j + 1] = bf16_high(w[j]);
-    }
-}
 __device__ __forceinline__ void unpack8(float (&v)[8], const Any8 &r, bool f32) {
     const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
     if (f32) {
@@ -226,7 +213,7 @@ struct EmbedRows {
     bool accumulate;  // backward: add to the gradient that is there
 };
 cudaError_t launch_token_embed(const EmbedRows &a, cudaStream_t stream);
-size_t token_embed_backward_bytes(int64_t R, int64_t rows, int64_t d);
+size_t token_embed_backward_bytes(int64_t R, int64_t d);
 cudaError_t launch_token_embed_backward(const EmbedRows &a, void *workspace, cudaStream_t stream);
 
 constexpr int64_t kMaxNormWidth = 32768;

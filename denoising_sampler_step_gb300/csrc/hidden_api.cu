@@ -135,7 +135,7 @@ dg_status dg_token_embed(const void *table, int32_t dtype, const float *scale, i
 
 size_t dg_token_embed_backward_workspace_size(int64_t R, int64_t vocab_len, int64_t d) {
     if (R < 1 || R > kMaxRows || vocab_len < 0 || vocab_len > kMaxVocab || d < 1 || d >= kMaxWidth) return 0;
-    return token_embed_backward_bytes(R, vocab_len, d);
+    return token_embed_backward_bytes(R, d);
 }
 
 dg_status dg_token_embed_backward(const void *grad, int32_t dtype, int64_t R, int64_t d, int64_t ldg,
@@ -153,7 +153,7 @@ dg_status dg_token_embed_backward(const void *grad, int32_t dtype, int64_t R, in
     if (rows == 0 || (R == 0 && a.accumulate)) return DG_OK;
     DG_TRY(check_vectors(what, {token}));
     if (R > 0) {
-        DG_TRY(check_workspace(what, workspace, workspace_bytes, token_embed_backward_bytes(R, rows, d)));
+        DG_TRY(check_workspace(what, workspace, workspace_bytes, token_embed_backward_bytes(R, d)));
         const Span t = span(a.table, rows, d), w = span(workspace, (int64_t)workspace_bytes);
         if (meet(t, span(a.rows, R, d))) return overlap(what, "grad_table", "grad");
         if (meet(t, span(token, 4 * R))) return overlap(what, "grad_table", "token");

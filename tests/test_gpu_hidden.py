@@ -172,7 +172,7 @@ def test_a_table_past_32_bits(B):
 
 @pytest.mark.parametrize("kind", ["uniform", "one", "masked", "distinct", "runs", "padded"])
 @pytest.mark.parametrize("R,V,d", [(1, 5, 8), (9, 4, 1), (64, 70, 257), (300, 40, 33), (2047, 3000, 40), (2049, 300, 8),
-                                   (8200, 20000, 16), (33000, 600, 9)])
+                                   (8200, 20000, 16), (33000, 600, 9), (70001, 70000, 3)])
 def test_gradient(B, R, V, d, kind):
     rng = np.random.default_rng(R)
     dt, tt = ("f32", "bf16") if R % 2 else ("bf16", "f32")
