@@ -55,24 +55,24 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// The first n of eight entries at q; the others hold anything (kWide) or zeros.  kWide: q starts where rows may
-// (wide_rows), and whole 16-byte groups (E4M3: 8) that hold an entry are read, without a branch: a choice between
+// Eight entries at q, those from n on anything (kWide) or zeros.  Without kWide they lie `step` apart, so that
+// neighbouring threads read neighbouring entries.  kWide: q starts where rows may (wide_rows), and whole 16-byte groups (E4M3: 8) that hold an entry are read, without a branch: a choice between
 // kinds of loads at run time, or a branch on n, kept rows from being in flight side by side.
 template <bool kWide>
-__device__ __forceinline__ void load8(Raw8<float> &r, const float *q, int n) {
+__device__ __forceinline__ void load8(Raw8<float> &r, const float *q, int n, int step = 1) {
     if constexpr (kWide) {
         r.a = *reinterpret_cast<const float4 *>(q);
         r.b = n > 4 ? *reinterpret_cast<const float4 *>(q + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
     } else {
         float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < n ? q[j] : 0.0f;
+        for (int j = 0; j < 8; ++j) v[j] = j * step < n ? q[j * step] : 0.0f;
         r.a = make_float4(v[0], v[1], v[2], v[3]);
         r.b = make_float4(v[4], v[5], v[6], v[7]);
     }
 }
 template <bool kWide>
-__device__ __forceinline__ void load8(Raw8<__nv_bfloat16> &r, const __nv_bfloat16 *q, int n) {
+__device__ __forceinline__ void load8(Raw8<__nv_bfloat16> &r, const __nv_bfloat16 *q, int n, int step = 1) {
     if constexpr (kWide) {
         r.a = *reinterpret_cast<const uint4 *>(q);
     } else {
@@ -80,19 +80,20 @@ __device__ __forceinline__ void load8(Raw8<__nv_bfloat16> &r, const __nv_bfloat1
         const uint16_t *u = reinterpret_cast<const uint16_t *>(q);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            w[j] = (2 * j < n ? (uint32_t)u[2 * j] : 0u) | (2 * j + 1 < n ? (uint32_t)u[2 * j + 1] << 16 : 0u);
+            w[j] = (2 * j * step < n ? (uint32_t)u[2 * j * step] : 0u) |
+                   ((2 * j + 1) * step < n ? (uint32_t)u[(2 * j + 1) * step] << 16 : 0u);
         r.a = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 template <bool kWide>
-__device__ __forceinline__ void load8(Raw8<E4m3> &r, const E4m3 *q, int n) {
+__device__ __forceinline__ void load8(Raw8<E4m3> &r, const E4m3 *q, int n, int step = 1) {
     if constexpr (kWide) {
         r.a = *reinterpret_cast<const uint2 *>(q);
     } else {
         uint32_t w[2] = {0u, 0u};
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (j < n) w[j >> 2] |= (uint32_t)q[j].code << (8 * (j & 3));
+            if (j * step < n) w[j >> 2] |= (uint32_t)q[j * step].code << (8 * (j & 3));
         r.a = make_uint2(w[0], w[1]);
     }
 }
@@ -120,15 +121,15 @@ __device__ __forceinline__ void unpack8(float (&v)[8], const Raw8<E4m3> &r) {
 }
 
 // Zeros in place of the values from n on.
-__device__ __forceinline__ void mask8(float (&v)[8], int n) {
-    if (n < 8)
+__device__ __forceinline__ void mask8(float (&v)[8], int n, int step = 1) {
+    if (n <= 7 * step)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < n ? v[j] : 0.0f;
+        for (int j = 0; j < 8; ++j) v[j] = j * step < n ? v[j] : 0.0f;
 }
 
 // The first n of eight values, each rounded once.
 template <bool kWide>
-__device__ __forceinline__ void store8(float *q, const float (&v)[8], int n) {
+__device__ __forceinline__ void store8(float *q, const float (&v)[8], int n, int step = 1) {
     if (kWide && n >= 8) {
         *reinterpret_cast<float4 *>(q) = make_float4(v[0], v[1], v[2], v[3]);
         *reinterpret_cast<float4 *>(q + 4) = make_float4(v[4], v[5], v[6], v[7]);
@@ -136,10 +137,10 @@ __device__ __forceinline__ void store8(float *q, const float (&v)[8], int n) {
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        if (j < n) q[j] = v[j];
+        if (j * step < n) q[j * step] = v[j];
 }
 template <bool kWide>
-__device__ __forceinline__ void store8(__nv_bfloat16 *q, const float (&v)[8], int n) {
+__device__ __forceinline__ void store8(__nv_bfloat16 *q, const float (&v)[8], int n, int step = 1) {
     const uint4 w = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
     if (kWide && n >= 8) {
         *reinterpret_cast<uint4 *>(q) = w;
@@ -148,10 +149,10 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *q, const float (&v)[8], in
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        if (j < n) reinterpret_cast<uint16_t *>(q)[j] = (uint16_t)(u[j >> 1] >> (16 * (j & 1)));
+        if (j * step < n) reinterpret_cast<uint16_t *>(q)[j * step] = (uint16_t)(u[j >> 1] >> (16 * (j & 1)));
 }
 template <bool kWide>
-__device__ __forceinline__ void store8(E4m3 *q, const float (&v)[8], int n) {
+__device__ __forceinline__ void store8(E4m3 *q, const float (&v)[8], int n, int step = 1) {
     const uint2 w = make_uint2(pack_e4m3x2(v[0], v[1]) | pack_e4m3x2(v[2], v[3]) << 16,
                                pack_e4m3x2(v[4], v[5]) | pack_e4m3x2(v[6], v[7]) << 16);
     if (kWide && n >= 8) {
@@ -161,22 +162,22 @@ __device__ __forceinline__ void store8(E4m3 *q, const float (&v)[8], int n) {
     const uint32_t u[2] = {w.x, w.y};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        if (j < n) q[j].code = (uint8_t)(u[j >> 2] >> (8 * (j & 3)));
+        if (j * step < n) q[j * step].code = (uint8_t)(u[j >> 2] >> (8 * (j & 3)));
 }
 
 // Eight entries of a type known at run time only, fp32 or not (bf16).
 struct Any8 {
     uint4 a, b;
 };
-__device__ __forceinline__ void load8(Any8 &r, const void *p, bool f32, int64_t at, int n) {
+__device__ __forceinline__ void load8(Any8 &r, const void *p, bool f32, int64_t at, int n, int step) {
     if (f32) {
         Raw8<float> t;
-        load8<false>(t, static_cast<const float *>(p) + at, n);
+        load8<false>(t, static_cast<const float *>(p) + at, n, step);
         r.a = *reinterpret_cast<const uint4 *>(&t.a);
         r.b = *reinterpret_cast<const uint4 *>(&t.b);
     } else {
         Raw8<__nv_bfloat16> t;
-        load8<false>(t, static_cast<const __nv_bfloat16 *>(p) + at, n);
+        load8<false>(t, static_cast<const __nv_bfloat16 *>(p) + at, n, step);
         r.a = t.a;
     }
 }
@@ -191,11 +192,11 @@ __device__ __forceinline__ void unpack8(float (&v)[8], const Any8 &r, bool f32) 
     }
 }
 template <bool kWide>
-__device__ __forceinline__ void store8(void *p, bool f32, int64_t at, const float (&v)[8], int n) {
+__device__ __forceinline__ void store8(void *p, bool f32, int64_t at, const float (&v)[8], int n, int step = 1) {
     if (f32)
-        store8<kWide>(static_cast<float *>(p) + at, v, n);
+        store8<kWide>(static_cast<float *>(p) + at, v, n, step);
     else
-        store8<kWide>(static_cast<__nv_bfloat16 *>(p) + at, v, n);
+        store8<kWide>(static_cast<__nv_bfloat16 *>(p) + at, v, n, step);
 }
 
 }  // namespace hidden

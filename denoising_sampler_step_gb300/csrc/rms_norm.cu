@@ -169,6 +169,19 @@ struct Columns {
     }
 };
 
+// The same where rows are read element by element: eight columns `step` apart, neighbouring threads' side by side.
+template <int N>
+struct Strided {
+    int at[N], n[N], step;
+    __device__ __forceinline__ Strided(int width, int threads) : step(threads) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            at[i] = threadIdx.x + i * 8 * threads;
+            n[i] = width - at[i];
+        }
+    }
+};
+
 // Eight columns as pairs, those from n on as zeros.
 __device__ __forceinline__ void mask4(f32x2 (&v)[4], int n) {
     if (n < 8)
@@ -199,25 +212,25 @@ __device__ __forceinline__ void singles(float (&v)[8], const f32x2 (&p)[4]) {
 }
 
 // offset + weight in these columns (ones without a weight), zeros past the row's end.
-__device__ __forceinline__ void load_weight(float (&w)[8], const void *weight, int dtype, float offset, int at, int n, int width) {
+__device__ __forceinline__ void load_weight(float (&w)[8], const void *weight, int dtype, float offset, int at, int n, int step) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] = 1.0f;
     if (weight) {
         Any8 raw;
-        load8(raw, weight, dtype == DG_F32, at, width - at);
+        load8(raw, weight, dtype == DG_F32, at, n, step);
         unpack8(w, raw, dtype == DG_F32);
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[j] += offset;
     }
-    mask8(w, n);
+    mask8(w, n, step);
 }
 template <int N>
 __device__ __forceinline__ void load_weight(f32x2 (&w)[N][4], const void *weight, int dtype, float offset,
-                                            const Columns<N> &col, int width) {
+                                            const Columns<N> &col) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         float v[8];
-        load_weight(v, weight, dtype, offset, col.read[i], col.n[i], width);
+        load_weight(v, weight, dtype, offset, col.at[i], col.n[i], 1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[i][j] = pair(v[2 * j], v[2 * j + 1]);
     }
@@ -267,7 +280,7 @@ __global__ void __launch_bounds__(max_threads(N) + 32) rms_norm_kernel(const Nor
     const float inv_d = 1.0f / (float)d;
     const bool out32 = a.out.dtype == DG_F32;
     f32x2 w[N][4];
-    load_weight(w, a.weight, a.weight_dtype, a.weight_offset, col, d);
+    load_weight(w, a.weight, a.weight_dtype, a.weight_offset, col);
     int turn = 0;
     for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x, turn ^= 1) {
         f32x2 v[N][4], sq = 0;
@@ -342,7 +355,7 @@ __global__ void __launch_bounds__(max_threads(N)) rms_norm_plain_kernel(const No
     __shared__ uint32_t maxima[2][32];
     const NormRows &a = p.a;
     const int d = (int)a.d, threads = blockDim.x;
-    const Columns<N> col(d, threads);
+    const Strided<N> col(d, threads);
     const bool codes = a.out.dtype == DG_E4M3;
     int turn = 0;
     for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x, turn ^= 1) {
@@ -350,16 +363,16 @@ __global__ void __launch_bounds__(max_threads(N)) rms_norm_plain_kernel(const No
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             Any8 raw;
-            load8(raw, a.x.p, a.x.dtype == DG_F32, r * a.x.ld + col.read[i], d - col.read[i]);
+            load8(raw, a.x.p, a.x.dtype == DG_F32, r * a.x.ld + col.at[i], col.n[i], col.step);
             unpack8(v[i], raw, a.x.dtype == DG_F32);
             if (a.residual.p) {
                 float t[8];
-                load8(raw, a.residual.p, a.residual.dtype == DG_F32, r * a.residual.ld + col.read[i], d - col.read[i]);
+                load8(raw, a.residual.p, a.residual.dtype == DG_F32, r * a.residual.ld + col.at[i], col.n[i], col.step);
                 unpack8(t, raw, a.residual.dtype == DG_F32);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] += t[j];
             }
-            mask8(v[i], col.n[i]);
+            mask8(v[i], col.n[i], col.step);
             float q = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) q = fmaf(v[i][j], v[i][j], q);
@@ -371,9 +384,9 @@ __global__ void __launch_bounds__(max_threads(N)) rms_norm_plain_kernel(const No
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             if (a.hidden.p && col.n[i] > 0)
-                store8<false>(a.hidden.p, a.hidden.dtype == DG_F32, r * a.hidden.ld + col.at[i], v[i], col.n[i]);
+                store8<false>(a.hidden.p, a.hidden.dtype == DG_F32, r * a.hidden.ld + col.at[i], v[i], col.n[i], col.step);
             float w[8];
-            load_weight(w, a.weight, a.weight_dtype, a.weight_offset, col.read[i], col.n[i], d);
+            load_weight(w, a.weight, a.weight_dtype, a.weight_offset, col.at[i], col.n[i], col.step);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 v[i][j] = v[i][j] * rstd * w[j];
@@ -390,9 +403,9 @@ __global__ void __launch_bounds__(max_threads(N)) rms_norm_plain_kernel(const No
             if (col.n[i] <= 0) continue;
             if (codes) {
                 to_codes(v[i], scale);
-                store8<false>(static_cast<E4m3 *>(a.out.p) + r * a.out.ld + col.at[i], v[i], col.n[i]);
+                store8<false>(static_cast<E4m3 *>(a.out.p) + r * a.out.ld + col.at[i], v[i], col.n[i], col.step);
             } else {
-                store8<false>(a.out.p, a.out.dtype == DG_F32, r * a.out.ld + col.at[i], v[i], col.n[i]);
+                store8<false>(a.out.p, a.out.dtype == DG_F32, r * a.out.ld + col.at[i], v[i], col.n[i], col.step);
             }
         }
     }
@@ -424,7 +437,7 @@ __global__ void __launch_bounds__(max_threads(N) + 32) rms_norm_backward_kernel(
     const Columns<N> col(d, threads);
     const float inv_d = 1.0f / (float)d;
     f32x2 w[N][4], dw[N][4];
-    load_weight(w, a.weight, a.weight_dtype, a.weight_offset, col, d);
+    load_weight(w, a.weight, a.weight_dtype, a.weight_offset, col);
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
@@ -486,7 +499,7 @@ __global__ void __launch_bounds__(max_threads(N)) rms_norm_backward_plain_kernel
     __shared__ float sums[2][32];
     const NormBackRows &a = p.a;
     const int d = (int)a.d, threads = blockDim.x;
-    const Columns<N> col(d, threads);
+    const Strided<N> col(d, threads);
     float dw[N][8];
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -500,13 +513,13 @@ __global__ void __launch_bounds__(max_threads(N)) rms_norm_backward_plain_kernel
         for (int i = 0; i < N; ++i) {
             float w[8], q = 0.0f;
             Any8 raw;
-            load_weight(w, a.weight, a.weight_dtype, a.weight_offset, col.read[i], col.n[i], d);
-            load8(raw, a.grad.p, a.grad.dtype == DG_F32, r * a.grad.ld + col.read[i], d - col.read[i]);
+            load_weight(w, a.weight, a.weight_dtype, a.weight_offset, col.at[i], col.n[i], col.step);
+            load8(raw, a.grad.p, a.grad.dtype == DG_F32, r * a.grad.ld + col.at[i], col.n[i], col.step);
             unpack8(g[i], raw, a.grad.dtype == DG_F32);
-            load8(raw, a.hidden.p, a.hidden.dtype == DG_F32, r * a.hidden.ld + col.read[i], d - col.read[i]);
+            load8(raw, a.hidden.p, a.hidden.dtype == DG_F32, r * a.hidden.ld + col.at[i], col.n[i], col.step);
             unpack8(xh[i], raw, a.hidden.dtype == DG_F32);
-            mask8(g[i], col.n[i]);
-            mask8(xh[i], col.n[i]);
+            
+            
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 xh[i][j] *= rstd;
@@ -525,18 +538,18 @@ __global__ void __launch_bounds__(max_threads(N)) rms_norm_backward_plain_kernel
             for (int j = 0; j < 8; ++j) up[j] = 0.0f;
             if (a.grad_hidden.p) {
                 Any8 raw;
-                load8(raw, a.grad_hidden.p, a.grad_hidden.dtype == DG_F32, r * a.grad_hidden.ld + col.at[i], col.n[i]);
+                load8(raw, a.grad_hidden.p, a.grad_hidden.dtype == DG_F32, r * a.grad_hidden.ld + col.at[i], col.n[i], col.step);
                 unpack8(up, raw, a.grad_hidden.dtype == DG_F32);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) g[i][j] = rstd * fmaf(-mean, xh[i][j], g[i][j]) + up[j];
-            store8<false>(a.grad_x.p, a.grad_x.dtype == DG_F32, r * a.grad_x.ld + col.at[i], g[i], col.n[i]);
+            store8<false>(a.grad_x.p, a.grad_x.dtype == DG_F32, r * a.grad_x.ld + col.at[i], g[i], col.n[i], col.step);
         }
     }
     if (a.grad_weight)
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (col.n[i] > 0) store8<true>(p.parts + blockIdx.x * p.part_ld + col.at[i], dw[i], 8);
+            if (col.n[i] > 0) store8<false>(p.parts + blockIdx.x * p.part_ld + col.at[i], dw[i], col.n[i], col.step);
 }
 
 // dweight from the CTAs' parts, 32 columns a CTA: a warp reads four parts at a time, eight lanes each.

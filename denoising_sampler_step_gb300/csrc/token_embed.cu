@@ -56,13 +56,14 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
         const TT *src = static_cast<const TT *>(a.table.p) + (on ? (t - a.vocab_start) * a.table.ld : 0);
         const float f = on && a.scale ? a.scale[t - a.vocab_start] : 1.0f;
         TO *dst = static_cast<TO *>(a.rows.p) + r * a.rows.ld;
-        for (int c0 = 8 * lane; c0 < d; c0 += kAhead * 8 * p.lanes) {
+        const int step = kWide ? 1 : p.lanes;  // between a thread's eight columns
+        for (int c0 = kWide ? 8 * lane : lane; c0 < d; c0 += kAhead * 8 * p.lanes) {
             Raw8<TT> raw[kAhead];
             if (on)
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {  // (past the row's end its last columns again)
-                    const int c = min(c0 + i * 8 * p.lanes, last);
-                    load8<kWide>(raw[i], src + c, d - c);
+                    const int c = kWide ? min(c0 + i * 8 * p.lanes, last) : c0 + i * 8 * p.lanes;
+                    load8<kWide>(raw[i], src + c, d - c, step);
                 }
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
@@ -77,7 +78,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = 0.0f;
                 }
-                store8<kWide>(dst + c, v, d - c);
+                store8<kWide>(dst + c, v, d - c, step);
             }
         }
     }
@@ -531,9 +532,10 @@ __device__ __forceinline__ UnitRange unit_range(const Key &key, int u0, int u1, 
     return r;
 }
 
-// gW[key][c ..] (+)= gamma sum; old: what is there, with accumulate
+// gW[key][c ..] (+)= gamma sum; old: what is there, with accumulate; step: between the eight columns without kWide
 template <typename TT, bool kAdd, bool kWide>
-__device__ __forceinline__ void write_row(const EmbedRows &a, int32_t key, int c, const float (&sum)[8], const Raw8<TT> &old) {
+__device__ __forceinline__ void write_row(const EmbedRows &a, int32_t key, int c, int step, const float (&sum)[8],
+                                          const Raw8<TT> &old) {
     float v[8];
     if constexpr (kAdd) {
         unpack8(v, old);
@@ -543,7 +545,7 @@ __device__ __forceinline__ void write_row(const EmbedRows &a, int32_t key, int c
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = sum[j] * a.gamma;
     }
-    store8<kWide>(static_cast<TT *>(a.table.p) + (int64_t)key * a.table.ld + c, v, (int)a.d - c);
+    store8<kWide>(static_cast<TT *>(a.table.p) + (int64_t)key * a.table.ld + c, v, (int)a.d - c, step);
 }
 
 // Sums the positions [r.lo, r.hi) of a unit in eight columns from c on: each token's to its row, parts to part(slot).
@@ -551,7 +553,7 @@ __device__ __forceinline__ void write_row(const EmbedRows &a, int32_t key, int c
 // one token's positions come from L1 but once), without a branch between the loads.
 template <int kAhead, typename TG, typename TT, bool kAdd, bool kWide, typename Key, typename Pos, typename Part>
 __device__ __forceinline__ void sum_unit(const EmbedRows &a, const Key &key, const Pos &pos, const Part &part, const UnitRange &r,
-                                         int u0, int c) {
+                                         int u0, int c, int step) {
     const int n = (int)a.d - c;
     const TG *g = static_cast<const TG *>(a.rows.p) + c;
     const TT *table = static_cast<const TT *>(a.table.p) + c;
@@ -567,8 +569,8 @@ __device__ __forceinline__ void sum_unit(const EmbedRows &a, const Key &key, con
         for (int j = 0; j <= kAhead; ++j) k[j] = i + j < r.hi ? key(i + j) : -1;
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            load8<kWide>(raw[j], g + (int64_t)pos(min(i + j, r.hi - 1)) * a.rows.ld, n);
-            if constexpr (kAdd) load8<kWide>(old[j], table + (int64_t)max(k[j], 0) * a.table.ld, n);
+            load8<kWide>(raw[j], g + (int64_t)pos(min(i + j, r.hi - 1)) * a.rows.ld, n, step);
+            if constexpr (kAdd) load8<kWide>(old[j], table + (int64_t)max(k[j], 0) * a.table.ld, n, step);
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
@@ -582,7 +584,7 @@ __device__ __forceinline__ void sum_unit(const EmbedRows &a, const Key &key, con
                 else if (r.part1 && i + j + 1 == r.hi)
                     part(1, acc);
                 else
-                    write_row<TT, kAdd, kWide>(a, k[j], c, acc, old[j]);
+                    write_row<TT, kAdd, kWide>(a, k[j], c, step, acc, old[j]);
 #pragma unroll
                 for (int t = 0; t < 8; ++t) acc[t] = 0.0f;
             }
@@ -611,11 +613,11 @@ __global__ void __launch_bounds__(32 * kSumWarps) sum_rows_kernel(const SumParam
     const UnitRange r = unit_range(key, u0, u1, U, p.none, lane);
     if (r.lo >= r.hi) return;
     if (r.part1 && slab0 == 0 && lane == 0) p.s.list[atomicAdd(p.s.count, 1)] = make_int2(m, key(u1 - 1));
-    const int c = slab0 * 256 + 8 * lane;
+    const int c = slab0 * 256 + (kWide ? 8 : 1) * lane, step = kWide ? 1 : 32;
     if (c < a.d)
         sum_unit<kSumAhead, TG, TT, kAdd, kWide>(a, key, pos, [&](int slot, const float (&acc)[8]) {
-            store8<true>(p.s.parts + ((int64_t)m * 2 + slot) * p.s.part_ld + c, acc, 8);
-        }, r, u0, c);
+            store8<kWide>(p.s.parts + ((int64_t)m * 2 + slot) * p.s.part_ld + c, acc, kWide ? 8 : (int)a.d - c, step);
+        }, r, u0, c, step);
 }
 
 constexpr int kJoinWarps = 8;
@@ -665,7 +667,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_parts_kernel(const SumPa
                 Raw8<TT> old;
                 if constexpr (kAdd)
                     load8<kWide>(old, static_cast<const TT *>(a.table.p) + (int64_t)e.y * a.table.ld + c8, (int)a.d - c8);
-                write_row<TT, kAdd, kWide>(a, e.y, c8, v, old);
+                write_row<TT, kAdd, kWide>(a, e.y, c8, 1, v, old);
             }
         }
         __syncthreads();
@@ -692,7 +694,8 @@ __global__ void __launch_bounds__(kSortThreads) few_rows_kernel(const SumParams 
     auto key = [&](int i) { return i >= 0 && i < R ? key_s[i] : -1; };
     auto pos = [&](int i) { return pos_s[i]; };
     const int quad = threadIdx.x / kFewLanes, sub = threadIdx.x % kFewLanes;
-    const int c = (int)blockIdx.x * kFewCols + 8 * sub;
+    const int at = (kWide ? 8 : 1) * sub, step = kWide ? 1 : kFewLanes;  // of the CTA's columns, this thread's eight
+    const int c = (int)blockIdx.x * kFewCols + at;
     const int units = (R + U - 1) / U;
     // (a warp holds eight units: their ranges one after another, each by all lanes)
     UnitRange r{0, 0, false, false};
@@ -706,8 +709,8 @@ __global__ void __launch_bounds__(kSortThreads) few_rows_kernel(const SumParams 
     const bool on = quad < units && c < a.d;
     if (on && r.lo < r.hi)
         sum_unit<4, TG, TT, kAdd, kWide>(a, key, pos, [&](int slot, const float (&acc)[8]) {
-            store8<true>(&parts[quad][slot][8 * sub], acc, 8);
-        }, r, quad * U, c);
+            store8<kWide>(&parts[quad][slot][at], acc, kFewCols - at, step);
+        }, r, quad * U, c, step);
     __syncthreads();
     // tokens that left parts: their unit's second, then the first ones of those after it, by all of the warp
     uint32_t longs = __ballot_sync(0xffffffffu, quad < units && r.part1 && sub == 0);
@@ -717,11 +720,11 @@ __global__ void __launch_bounds__(kSortThreads) few_rows_kernel(const SumParams 
         const int32_t k = key_s[owner * U + U - 1];
         float acc[8];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) acc[t] = lane < kFewLanes ? parts[owner][1][8 * sub + t] : 0.0f;
+        for (int t = 0; t < 8; ++t) acc[t] = lane < kFewLanes ? parts[owner][1][at + t * step] : 0.0f;
         for (int m = owner + 1 + lane / kFewLanes; m < units && key_s[m * U] == k; m += 32 / kFewLanes) {
             Raw8<float> raw;
             float v[8];
-            load8<true>(raw, &parts[m][0][8 * sub], 8);
+            load8<kWide>(raw, &parts[m][0][at], kFewCols - at, step);
             unpack8(v, raw);
 #pragma unroll
             for (int t = 0; t < 8; ++t) acc[t] += v[t];
@@ -733,20 +736,20 @@ __global__ void __launch_bounds__(kSortThreads) few_rows_kernel(const SumParams 
         if (lane < kFewLanes && c < a.d) {
             Raw8<TT> old;
             if constexpr (kAdd)
-                load8<kWide>(old, static_cast<const TT *>(a.table.p) + (int64_t)k * a.table.ld + c, (int)a.d - c);
-            write_row<TT, kAdd, kWide>(a, k, c, acc, old);
+                load8<kWide>(old, static_cast<const TT *>(a.table.p) + (int64_t)k * a.table.ld + c, (int)a.d - c, step);
+            write_row<TT, kAdd, kWide>(a, k, c, step, acc, old);
         }
     }
 }
 
 template <typename TT, bool kWide>
 __global__ void __launch_bounds__(256) clear_rows_kernel(const EmbedRows a, int64_t rows) {
-    const int d = (int)a.d, eights = (d + 7) / 8;
+    const int d = (int)a.d, lane = threadIdx.x & 31;
     const float zero[8] = {};
     grid_launch_dependents();  // the order of the tokens is found meanwhile
     for (int64_t v = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); v < rows; v += (int64_t)gridDim.x * 8)
-        for (int c = threadIdx.x & 31; c < eights; c += 32)
-            store8<kWide>(static_cast<TT *>(a.table.p) + v * a.table.ld + 8 * c, zero, d - 8 * c);
+        for (int c = (kWide ? 8 : 1) * lane; c < d; c += 256)
+            store8<kWide>(static_cast<TT *>(a.table.p) + v * a.table.ld + c, zero, d - c, kWide ? 1 : 32);
 }
 
 // ---------------------------------------------------------------- plan
