@@ -3,13 +3,16 @@
 //
 // The vocabulary is the M side of the product and the positions its N side: a tcgen05 CTA pair
 // (cta_group::2) multiplies 256 vocabulary rows (128 in each CTA) by up to 256 positions (half of them
-// in each CTA's shared memory), K = 32 per instruction, 128 per ring slot.  So a single position costs
+// in each CTA's shared memory), K = 32 per instruction, 256 codes per ring slot.  So a single position costs
 // an N of 32, a table row is read once per 256 positions, and the accumulator's lanes are consecutive
-// vocabulary entries: a warp stores 32 of them per position straight from its registers.  The pairs are
-// persistent: two accumulators in TMEM (2 x 256 columns) let the stores of one tile run under the next
-// tile's product.
+// vocabulary entries.  The pairs are persistent: two accumulators in TMEM (2 x 256 columns) let the stores
+// of one tile run under the next tile's product.  Where one tile takes all positions, their codes stay in
+// shared memory; the table's rows per tile are then as many as make the rounds of tiles even.
 //
-// Bound by HBM up to some 300 positions (table + logits), by the E4M3 MMA rate above.
+// Bound by HBM up to some 300 positions (table + logits), by the E4M3 MMA rate above.  V = 262,144,
+// d = 2,816: 1 position 111 us (6.7 TB/s), 256 with fp32 logits 163 us (6.2 TB/s), with bf16 ones 151 us; 2,048 with
+// bf16 ones 870 us (3.48 PFLOP/s) for a call by itself, 1,030 us in a row of calls, where the chip's power limit
+// lowers the clock.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -139,7 +142,8 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&v)
 // Logits through shared memory: a half of the epilogue (four warps, a lane quarter each) gathers kTokens positions of
 // all the tile's table rows, [position][table row], which one thread sends out as one tile; rows and columns past the
 // matrix are cut off there.  So a position's logits leave as one piece of 256 or 512 bytes, where a warp's own stores
-// were pieces of 64 or 128 that took twice the time of the bytes.
+// were pieces of 64 or 128 that took twice the time of the bytes (256 positions, fp32: 185 us).  Up to kFewPositions the
+// logits are a small part of the bytes, and the ring has the room instead.
 template <typename T>
 constexpr int kTokens = kStageBytes / (kRowsCta * (int)sizeof(T));
 
@@ -528,7 +532,8 @@ cudaError_t launch_head_e4m3(const uint8_t *X, int64_t ldx, const float *x_scale
     const cudaError_t e = ensure_head_attributes();
     if (e != cudaSuccess) return e;
     const unsigned grid = 2 * (unsigned)std::min(p.tiles, pairs);
-    const int smem = fixed + p.stages * p.stage_bytes;
+    // (a CTA takes all of an SM's TMEM: no other one beside it)
+    const int smem = std::max(fixed + p.stages * p.stage_bytes, kSmemLimit / 2 + 1024);
     if (dtype == DG_BF16)
         head_kernel<__nv_bfloat16><<<grid, kThreads, smem, stream>>>(tm_x, tm_w, tm_x2, tm_w2, tm_out, p);
     else

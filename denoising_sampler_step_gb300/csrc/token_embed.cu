@@ -4,7 +4,7 @@
 //   gW[v] (+)= gamma sum over {r : token[r] = v} of g[r]
 //
 // Forward: a gather, bound by HBM (a table row and an output row per position) and by latency where there
-// are few positions: 8 positions of 256 columns 1.65 us, 8,192 bf16 rows of 2,816 from E4M3 codes 13.5 us (69 MB, 5.1 TB/s).
+// are few positions: 16 positions of 256 columns 1.65 us, 8,192 bf16 rows of 2,816 from E4M3 codes 13.5 us (69 MB, 5.1 TB/s).
 //
 // Backward: the positions are put in order of their tokens, equal ones by position, so that every table row is
 // written once, from its positions in order: no atomics on values, results repeat bit for bit.  The order is found in
@@ -17,7 +17,7 @@
 // while the one before them ends; the order is found while the gradient is cleared.
 //
 // Clearing is bound by HBM: 262,144 x 2,816 bf16 and 8,192 positions 231 us, 6.6 TB/s.  Without it the sums are bound by the
-// latency of their loads, and the call by the four kernels that wait for one another: 20,001 positions of 768 45 us, of
+// latency of their loads, and the call by the four kernels that wait for one another: 20,001 positions of 1,001 45 us, of
 // them order and merge 20, sums 21, join 6.
 #include <algorithm>
 #include <type_traits>
@@ -195,7 +195,7 @@ __device__ __forceinline__ int count_before(const int32_t *keys, int R, int i, i
     return n;
 }
 
-// By one CTA, up to kFewRows, where one kernel is called in 12 us (256 positions, bf16 of 2,816) to 23 (512), and the
+// By one CTA, up to kFewRows, where one kernel is called in 12 us (256 positions, fp32 of 2,816) to 23 (512), and the
 // kernels of more positions in 29.
 constexpr int kFewRows = 512;
 __device__ __forceinline__ void order_few(const SortParams &p, int32_t *unsorted, int32_t *key_s, int32_t *pos_s) {
@@ -809,7 +809,7 @@ cudaError_t sort_tokens(const SortParams &sp, bool chained, cudaStream_t stream)
     if (sp.R > kSortMost) return launch_chained(sort_far_kernel, kSortCtas, kSortThreads, 0, stream, chained, kSortCtas, sp);
     // Counting keeps every SM busy for the square of a run, the radix sort a CTA per run for longer.  d = 512: 2,048
     // positions 32.8 us with clearing by counting, 34.5 by sorting; 8,192 without clearing 23.1 and about 31, with it,
-    // when the SMs are taken, 49.0 and 44.9; 20,001 without, d = 768, 49.3 and 45.4.
+    // when the SMs are taken, 49.0 and 44.9; 20,001 without, d = 1,001, 49.3 and 45.4.
     cudaError_t e;
     if (sp.R <= (chained ? kRun : kCountRows))
         e = launch_chained(count_tokens_kernel, (unsigned)((sp.R + kCountItems - 1) / kCountItems), kCountThreads, 0, stream,
