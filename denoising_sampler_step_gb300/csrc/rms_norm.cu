@@ -557,28 +557,36 @@ __global__ void __launch_bounds__(max_threads(N)) rms_norm_backward_plain_kernel
             if (col.n[i] > 0) store8<false>(p.parts + blockIdx.x * p.part_ld + col.at[i], dw[i], col.n[i], col.step);
 }
 
-// dweight from the CTAs' parts, 32 columns a CTA: a warp reads four parts at a time, eight lanes each.
-constexpr int kWeightThreads = 256;
+// dweight from the CTAs' parts, 16 columns a CTA: 128 parts at once, four lanes each, so that a thread's loads are in
+// flight together.
+constexpr int kWeightThreads = 512, kWeightCols = 16;
 __global__ void __launch_bounds__(kWeightThreads) norm_weight_kernel(const float *__restrict__ parts, int64_t part_ld, int n,
                                                                      int64_t d, void *__restrict__ out, int dtype) {
-    __shared__ float4 acc[kWeightThreads / 8][8];
-    const int at = threadIdx.x / 8;
-    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x % 8 * 4;
+    __shared__ float4 acc[kWeightThreads / 32][kWeightCols / 4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t c = (int64_t)blockIdx.x * kWeightCols + lane % 4 * 4;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     grid_dependency_wait();
     if (c < part_ld)
 #pragma unroll 8
-        for (int i = at; i < n; i += kWeightThreads / 8) {
+        for (int i = threadIdx.x / 4; i < n; i += kWeightThreads / 4) {
             const float4 v = *reinterpret_cast<const float4 *>(parts + i * part_ld + c);
             s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
         }
-    acc[at][threadIdx.x % 8] = s;
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+        s.x += __shfl_xor_sync(0xffffffffu, s.x, off);
+        s.y += __shfl_xor_sync(0xffffffffu, s.y, off);
+        s.z += __shfl_xor_sync(0xffffffffu, s.z, off);
+        s.w += __shfl_xor_sync(0xffffffffu, s.w, off);
+    }
+    if (lane < 4) acc[warp][lane] = s;
     __syncthreads();
-    const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.x;
-    if (threadIdx.x < 32 && col < d) {
+    const int64_t col = (int64_t)blockIdx.x * kWeightCols + threadIdx.x;
+    if (threadIdx.x < kWeightCols && col < d) {
         float sum = 0.0f;
-#pragma unroll 8
-        for (int i = 0; i < kWeightThreads / 8; ++i) sum += reinterpret_cast<const float *>(acc[i])[threadIdx.x];
+#pragma unroll
+        for (int i = 0; i < kWeightThreads / 32; ++i) sum += reinterpret_cast<const float *>(acc[i])[threadIdx.x];
         if (dtype == DG_F32)
             static_cast<float *>(out)[col] = sum;
         else
@@ -754,7 +762,7 @@ cudaError_t launch_rms_norm_backward(const NormBackRows &a, void *workspace, cud
     if (!a.grad_weight) return cudaSuccess;
     // (starts while the rows' kernel ends)
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.d + 31) / 32), 1, 1);
+    cfg.gridDim = dim3((unsigned)((a.d + kWeightCols - 1) / kWeightCols), 1, 1);
     cfg.blockDim = dim3(kWeightThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
