@@ -16,7 +16,7 @@
 // they lie.
 //
 // 8,192 rows of 2,816: bf16 with an fp32 residual to codes, hidden kept, 44 us (5.8 TB/s of 254 MB; between other work
-// 39 us); the gradient in bf16 with the residual's 35 us (5.3 TB/s), 5 of them the second kernel's.  What keeps them from a
+// 39 us); the gradient in bf16 with the residual's 34 us (5.4 TB/s), some 4 of them the second kernel's.  What keeps them from a
 // copy's rate is latency: an SM holds 6 to 8 rows, and a row's two sums over its threads stop its loads' consumer.  One row of
 // 2,816: 2.6 us.  Rows read where they lie: 20,001 x 1,001 bf16 51 us, its gradient 84 us.
 #include <algorithm>

@@ -8,7 +8,7 @@
 //
 // Backward: the positions are put in order of their tokens, equal ones by position, so that every table row is
 // written once, from its positions in order: no atomics on values, results repeat bit for bit.  The order is found in
-// runs of 4,096, by counting or by a radix sort in shared memory (sort_tokens says when), that are merged by search; a
+// runs, by counting or by a radix sort in shared memory (sort_tokens says when), that are merged by search; a
 // radix sort by a cluster took 20 us and more, its passes waiting on barriers and scattered stores.  The sorted
 // positions are cut into units of up to 32; a warp takes a unit and 256 columns.  A token that ends within the next unit
 // is finished by the warp it began in.  One that covers a whole unit and its neighbours (a mask or padding token)
@@ -16,10 +16,11 @@
 // all of it, every CTA for a few columns of all positions, the parts in shared memory.  The kernels of a call start
 // while the one before them ends; the order is found while the gradient is cleared.
 //
-// Clearing is bound by HBM: 262,144 x 2,816 bf16 and 8,192 positions 231 us, 6.6 TB/s.  Without it the sums are bound by the
-// latency of their loads, and the call by the four kernels that wait for one another: 20,001 positions of 1,001 45 us, of
-// them order and merge 20, sums 21, join 6.
+// Clearing is bound by HBM: 262,144 x 2,816 bf16 and 8,192 positions 228 us, 6.7 TB/s.  Without it the sums are bound by the
+// latency of their loads, and the call by the four kernels that wait for one another: 20,001 positions of 1,001 41 us, of
+// them some 21 the sums.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "dg_internal.h"
@@ -119,6 +120,7 @@ struct SortParams {
     const int32_t *token;
     int64_t V, vocab_start, vocab_end;
     int32_t R, none;  // none: the key of a position without a table row, above all others
+    int run;          // positions that are ordered together
     int passes, bits;
     SortSpace s;
 };
@@ -211,19 +213,19 @@ __device__ __forceinline__ void order_few(const SortParams &p, int32_t *unsorted
     __syncthreads();
 }
 
-// By the whole chip, runs of up to kRun positions: place c of [1] takes run c, or [0] the only one.  A warp takes four
+// By the whole chip, runs of p.run positions: place c of [1] takes run c, or [0] the only one.  A warp takes four
 // positions at once against the keys that its lanes share out: shared memory would hold it up with one.
-constexpr int kRun = 4096, kCountRows = 8192, kCountThreads = 512, kCountItems = kCountThreads / 32 * 4;
+constexpr int kOneRun = 2048, kNearRun = 1024, kCountThreads = 512, kCountItems = kCountThreads / 32 * 4;
 __global__ void __launch_bounds__(kCountThreads) count_tokens_kernel(const SortParams p) {
-    __shared__ __align__(16) int32_t keys[kRun];
+    __shared__ __align__(16) int32_t keys[kOneRun];
     grid_launch_dependents();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.s.count = 0;
-    const int first = (int)blockIdx.x / (kRun / kCountItems) * kRun, n = min(kRun, p.R - first);
+    const int ctas = p.run / kCountItems, first = (int)blockIdx.x / ctas * p.run, n = min(p.run, p.R - first);
     gather_keys(p, first, n, keys);
     __syncthreads();
     const int4 *fours = reinterpret_cast<const int4 *>(keys);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int all = (n + 3) / 4, own = (int)blockIdx.x % (kRun / kCountItems) * (kCountItems / 4) + warp;
+    const int all = (n + 3) / 4, own = (int)blockIdx.x % ctas * (kCountItems / 4) + warp;
     if (own < all) {
         const int4 mine = fours[own];
         const int32_t k[4] = {mine.x, mine.y, mine.z, mine.w};
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(kCountThreads) count_tokens_kernel(const SortP
             for (int j = 0; j < 4; ++j) at += k[j] < k[q] || (k[j] == k[q] && j < q);
             const int i = 4 * own + q;
             if (lane == q && i < n) {
-                const int to = p.R > kRun;
+                const int to = p.R > p.run;
                 p.s.key[to][first + at] = k[q];
                 p.s.pos[to][first + at] = first + i;
             }
@@ -254,6 +256,50 @@ __global__ void __launch_bounds__(kCountThreads) count_tokens_kernel(const SortP
     }
     // what clears the gradient has completed before this kernel has, and so before the sums begin
     grid_dependency_wait();
+}
+
+// Merges counted runs, all keys in shared memory: an item's place is its own place in its run, and in the other runs that
+// of the first larger key (runs before it) or of the first one not smaller (after it).  Four threads per item share the
+// other runs.
+constexpr int kNearRows = 24576, kNearThreads = 512, kNearShare = 4;
+__global__ void __launch_bounds__(kNearThreads) merge_near_kernel(const SortParams p) {
+    extern __shared__ int4 near_fours[];
+    const int32_t *keys = reinterpret_cast<const int32_t *>(near_fours);
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int item = (int)blockIdx.x * (kNearThreads / kNearShare) + threadIdx.x / kNearShare, q = threadIdx.x % kNearShare;
+    const int i = min(item, p.R - 1), own = i / kNearRun, runs = (p.R + kNearRun - 1) / kNearRun;
+    const int32_t place = p.s.pos[1][i];
+    const int4 *fours = reinterpret_cast<const int4 *>(p.s.key[1]);  // (whole 16 bytes each: lay_out)
+    const int all = (p.R + 3) / 4;
+    constexpr int kAhead = 8;
+    for (int g0 = threadIdx.x; g0 < all; g0 += kAhead * kNearThreads) {
+        int4 v[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) v[j] = fours[min(g0 + j * kNearThreads, all - 1)];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (g0 + j * kNearThreads < all) near_fours[g0 + j * kNearThreads] = v[j];
+    }
+    __syncthreads();
+    const int32_t k = keys[i];
+    int at = q == 0 ? i - own * kNearRun : 0;
+    for (int c = q; c < runs; c += kNearShare) {
+        if (c == own) continue;
+        const int32_t *run = keys + c * kNearRun;
+        const int n = min(kNearRun, p.R - c * kNearRun), t = k + (c < own);
+        int found = 0;
+#pragma unroll
+        for (int step = kNearRun; step > 0; step >>= 1)
+            if (found + step <= n && run[found + step - 1] < t) found += step;
+        at += found;
+    }
+#pragma unroll
+    for (int off = 1; off < kNearShare; off <<= 1) at += __shfl_xor_sync(0xffffffffu, at, off);
+    if (item < p.R && q == 0) {
+        p.s.key[0][at] = k;
+        p.s.pos[0][at] = place;
+    }
 }
 
 // The lanes whose digit is this lane's; `in`: the lanes that have one.
@@ -294,9 +340,10 @@ __device__ __forceinline__ void scan_warps(uint32_t *hist, uint32_t *total, int 
 }
 
 // A run of kRun positions by a stable radix sort in one CTA, least digit first, an item's key and position in
-// registers and, between passes, in shared memory; a warp takes N * 32 items in a row.  Run c goes to place c of [1], or
-// the only one to [0].  Digits of at most 8 bits: with 10, two passes in place of three, clearing and summing the counts
+// registers and, between passes, in shared memory; a warp takes N * 32 items in a row.  Run c goes to place c of [1].
+// Digits of at most 8 bits: with 10, two passes in place of three, clearing and summing the counts
 // took longer than the pass that it saved.
+constexpr int kRun = 4096;
 __global__ void __launch_bounds__(kSortThreads) sort_run_kernel(const SortParams p) {
     constexpr int N = kRun / kSortThreads;
     __shared__ int32_t key_s[kRun], pos_s[kRun];
@@ -362,19 +409,17 @@ __global__ void __launch_bounds__(kSortThreads) sort_run_kernel(const SortParams
                 pos[j] = pos_s[local0 + 32 * j];
             }
     }
-    const int to = p.R > kRun;
 #pragma unroll
     for (int j = 0; j < N; ++j)
         if (in[j] & lane_bit) {
-            p.s.key[to][first + local0 + 32 * j] = key[j];
-            p.s.pos[to][first + local0 + 32 * j] = pos[j];
+            p.s.key[1][first + local0 + 32 * j] = key[j];
+            p.s.pos[1][first + local0 + 32 * j] = pos[j];
         }
     // what clears the gradient has completed before this kernel has, and so before the sums begin
     grid_dependency_wait();
 }
 
-// Merges the runs: an item's place is its own place in its run, and in the other runs that of the
-// first larger key (runs before it) or of the first one not smaller (after it).
+// Merges runs of kRun likewise, from global memory.
 __global__ void __launch_bounds__(256) merge_runs_kernel(const SortParams p) {
     constexpr int kAtOnce = 4;  // searches
     grid_dependency_wait();
@@ -804,19 +849,37 @@ cudaError_t launch_chained(void (*kernel)(Args...), unsigned grid, unsigned thre
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+cudaError_t ensure_merge_attributes() {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<int> done[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < kMaxDevices && done[dev].load(std::memory_order_acquire))) return e;
+    e = cudaFuncSetAttribute(merge_near_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNearRows * (int)sizeof(int32_t));
+    if (e == cudaSuccess && dev < kMaxDevices) done[dev].store(1, std::memory_order_release);
+    return e;
+}
+
 // chained: after the kernel that clears the gradient, which starts after all that was launched before it
-cudaError_t sort_tokens(const SortParams &sp, bool chained, cudaStream_t stream) {
+cudaError_t sort_tokens(SortParams sp, bool chained, cudaStream_t stream) {
     if (sp.R > kSortMost) return launch_chained(sort_far_kernel, kSortCtas, kSortThreads, 0, stream, chained, kSortCtas, sp);
-    // Counting keeps every SM busy for the square of a run, the radix sort a CTA per run for longer.  d = 512: 2,048
-    // positions 32.8 us with clearing by counting, 34.5 by sorting; 8,192 without clearing 23.1 and about 31, with it,
-    // when the SMs are taken, 49.0 and 44.9; 20,001 without, d = 1,001, 49.3 and 45.4.
-    cudaError_t e;
-    if (sp.R <= (chained ? kRun : kCountRows))
-        e = launch_chained(count_tokens_kernel, (unsigned)((sp.R + kCountItems - 1) / kCountItems), kCountThreads, 0, stream,
-                           chained, 1u, sp);
-    else
-        e = launch_chained(sort_run_kernel, (unsigned)((sp.R + kRun - 1) / kRun), kSortThreads, 0, stream, chained, 1u, sp);
-    if (e != cudaSuccess || sp.R <= kRun) return e;
+    // Runs counted side by side and merged in shared memory take half the time of radix runs merged from global memory:
+    // d = 512, 5,000 positions 15.4 us and 23.6, 16,000 25.9 and 29.3, 24,576 34.7 and 36.8; 32,768 44.8 and 44.0, as
+    // every CTA of the merge loads all keys.  Up to kOneRun they are one run: 2,048 positions 12.8 us and, merged of two,
+    // 13.6; 3,000 14.9 and 14.3.
+    if (sp.R <= kNearRows) {
+        const bool one = sp.R <= kOneRun;
+        sp.run = one ? kOneRun : kNearRun;
+        cudaError_t e = launch_chained(count_tokens_kernel, (unsigned)((sp.R + kCountItems - 1) / kCountItems), kCountThreads, 0,
+                                       stream, chained, 1u, sp);
+        if (e == cudaSuccess && !one) e = ensure_merge_attributes();
+        if (e != cudaSuccess || one) return e;
+        const int items = kNearThreads / kNearShare;
+        return launch_chained(merge_near_kernel, (unsigned)((sp.R + items - 1) / items), kNearThreads,
+                              (size_t)(sp.R + 3) / 4 * sizeof(int4), stream, true, 1u, sp);
+    }
+    const cudaError_t e = launch_chained(sort_run_kernel, (unsigned)((sp.R + kRun - 1) / kRun), kSortThreads, 0, stream, chained, 1u, sp);
+    if (e != cudaSuccess) return e;
     return launch_chained(merge_runs_kernel, (unsigned)((sp.R + 255) / 256), 256u, 0, stream, true, 1u, sp);
 }
 
