@@ -56,7 +56,7 @@ struct HeadParams {
     int stages, stage_bytes, resident_bytes;
     uint32_t idesc;
     int stream_table;   // each table byte is read once: leave L2 first
-    int stream_logits;  // the logits do not stay in L2 either way
+    int stream_logits;  // the logits do not stay in L2 either way (128 positions, fp32: 136.1 us for 140.9)
     int staged;         // logits go through shared memory
 };
 
@@ -142,8 +142,9 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&v)
 // Logits through shared memory: a half of the epilogue (four warps, a lane quarter each) gathers kTokens positions of
 // all the tile's table rows, [position][table row], which one thread sends out as one tile; rows and columns past the
 // matrix are cut off there.  So a position's logits leave as one piece of 256 or 512 bytes, where a warp's own stores
-// were pieces of 64 or 128 that took twice the time of the bytes (256 positions, fp32: 185 us).  Up to kFewPositions the
-// logits are a small part of the bytes, and the ring has the room instead.
+// were pieces of 64 or 128 that took twice the time of the bytes (256 positions, fp32: 185 us;
+// 128: 139.6 us and as tiles 136.1).  Up to kFewPositions the logits are a small part of the bytes, and the ring has the
+// room instead (64 positions 126.5 us, as tiles 128.2).
 template <typename T>
 constexpr int kTokens = kStageBytes / (kRowsCta * (int)sizeof(T));
 
@@ -494,7 +495,8 @@ cudaError_t launch_head_e4m3(const uint8_t *X, int64_t ldx, const float *x_scale
     p.k_blocks = (int)((d + kBlockK - 1) / kBlockK);
     p.k_steps = (int)((d + 31) / 32);
     p.full_blocks = (int)(d / kBlockK);
-    // the positions' codes are the same for every tile where one tile holds them all.  A product reads kRowsCta
+    // the positions' codes are the same for every tile where one tile holds them all (64 positions 126.5 us, sent for with
+    // every tile 128.7).  A product reads kRowsCta
     // table rows from where a tile's begin, whatever lies there past the tile's own: the last slot's need room
     const int slots = (p.k_blocks + kSlotBlocks - 1) / kSlotBlocks;
     const int x_slot = kSlotBlocks * (p.tile_r / 2) * kBlockK, slack = (kRowsCta - p.rows_cta) * kBlockK;
