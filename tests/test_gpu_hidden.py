@@ -205,7 +205,7 @@ def test_gradient(B, R, V, d, kind):
 
 # where the order of the tokens is found in another way, or in one run, or one position, more
 @pytest.mark.parametrize("kind", ["uniform", "masked"])
-@pytest.mark.parametrize("R,V,d", [(512, 70, 5), (513, 70, 5), (1025, 9, 8), (2048, 700, 8), (4097, 33, 8), (24575, 50, 8),
+@pytest.mark.parametrize("R,V,d", [(256, 70, 5), (257, 70, 5), (512, 70, 5), (513, 70, 5), (1025, 9, 8), (2048, 700, 8), (4097, 33, 8), (24575, 50, 8),
                                    (24576, 9000, 8), (24577, 50, 8), (65536, 1000, 8), (65537, 1000, 8)])
 def test_gradient_where_the_order_changes(B, R, V, d, kind):
     test_gradient(B, R, V, d, kind)
