@@ -198,7 +198,7 @@ __device__ __forceinline__ int count_before(const int32_t *keys, int R, int i, i
 }
 
 // By one CTA, up to kFewRows: 256 positions of 2,816 fp32 8.8 us in one kernel and, up to 128, 8.4 us, but called in 12.6
-// for 10.8; 512 9.0 and, in one kernel, 14.3.
+// for 10.8; 512 9.0 and, in one kernel, 14.3.  (With 32,000 x 512 cleared before, 300 take 26.5 and, in one kernel, 22.0.)
 constexpr int kFewRows = 256;
 __device__ __forceinline__ void order_few(const SortParams &p, int32_t *unsorted, int32_t *key_s, int32_t *pos_s) {
     constexpr int T = kSortThreads / kFewRows;
