@@ -759,8 +759,8 @@ size_t dg_token_embed_backward_workspace_size(int64_t R, int64_t vocab_len, int6
  *   hidden    [R, ldh] of hidden_dtype: h rounded once (y is taken of the unrounded one), or NULL.  It may
  *             replace x or residual (same pointer, type and stride).
  *   out       [R, ldo] of out_dtype: y.  It may replace x or residual likewise (not hidden).  DG_E4M3: out_scale [R] fp32 =
- *             max|y| / 448 and codes e4m3(y / out_scale), ties to even (the quotient within two fp32 roundings; a row
- *             of zeros: scale 0, codes 0): what dg_head_e4m3 takes.  A row with an infinity or NaN has NaN or infinity as its scale.
+ *             max|y| / 448 and codes e4m3(y / out_scale), the quotient rounded to fp32 once, ties to even, magnitudes past 448
+ *             as 448 (a row of zeros: scale 0, codes 0): what dg_head_e4m3 takes.  A row with an infinity or NaN has NaN or infinity as its scale.
  *   rstd      [R] fp32 or NULL: what the backward pass takes
  * Requires 1 <= d <= 32768 (above: DG_ERR_UNSUPPORTED), eps >= 0 and finite, weight_offset finite, R <= 2^28.
  */
