@@ -572,10 +572,10 @@ __global__ void __launch_bounds__(max_threads(N)) rms_norm_backward_plain_kernel
 }
 
 // dweight from the CTAs' parts, 16 columns a CTA: 128 parts at once, four lanes each, so that a thread's loads are in
-// flight together.
+// flight together.  It is resident while the parts are written: they are read past L1, and not as constant data.
 constexpr int kWeightThreads = 512, kWeightCols = 16;
-__global__ void __launch_bounds__(kWeightThreads) norm_weight_kernel(const float *__restrict__ parts, int64_t part_ld, int n,
-                                                                     int64_t d, void *__restrict__ out, int dtype) {
+__global__ void __launch_bounds__(kWeightThreads) norm_weight_kernel(const float *parts, int64_t part_ld, int n, int64_t d,
+                                                                     void *out, int dtype) {
     __shared__ float4 acc[kWeightThreads / 32][kWeightCols / 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t c = (int64_t)blockIdx.x * kWeightCols + lane % 4 * 4;
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(kWeightThreads) norm_weight_kernel(const float
     if (c < part_ld)
 #pragma unroll 8
         for (int i = threadIdx.x / 4; i < n; i += kWeightThreads / 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(parts + i * part_ld + c);
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(parts + i * part_ld + c));
             s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
         }
 #pragma unroll
