@@ -931,7 +931,7 @@ def dg_token_embed_backward_workspace_size(R: int, vocab_len: int, d: int) -> in
 
 
 def embed_workspace(R: int, vocab_len: int, d: int, device) -> torch.Tensor:
-    """A workspace tensor large enough for dg_token_embed_backward."""
+    """A workspace tensor large enough for dg_token_embed_backward, of these sizes or smaller ones."""
     return _scratch(dg_token_embed_backward_workspace_size(R, vocab_len, d), device, None)
 
 
@@ -1028,7 +1028,7 @@ def dg_rms_norm_backward_workspace_size(R: int, d: int) -> int:
 
 
 def norm_workspace(R: int, d: int, device) -> torch.Tensor:
-    """A workspace tensor large enough for dg_rms_norm_backward."""
+    """A workspace tensor large enough for dg_rms_norm_backward, of these sizes or smaller ones."""
     return _scratch(dg_rms_norm_backward_workspace_size(R, d), device, None)
 
 

@@ -801,16 +801,15 @@ __global__ void __launch_bounds__(256) clear_rows_kernel(const EmbedRows a, int6
 
 // Sorted positions of a unit: long ones, which leave fewer parts, where that still leaves every SM some warps
 // (8,192 x 2,816: 37.7 us with 32, 38.5 with 16; 8,192 x 512 with 8 26.9 for 23.2).
-int unit_of(int64_t R, int64_t d) {
-    const int64_t warps = (d + 255) / 256 * R;  // of one position each
-    return warps >= 32 * 2048 ? 32 : 16;
-}
+constexpr int kUnit = 16, kLongUnit = 32;
+constexpr int64_t kLongFrom = 32 * 2048;  // positions times slabs of 256 columns
+int unit_of(int64_t R, int64_t d) { return (d + 255) / 256 * R >= kLongFrom ? kLongUnit : kUnit; }
 
 size_t align16(size_t b) { return (b + 15) & ~size_t(15); }
 
-SortSpace lay_out(uint8_t *base, int64_t R, int64_t d, size_t *bytes) {
+SortSpace lay_out(uint8_t *base, int64_t R, int64_t d, int unit, size_t *bytes) {
     SortSpace s;
-    const int64_t units = (R + unit_of(R, d) - 1) / unit_of(R, d);
+    const int64_t units = (R + unit - 1) / unit;
     size_t at = 0;
     auto take = [&](size_t n) {
         uint8_t *q = base + at;
@@ -920,10 +919,18 @@ cudaError_t launch_token_embed(const EmbedRows &a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
+// What any call of up to R positions and d columns needs, so that a workspace for the largest call serves smaller ones:
+// calls just too small for long units leave twice the parts of those just above.
 size_t token_embed_backward_bytes(int64_t R, int64_t d) {
-    size_t bytes;
-    lay_out(nullptr, R, d, &bytes);
-    return bytes;
+    size_t most, bytes;
+    lay_out(nullptr, R, d, unit_of(R, d), &most);
+    if (unit_of(R, d) == kUnit) return most;  // (so are all smaller calls')
+    // the largest calls of short units, slab by slab; of kUnit positions and fewer there is one unit of either length
+    for (int64_t slabs = 1; slabs <= (d + 255) / 256 && (kLongFrom - 1) / slabs > kUnit; ++slabs) {
+        lay_out(nullptr, std::min(R, (kLongFrom - 1) / slabs), std::min(d, slabs * 256), kUnit, &bytes);
+        most = std::max(most, bytes);
+    }
+    return most;
 }
 
 cudaError_t launch_token_embed_backward(const EmbedRows &a, void *workspace, cudaStream_t stream) {
@@ -940,7 +947,7 @@ cudaError_t launch_token_embed_backward(const EmbedRows &a, void *workspace, cud
     if (a.R == 0) return cudaSuccess;
     size_t bytes;
     SortParams sp{};
-    sp.s = lay_out(static_cast<uint8_t *>(workspace), a.R, a.d, &bytes);
+    sp.s = lay_out(static_cast<uint8_t *>(workspace), a.R, a.d, unit_of(a.R, a.d), &bytes);
     sp.token = a.token;
     sp.V = a.V;
     sp.vocab_start = a.vocab_start;

@@ -746,7 +746,8 @@ dg_status dg_token_embed_backward(const void *grad, int32_t dtype, int64_t R, in
                                   float gamma, void *grad_table, int32_t table_dtype, int64_t rows_pad, int64_t ldt,
                                   int32_t accumulate, void *workspace, size_t workspace_bytes, dg_stream_t stream);
 
-/* Bytes of workspace dg_token_embed_backward needs for a slice of vocab_len entries (0 for an invalid shape). */
+/* Bytes of workspace dg_token_embed_backward needs for a slice of vocab_len entries (0 for an invalid shape); enough for
+ * every call of fewer positions, entries or columns too. */
 size_t dg_token_embed_backward_workspace_size(int64_t R, int64_t vocab_len, int64_t d);
 
 /*
@@ -790,7 +791,8 @@ dg_status dg_rms_norm_backward(const void *grad, int32_t dtype, int64_t R, int64
                                int64_t ldx, void *grad_weight, void *workspace, size_t workspace_bytes,
                                dg_stream_t stream);
 
-/* Bytes of workspace dg_rms_norm_backward needs on the current device (0 for an invalid shape). */
+/* Bytes of workspace dg_rms_norm_backward needs on the current device (0 for an invalid shape); enough for every call of
+ * fewer rows or columns too. */
 size_t dg_rms_norm_backward_workspace_size(int64_t R, int64_t d);
 
 /*

@@ -27,3 +27,23 @@ def test_the_norms_gradient_again_and_again(B, R, d):
             B.dg_rms_norm_backward(t, h, rstd, w, ws=ws, out={"grad": out, "grad_weight": got[i, k]})
     for k in range(3):
         assert (got[:, k] == ref[k]).all()
+
+
+@pytest.mark.parametrize("most,calls", [((8192, 2816), [(5000, 2816), (5957, 2816), (8192, 2500), (6553, 2560), (17, 2816), (1, 1)]),
+                                        ((40000, 1001), [(40000, 256), (40000, 257), (16383, 1001), (32767, 512), (300, 40)])])
+def test_a_workspace_for_the_largest_call_serves_smaller_ones(B, most, calls):
+    g = torch.Generator(device="cuda").manual_seed(1)
+    need = B.dg_token_embed_backward_workspace_size(most[0], 500, most[1])
+    ws = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+    for R, d in calls:
+        grad = torch.randn(R, (d + 7) // 8 * 8, generator=g, device="cuda")[:, :d]
+        tok = torch.randint(500, (R,), generator=g, device="cuda").int()
+        tok[torch.rand(R, generator=g, device="cuda") < 0.5] = 77
+        got = B.dg_token_embed_backward(grad, tok, 500, ws=ws[:need])
+        assert torch.equal(got, B.dg_token_embed_backward(grad, tok, 500))
+        assert (ws[need:] == 0xFF).all()
+        # (n + 3) roundings of 2^-24 of the terms' magnitudes
+        want = torch.zeros(500, d, dtype=torch.float64, device="cuda").index_add_(0, tok, grad.double())
+        size = torch.zeros(500, d, dtype=torch.float64, device="cuda").index_add_(0, tok, grad.double().abs())
+        n = torch.bincount(tok, minlength=500)[:, None]
+        assert ((got - want).abs() <= (n + 3) * 2.0 ** -24 * size).all()
