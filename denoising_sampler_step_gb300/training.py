@@ -68,12 +68,16 @@ class _TokenEmbed(torch.autograd.Function):
 class _RmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, weight, eps, weight_offset, dtype):
+        ctx.weight_offset, ctx.types = weight_offset, (x.dtype, None if residual is None else residual.dtype)
+        ctx.set_materialize_grads(False)
+        dtype = x.dtype if dtype is None else dtype
+        if residual is not None and x.dtype == torch.float32:
+            # hidden has the second matrix's type: fp32 where either is, so that the backward pass loses no bits
+            x, residual = residual, x
         o = B.dg_rms_norm(x, weight, residual=residual, eps=eps, weight_offset=weight_offset, dtype=dtype)
         hidden = o.get("hidden", x)
         ctx.save_for_backward(hidden, weight, o["rstd"])
-        ctx.weight_offset, ctx.types = weight_offset, (x.dtype, None if residual is None else residual.dtype)
-        ctx.set_materialize_grads(False)
-        return o["out"], (None if residual is None else hidden)
+        return o["out"], (None if residual is None else hidden.to(ctx.types[1]))
 
     @staticmethod
     def backward(ctx, g, gh):
@@ -211,7 +215,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torc
              eps: float = 1e-6, weight_offset: float = 0.0,
              dtype: torch.dtype | None = None) -> tuple[torch.Tensor, torch.Tensor | None]:
     """(y, h) with h = x + residual and y = h / rms(h) (weight_offset + weight), differentiable in all three
-    (binding.dg_rms_norm); h is None without a residual."""
+    (binding.dg_rms_norm); h is None without a residual, and has the residual's type with one.  The backward pass
+    keeps h, and computes gradients, in fp32 where x or the residual is fp32; each is rounded once to its input's type."""
     if dtype is not None and not dtype.is_floating_point:
         raise TypeError("8-bit outputs are not differentiable: use binding.dg_rms_norm")
     return _RmsNorm.apply(x, residual, weight, eps, weight_offset, dtype)
