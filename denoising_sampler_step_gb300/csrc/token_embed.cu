@@ -197,11 +197,16 @@ __device__ __forceinline__ int count_before(const int32_t *keys, int R, int i, i
     return n;
 }
 
-// By one CTA, up to kFewRows: 256 positions of 2,816 fp32 8.8 us in one kernel and, up to 128, 8.4 us, but called in 12.6
-// for 10.8; 512 9.0 and, in one kernel, 14.3.  (With 32,000 x 512 cleared before, 300 take 26.5 and, in one kernel, 22.0.)
-constexpr int kFewRows = 256;
+// By one CTA, up to kFewRows positions.  A gradient that is added to, fp32 (V = 32,000, d = 512; with the limit at 256 and at 512):
+// 256 positions 8.4 us and 9.3, 512 11.0 and 13.7.  A cleared one finds the order under the clearing, and one kernel in place of
+// three follows it, so that up to 512 one kernel is as fast or faster: 300 positions 22.1 us for 26.2, 512 25.6 for 26.8; 300 of
+// 1,001 34.1 for 39.3; of 2,816 over 262,144 bf16 rows 208 for 213; and 512 of 256 over 4,096 12.4 for 11.1 in a graph, but called
+// in 14.5 for 14.7.
+template <bool kAdd>
+constexpr int kFewRows = kAdd ? 256 : 512;
+template <int kRows>
 __device__ __forceinline__ void order_few(const SortParams &p, int32_t *unsorted, int32_t *key_s, int32_t *pos_s) {
-    constexpr int T = kSortThreads / kFewRows;
+    constexpr int T = kSortThreads / kRows;
     gather_keys(p, 0, p.R, unsorted);
     __syncthreads();
     const int i = threadIdx.x / T;
@@ -722,18 +727,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_parts_kernel(const SumPa
 // ---------------------------------------------------------------- few positions
 
 constexpr int kFewUnit = 4, kFewLanes = 4;  // positions of a unit; threads of a unit, eight columns each
-constexpr int kFewUnits = kFewRows / kFewUnit;
 constexpr int kFewCols = 8 * kFewLanes;
 
 // All of it in one kernel: a CTA orders the positions for itself, and sums kFewCols columns of all of them, four threads
 // per unit; parts stay in shared memory.
 template <typename TG, typename TT, bool kAdd, bool kWide>
 __global__ void __launch_bounds__(kSortThreads) few_rows_kernel(const SumParams p, const SortParams sp) {
-    __shared__ __align__(16) float parts[kFewUnits][2][kFewCols];
-    __shared__ __align__(16) int32_t unsorted[kFewRows];
-    __shared__ int32_t key_s[kFewRows], pos_s[kFewRows];
+    constexpr int kRows = kFewRows<kAdd>;
+    __shared__ __align__(16) float parts[kRows / kFewUnit][2][kFewCols];
+    __shared__ __align__(16) int32_t unsorted[kRows];
+    __shared__ int32_t key_s[kRows], pos_s[kRows];
     const EmbedRows &a = p.a;
-    order_few(sp, unsorted, key_s, pos_s);
+    order_few<kRows>(sp, unsorted, key_s, pos_s);
     grid_dependency_wait();  // (what clears the gradient)
     const int R = (int)a.R, U = kFewUnit;
     auto key = [&](int i) { return i >= 0 && i < R ? key_s[i] : -1; };
@@ -885,10 +890,9 @@ cudaError_t sort_tokens(SortParams sp, bool chained, cudaStream_t stream) {
 
 template <typename TG, typename TT, bool kAdd, bool kWide>
 cudaError_t sums(const SumParams &p, const SortParams &sp, cudaStream_t stream) {
-    if (p.a.R <= kFewRows) {
+    if (p.a.R <= kFewRows<kAdd>)
         return launch_chained(few_rows_kernel<TG, TT, kAdd, kWide>, (unsigned)((p.a.d + kFewCols - 1) / kFewCols), kSortThreads, 0,
                               stream, !kAdd, 1u, p, sp);
-    }
     cudaError_t e = sort_tokens(sp, !kAdd, stream);
     if (e != cudaSuccess) return e;
     const unsigned ctas = (unsigned)((p.units + p.cta_units - 1) / p.cta_units * p.slab_ctas);
