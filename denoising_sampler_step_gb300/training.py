@@ -31,12 +31,11 @@ def _upstream(g: torch.Tensor, weight: torch.Tensor | None) -> torch.Tensor:
     return g.float().contiguous()
 
 
-def _constants(**tensors) -> None:
-    """Refuses arguments whose gradient would be dropped."""
-    for name, t in tensors.items():
-        if t is not None and t.requires_grad and torch.is_grad_enabled():
-            raise ValueError(f"{name} requires a gradient, and the loss is differentiable in the logits alone: "
-                             f"pass {name}.detach()")
+def _constants(alone: str = "the loss is differentiable in the logits alone", **values) -> None:
+    """Refuses arguments, matrices and numbers alike, whose gradient would be dropped."""
+    for name, t in values.items():
+        if isinstance(t, torch.Tensor) and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} requires a gradient, and {alone}: pass {name}.detach()")
 
 
 def _first_order() -> None:
@@ -173,6 +172,7 @@ class _Preference(torch.autograd.Function):
 def token_logp(logits: torch.Tensor, token: torch.Tensor, temperature: float = 1.0,
                mask: torch.Tensor | None = None) -> torch.Tensor:
     """ln softmax(logits / T)[token] per row [R], differentiable in the logits."""
+    _constants(temperature=temperature)
     return _TokenLogp.apply(logits, token, temperature, _weight(mask))
 
 
@@ -180,7 +180,7 @@ def distill_loss(logits: torch.Tensor, indices: torch.Tensor, teacher: torch.Ten
                  teacher_lse: torch.Tensor | None = None, temperature: float = 1.0,
                  mask: torch.Tensor | None = None) -> torch.Tensor:
     """Distillation loss per row [R] from a teacher's top logits (binding.dg_distill_loss)."""
-    _constants(teacher=teacher, teacher_lse=teacher_lse)
+    _constants(teacher=teacher, teacher_lse=teacher_lse, temperature=temperature)
     return _Distill.apply(logits, indices, teacher, teacher_lse, temperature, _weight(mask))
 
 
@@ -189,7 +189,8 @@ def policy_loss(logits: torch.Tensor, token: torch.Tensor, old_logp: torch.Tenso
                 kl_coef: float = 0.0, temperature: float = 1.0,
                 mask: torch.Tensor | None = None) -> tuple[torch.Tensor, dict]:
     """(loss per row [R], {logp, kl, clipped}) of the clipped policy loss (binding.dg_policy_loss)."""
-    _constants(old_logp=old_logp, advantage=advantage, ref_logp=ref_logp)
+    _constants(old_logp=old_logp, advantage=advantage, ref_logp=ref_logp, clip_low=clip_low, clip_high=clip_high,
+               kl_coef=kl_coef, temperature=temperature)
     loss, logp, kl, clipped = _Policy.apply(logits, token, old_logp, advantage, ref_logp, clip_low, clip_high,
                                             kl_coef, temperature, _weight(mask))
     return loss, {"logp": logp, "kl": kl, "clipped": clipped}
@@ -200,7 +201,7 @@ def preference_loss(logits: torch.Tensor, token: torch.Tensor, ref_logp: torch.T
                     temperature: float = 1.0, weight: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """(loss per pair [P], log ratios per sequence [2P]) of the preference loss
     (binding.dg_preference_loss); `weight` [R] masks tokens or normalises by length."""
-    _constants(ref_logp=ref_logp, weight=weight)
+    _constants(ref_logp=ref_logp, weight=weight, beta=beta, label_smoothing=label_smoothing, temperature=temperature)
     return _Preference.apply(logits, token, ref_logp, seq_start, beta, label_smoothing, temperature, weight)
 
 
@@ -208,6 +209,7 @@ def token_embed(table: torch.Tensor, token: torch.Tensor, gamma: float = 1.0,
                 dtype: torch.dtype | None = None) -> torch.Tensor:
     """gamma times the rows of `table` [V, d] (fp32 or bf16) at `token` [R] (int32; negative: padding, a row of
     zeros), differentiable in the table (binding.dg_token_embed).  The gradient has the table's type and size."""
+    _constants("token_embed is differentiable in the table alone", gamma=gamma)
     return _TokenEmbed.apply(table, token, gamma, dtype)
 
 
@@ -217,6 +219,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torc
     """(y, h) with h = x + residual and y = h / rms(h) (weight_offset + weight), differentiable in all three
     (binding.dg_rms_norm); h is None without a residual, and has the residual's type with one.  The backward pass
     keeps h, and computes gradients, in fp32 where x or the residual is fp32; each is rounded once to its input's type."""
+    _constants("rms_norm is differentiable in its matrices and weight alone", eps=eps, weight_offset=weight_offset)
     if dtype is not None and not dtype.is_floating_point:
         raise TypeError("8-bit outputs are not differentiable: use binding.dg_rms_norm")
     return _RmsNorm.apply(x, residual, weight, eps, weight_offset, dtype)
