@@ -31,19 +31,27 @@ dg_status check_rows(const char *what, const char *name, const Rows &m, int64_t 
     return DG_OK;
 }
 
+// Memory from lo to hi, of a matrix only the first `width` bytes of every `pitch`.
 struct Span {
-    uintptr_t lo, hi;
+    uintptr_t lo, hi, pitch = 0, width = 0;
 };
 Span span(const Rows &m, int64_t rows, int64_t d) {
     const uintptr_t lo = reinterpret_cast<uintptr_t>(m.p);
     if (!m.p || rows < 1) return {lo, lo};
-    return {lo, lo + (uintptr_t)(((rows - 1) * m.ld + d) * entry_size(m.dtype))};
+    const int64_t size = entry_size(m.dtype);
+    return {lo, lo + (uintptr_t)(((rows - 1) * m.ld + d) * size), (uintptr_t)(m.ld * size), (uintptr_t)(d * size)};
 }
 Span span(const void *p, int64_t bytes) {
     const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
     return {lo, lo + (p ? (uintptr_t)bytes : 0)};
 }
-bool meet(const Span &a, const Span &b) { return a.lo < b.hi && b.lo < a.hi; }
+bool meet(const Span &a, const Span &b) {
+    if (!(a.lo < b.hi && b.lo < a.hi)) return false;
+    if (a.pitch == 0 || a.pitch != b.pitch) return true;
+    // columns of one buffer: b's may lie in what a leaves of each row
+    const uintptr_t off = b.lo >= a.lo ? (b.lo - a.lo) % a.pitch : a.pitch - 1 - (a.lo - b.lo - 1) % a.pitch;
+    return off < a.width || off + b.width > a.pitch;
+}
 
 // Whether `out` may stand where `in` does: apart, or exactly in its place.
 bool apart_or_same(const Rows &out, const Rows &in, int64_t rows, int64_t d) {

@@ -705,7 +705,7 @@ dg_status dg_preference_loss(const void *logits, int32_t dtype, int64_t R, int64
  *   matrices   row-major, `ld` elements between rows, any width d >= 1, any alignment of their entries'
  *              size (rows on 16-byte boundaries are faster; the head requires them).  Columns at d and past
  *              it are not written, and what they hold does not matter.  An output that overlaps an input is DG_ERR_INVALID_ARG,
- *              but where a call says that it may replace one.
+ *              but where a call says that it may replace one; different columns of one buffer (equal strides) do not overlap.
  *   dtypes     DG_F32 or DG_BF16, and DG_E4M3 with fp32 scales where named: a value is scale times its code's.
  *   vectors    tokens, scales and statistics are contiguous and 4-byte aligned.
  *   Sums and statistics are fp32, outputs are rounded once, results are bitwise reproducible.
