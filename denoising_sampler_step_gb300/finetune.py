@@ -96,6 +96,14 @@ def run(steps: int = 60, K: int = 64, seed: int = 0, log=print) -> dict:
     return report
 
 
+def denoising_loss(table, weight, noised, clean, signal, gamma):
+    """Loss per position that holds a token: that of the clean tokens, from the noised ones and the signal."""
+    x = training.token_embed(table, noised, gamma)
+    y, _ = training.rms_norm(x, weight, residual=signal)
+    logp = training.token_logp(y @ table.T, clean, mask=noised >= 0)
+    return -logp.sum() / (noised >= 0).sum()
+
+
 def denoise(steps: int = 60, noise: float = 0.3, seed: int = 0, log=print) -> dict:
     """Trains a tied table and a norm to name a canvas' clean tokens from a noised one (a share `noise` of its
     positions hold one mask token, some are padding) and a self-conditioning signal."""
@@ -109,14 +117,12 @@ def denoise(steps: int = 60, noise: float = 0.3, seed: int = 0, log=print) -> di
     signal = 0.1 * torch.randn(R, d, generator=g, device="cuda")
     noised = torch.where(torch.rand(R, generator=g, device="cuda") < noise, V - 1, clean)
     noised[-wl.R // 4:] = -1                  # padding: no embedding, no loss
+    noised = noised.to(torch.int32)
     opt = torch.optim.Adam([table, weight], lr=0.005)
     losses = []
     for _ in range(steps):
         opt.zero_grad()
-        x = training.token_embed(table, noised.to(torch.int32), gamma)
-        y, _ = training.rms_norm(x, weight, residual=signal)
-        logp = training.token_logp(y @ table.T, clean, mask=noised >= 0)
-        loss = -logp.sum() / (noised >= 0).sum()
+        loss = denoising_loss(table, weight, noised, clean, signal, gamma)
         loss.backward()
         opt.step()
         losses.append(loss.detach())
