@@ -941,6 +941,8 @@ def dg_token_embed(table: torch.Tensor, token: torch.Tensor, gamma: float = 1.0,
     """gamma times the table's rows at `token` [R] (int32; negative: padding, a row of zeros) -> [R, d].
     table: fp32 or bf16 [rows_pad, d], or E4M3 codes with the row scales `scale`; row j is vocabulary entry
     vocab_start + j (the whole table by default), and tokens outside [vocab_start, vocab_end) give zeros.
+    V: the vocabulary's size, which a slice's caller gives too (default: vocab_end); a token at or past it is an
+    error that dg_get_device_status reports.
     dtype: of a new output (default: the table's, bf16 for codes)."""
     device = _here(table, "table")
     rows, d = table.shape

@@ -18,7 +18,9 @@
 // 8,192 rows of 2,816: bf16 with an fp32 residual to codes, hidden kept, 44 us (5.8 TB/s of 254 MB; between other work
 // 39 us); the gradient in bf16 with the residual's 34 us (5.4 TB/s), some 4 of them the second kernel's.  What keeps them from a
 // copy's rate is latency: an SM holds 6 to 8 rows, and a row's two sums over its threads stop its loads' consumer.  One row of
-// 2,816: 2.6 us.  Rows read where they lie: 20,001 x 1,001 bf16 51 us, its gradient 84 us.
+// 2,816: 2.6 us.  Rows read where they lie: 20,001 x 1,001 bf16 62 us, its gradient 82 us.
+// Above 8,192 columns a thread's eight eights do not fit its registers: 2,000 x 10,001 bf16 29 us (0.41 of a copy's rate; 0.6 kB
+// spilled a thread), the gradient 106 us (0.17; 2.2 kB); 2,000 x 8,192 17 us (0.58) and 29 us (0.50).
 #include <algorithm>
 #include <atomic>
 
@@ -537,8 +539,6 @@ __global__ void __launch_bounds__(max_threads(N)) rms_norm_backward_plain_kernel
             unpack8(g[i], raw, a.grad.dtype == DG_F32);
             load8(raw, a.hidden.p, a.hidden.dtype == DG_F32, r * a.hidden.ld + col.at[i], col.n[i], col.step);
             unpack8(xh[i], raw, a.hidden.dtype == DG_F32);
-            
-            
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 xh[i][j] *= rstd;
@@ -739,7 +739,8 @@ cudaError_t launch_rms_norm(const NormRows &a, cudaStream_t stream) {
     NormParams p{a, {}};
     p.src.m[0] = a.x;
     p.src.m[1] = a.residual;
-    // (hidden of another type than the residual, or without one, is rare: rows read where they lie)
+    // hidden of another type than the residual, or without one, has no kernel of its own: rows are read where they lie (8,192 x
+    // 2,816 bf16 with an fp32 hidden 148 us, of the residual's type 33 us)
     const bool plain = a.hidden.p && (!a.residual.p || a.hidden.dtype != a.residual.dtype);
     const Plan plan = make_plan(&p.src, a.R, a.d, !plain && wide_rows(a.hidden) && wide_rows(a.out));
     if (plan.ring)

@@ -104,8 +104,11 @@ void gather_out(const GatherParams &p, unsigned grid, cudaStream_t stream) {
 
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 8, kMaxBins = 1 << kDigitBits;
-constexpr int kSortMost = 65536;  // positions that are ordered in runs, which are then merged
-constexpr int kSortCtas = 8;      // of the cluster that sorts more
+// Up to kSortMost positions are ordered in runs, which are then merged; more by a cluster of kSortCtas (the largest size that
+// every device takes).  Frequencies of text, bf16 of 512 columns added to fp32: 65,536 positions 61.6 us and by the cluster 81.4,
+// 131,072 107 and 133, 262,144 234 and 237, 524,288 574 and 436; so the limit errs low by a factor of four.
+constexpr int kSortMost = 65536;
+constexpr int kSortCtas = 8;
 
 // Where everything lies in the workspace.
 struct SortSpace {
@@ -198,7 +201,8 @@ __device__ __forceinline__ int count_before(const int32_t *keys, int R, int i, i
 }
 
 // By one CTA, up to kFewRows positions.  A gradient that is added to, fp32 (V = 32,000, d = 512; with the limit at 256 and at 512):
-// 256 positions 8.4 us and 9.3, 512 11.0 and 13.7.  A cleared one finds the order under the clearing, and one kernel in place of
+// 256 positions 8.4 us and 9.3, 512 11.0 and 13.7 (1,024 threads leave 64 registers each: the kernels that add spill 90 to 180
+// bytes a thread, and 24 of the 32 warps only help to find the order).  A cleared one finds the order under the clearing, and one kernel in place of
 // three follows it, so that up to 512 one kernel is as fast or faster: 300 positions 22.1 us for 26.2, 512 25.6 for 26.8; 300 of
 // 1,001 34.1 for 39.3; of 2,816 over 262,144 bf16 rows 208 for 213; and 512 of 256 over 4,096 12.4 for 11.1 in a graph, but called
 // in 14.5 for 14.7.
@@ -869,8 +873,8 @@ cudaError_t ensure_merge_attributes() {
 cudaError_t sort_tokens(SortParams sp, bool chained, cudaStream_t stream) {
     if (sp.R > kSortMost) return launch_chained(sort_far_kernel, kSortCtas, kSortThreads, 0, stream, chained, kSortCtas, sp);
     // Runs counted side by side and merged in shared memory take half the time of radix runs merged from global memory:
-    // d = 512, 5,000 positions 15.4 us and 23.6, 16,000 25.9 and 29.3, 24,576 34.7 and 36.8; 32,768 44.8 and 44.0, as
-    // every CTA of the merge loads all keys.  Up to kOneRun they are one run: 2,048 positions 12.8 us and, merged of two,
+    // d = 512, 5,000 positions 15.4 us and 23.6, 16,000 25.9 and 29.3, 24,576 34.9 and 37.3; 32,768 45.7 and 42.8,
+    // 57,344 86.5 and 58.7, as every CTA of the merge loads all keys.  Up to kOneRun they are one run: 2,048 positions 12.8 us and, merged of two,
     // 13.6; 3,000 14.9 and 14.3.
     if (sp.R <= kNearRows) {
         const bool one = sp.R <= kOneRun;

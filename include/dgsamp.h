@@ -735,8 +735,8 @@ dg_status dg_token_embed(const void *table, int32_t dtype, const float *scale, i
  *   grad_table[v - vocab_start] (+)= gamma * (sum over {r : token[r] = v} of grad[r])
  *   grad        [R, ldg] of dtype; rows without a table row here are not read
  *   grad_table  [rows_pad, ldt] of table_dtype.  accumulate == 0: every row of the slice is written (zeros
- *               where a token does not occur).  Else the sum, in fp32, is added to what is there, and rows of
- *               tokens that do not occur are neither read nor written.
+ *               where a token does not occur).  Else the sum, in fp32, is added to what is there; rows of
+ *               tokens that do not occur are not written, and what they hold does not matter.
  *   workspace   at least dg_token_embed_backward_workspace_size bytes, 16-byte aligned, its contents on
  *               entry do not matter; calls that may overlap on the GPU need one each
  * Tokens and sizes as dg_token_embed.  R == 0 clears the slice, or queues nothing with accumulate.
@@ -758,10 +758,12 @@ size_t dg_token_embed_backward_workspace_size(int64_t R, int64_t vocab_len, int6
  *   residual  [R, ldr] of residual_dtype, or NULL (h = x)
  *   weight    [d] of weight_dtype, or NULL: y = h rstd
  *   hidden    [R, ldh] of hidden_dtype: h rounded once (y is taken of the unrounded one), or NULL.  It may
- *             replace x or residual (same pointer, type and stride).
+ *             replace x or residual (same pointer, type and stride).  Of the residual's type it costs its bytes; of another
+ *             type, or without a residual, the call takes three to four times as long.  (An fp32 h of an fp32 and a bf16
+ *             matrix: pass the fp32 one as the residual.)
  *   out       [R, ldo] of out_dtype: y.  It may replace x or residual likewise (not hidden).  DG_E4M3: out_scale [R] fp32 =
  *             max|y| / 448 and codes e4m3(y / out_scale), the quotient rounded to fp32 once, ties to even, magnitudes past 448
- *             as 448 (a row of zeros: scale 0, codes 0): what dg_head_e4m3 takes.  A row with an infinity or NaN has NaN or infinity as its scale.
+ *             as 448 (a row of zeros, eps > 0: scale 0, codes 0): what dg_head_e4m3 takes.  A row with an infinity or NaN has NaN or infinity as its scale.
  *   rstd      [R] fp32 or NULL: what the backward pass takes
  * Requires 1 <= d <= 32768 (above: DG_ERR_UNSUPPORTED), eps >= 0 and finite, weight_offset finite, R <= 2^28.
  */
