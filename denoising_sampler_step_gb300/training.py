@@ -70,8 +70,8 @@ class _RmsNorm(torch.autograd.Function):
         ctx.weight_offset, ctx.types = weight_offset, (x.dtype, None if residual is None else residual.dtype)
         ctx.set_materialize_grads(False)
         dtype = x.dtype if dtype is None else dtype
-        if residual is not None and x.dtype == torch.float32:
-            # hidden has the second matrix's type: fp32 where either is, so that the backward pass loses no bits
+        if residual is not None and x.dtype == torch.float32 != residual.dtype:
+            # hidden has the second matrix's type: fp32 here too, so that the backward pass loses no bits
             x, residual = residual, x
         o = B.dg_rms_norm(x, weight, residual=residual, eps=eps, weight_offset=weight_offset, dtype=dtype)
         hidden = o.get("hidden", x)
